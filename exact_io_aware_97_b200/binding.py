@@ -16,13 +16,21 @@ LIB_PATH = os.path.join(PKG, "libfa.so")
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_WORKSPACE, FA_ERR_CUDA, FA_ERR_TIMEOUT = range(6)
 FA_BF16, FA_F32, FA_TF32 = 0, 1, 2
+FA_ROPE_NONE, FA_ROPE_LINEAR, FA_ROPE_NTK, FA_ROPE_BANDS = range(4)
 
 EXPORTED = ("fa_fwd", "fa_fwd_workspace_size", "fa_decode", "fa_decode_workspace_size", "fa_decode_noalloc",
             "fa_decode_paged", "fa_decode_paged_workspace_size", "fa_bwd", "fa_bwd_workspace_size", "fa_bwd_varlen",
             "fa_bwd_varlen_workspace_size", "fa_fwd_qkvpacked",
             "fa_fwd_fp8", "fa_fwd_fp8_workspace_size", "fa_selftest_wait_timeout",
+            "fa_rope", "fa_rope_frequencies", "fa_cache_append_fp8", "fa_decode_paged_fp8",
+            "fa_decode_paged_fp8_workspace_size", "fa_pages_fork", "fa_pages_compact", "fa_pages_workspace_size",
             "fa_last_device_error", "fa_status_string", "fa_device_sm_count")
 FA_DECODE_NOALLOC_SCRATCH_BYTES = 16 << 20
+
+
+class FaPool(ctypes.Structure):
+    """fa_pool: one array of a paged cache."""
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t)]
 
 
 class FaError(RuntimeError):
@@ -71,6 +79,23 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     L.fa_bwd_varlen.restype = i
     L.fa_bwd_varlen_workspace_size.argtypes = [i, i, i, i]
     L.fa_bwd_varlen_workspace_size.restype = sz
+    ll, db = ctypes.c_longlong, ctypes.c_double
+    L.fa_rope.argtypes = [vp] * 6 + [ll] + [i] * 6 + [f, i, i] + [ll] * 4 + [vp]
+    L.fa_rope.restype = i
+    L.fa_rope_frequencies.argtypes = [vp, i, db, i, db, db, db, db]
+    L.fa_rope_frequencies.restype = i
+    L.fa_cache_append_fp8.argtypes = [vp] * 9 + [i] * 8 + [vp]
+    L.fa_cache_append_fp8.restype = i
+    L.fa_decode_paged_fp8.argtypes = [vp] * 9 + [i] * 9 + [f, vp, sz, vp]
+    L.fa_decode_paged_fp8.restype = i
+    L.fa_decode_paged_fp8_workspace_size.argtypes = [i] * 5
+    L.fa_decode_paged_fp8_workspace_size.restype = sz
+    L.fa_pages_fork.argtypes = [vp, i] + [vp] * 7 + [i] * 5 + [vp, sz, vp]
+    L.fa_pages_fork.restype = i
+    L.fa_pages_compact.argtypes = [vp, i] + [vp] * 4 + [i] * 4 + [vp, sz, vp]
+    L.fa_pages_compact.restype = i
+    L.fa_pages_workspace_size.argtypes = [i, i]
+    L.fa_pages_workspace_size.restype = sz
     L.fa_selftest_wait_timeout.argtypes = [vp]
     L.fa_selftest_wait_timeout.restype = i
     L.fa_last_device_error.argtypes = [vp]
@@ -251,6 +276,89 @@ def fa_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, total, d, scale
 
 def fa_bwd_varlen_workspace_size(B, Hq, total, d) -> int:
     return int(load().fa_bwd_varlen_workspace_size(int(B), int(Hq), int(total), int(d)))
+
+
+def fa_rope(q, k, q_out, k_out, positions, freqs, rows, period, Hq, Hk, d, rot_dim, interleaved, amplitude, backward,
+            dtype, q_stride, k_stride, q_out_stride, k_out_stride, stream=None) -> None:
+    """q, k and the outputs as raw addresses or dense tensors; strides in elements between rows."""
+    st = load().fa_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), _ptr_i32(positions, "positions"), _ptr(freqs),
+                        int(rows), int(period), int(Hq), int(Hk), int(d), int(rot_dim), int(bool(interleaved)),
+                        float(amplitude), int(bool(backward)), int(dtype), int(q_stride), int(k_stride),
+                        int(q_out_stride), int(k_out_stride), _stream(stream))
+    _check(st, "fa_rope")
+
+
+def fa_rope_frequencies(rot_dim, theta=10000.0, scaling=FA_ROPE_NONE, factor=1.0, original_len=0.0, low=0.0,
+                        high=0.0) -> list:
+    """rot_dim / 2 angular frequencies as floats (host)."""
+    buf = (ctypes.c_double * max(1, int(rot_dim) // 2))()
+    _check(load().fa_rope_frequencies(ctypes.cast(buf, ctypes.c_void_p), int(rot_dim), float(theta), int(scaling),
+                                      float(factor), float(original_len), float(low), float(high)),
+           "fa_rope_frequencies")
+    return list(buf)
+
+
+def fa_cache_append_fp8(k, v, cu_seqlens, block_table, seqlens, k_pages, v_pages, k_scale, v_scale, B, total, Hkv,
+                        num_pages, page_size, max_pages_per_seq, scale_block, d, stream=None) -> None:
+    st = load().fa_cache_append_fp8(_ptr(k), _ptr(v), _ptr_i32(cu_seqlens, "cu_seqlens"),
+                                    _ptr_i32(block_table, "block_table"), _ptr_i32(seqlens, "seqlens"),
+                                    _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), int(B), int(total),
+                                    int(Hkv), int(num_pages), int(page_size), int(max_pages_per_seq),
+                                    int(scale_block), int(d), _stream(stream))
+    _check(st, "fa_cache_append_fp8")
+
+
+def fa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, o, lse, B, Nq, Hq, Hkv,
+                        num_pages, page_size, max_pages_per_seq, scale_block, d, scale, workspace, workspace_bytes,
+                        stream=None) -> None:
+    st = load().fa_decode_paged_fp8(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                                    _ptr_i32(block_table, "block_table"), _ptr_i32(seqlens, "seqlens"), _ptr(o),
+                                    _ptr(lse), int(B), int(Nq), int(Hq), int(Hkv), int(num_pages), int(page_size),
+                                    int(max_pages_per_seq), int(scale_block), int(d), float(scale), _ptr(workspace),
+                                    int(workspace_bytes), _stream(stream))
+    _check(st, "fa_decode_paged_fp8")
+
+
+def fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d) -> int:
+    return int(load().fa_decode_paged_fp8_workspace_size(int(B), int(Nq), int(Hq), int(Hkv), int(d)))
+
+
+def _pool_array(pools, num_pages):
+    """fa_pool array of tensors [num_pages, ...]; raw (address, page_bytes) pairs pass through."""
+    arr = (FaPool * max(1, len(pools)))()
+    for n, t in enumerate(pools):
+        if isinstance(t, tuple):
+            arr[n].base, arr[n].page_bytes = t
+            continue
+        if t.dim() < 1 or t.shape[0] != num_pages:
+            raise ValueError(f"pool {n}: expected [{num_pages}, ...], got shape {tuple(t.shape)}")
+        arr[n].base, arr[n].page_bytes = _ptr(t), t.numel() // num_pages * t.element_size()
+    return ctypes.cast(arr, ctypes.c_void_p) if len(pools) else None, arr
+
+
+def fa_pages_fork(pools, block_table, seqlens, parent, block_table_out, seqlens_out, free_pages, n_free, B, B_out,
+                  num_pages, page_size, max_pages_per_seq, workspace, workspace_bytes, stream=None) -> None:
+    ptr, _keep = _pool_array(pools, int(num_pages))
+    st = load().fa_pages_fork(ptr, len(pools), _ptr_i32(block_table, "block_table"), _ptr_i32(seqlens, "seqlens"),
+                              _ptr_i32(parent, "parent"), _ptr_i32(block_table_out, "block_table_out"),
+                              _ptr_i32(seqlens_out, "seqlens_out"), _ptr_i32(free_pages, "free_pages"),
+                              _ptr_i32(n_free, "n_free"), int(B), int(B_out), int(num_pages), int(page_size),
+                              int(max_pages_per_seq), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    _check(st, "fa_pages_fork")
+
+
+def fa_pages_compact(pools, block_table, seqlens, block_table_out, n_live, B, num_pages, page_size,
+                     max_pages_per_seq, workspace, workspace_bytes, stream=None) -> None:
+    ptr, _keep = _pool_array(pools, int(num_pages))
+    st = load().fa_pages_compact(ptr, len(pools), _ptr_i32(block_table, "block_table"),
+                                 _ptr_i32(seqlens, "seqlens"), _ptr_i32(block_table_out, "block_table_out"),
+                                 _ptr_i32(n_live, "n_live"), int(B), int(num_pages), int(page_size),
+                                 int(max_pages_per_seq), _ptr(workspace), int(workspace_bytes), _stream(stream))
+    _check(st, "fa_pages_compact")
+
+
+def fa_pages_workspace_size(num_pages, B_out=0) -> int:
+    return int(load().fa_pages_workspace_size(int(num_pages), int(B_out)))
 
 
 def fa_selftest_wait_timeout(stream=None) -> None:
@@ -465,3 +573,222 @@ def forward_fp8(q8, k8, v8, descale_q, descale_k, descale_v, causal=False, scale
     fa_fwd_fp8(q8, k8, v8, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, descale_q, descale_k, descale_v, causal, workspace,
                ws_bytes)
     return o, lse
+
+
+# ------------------------------------------------------------------ rotary positions, 8-bit cache, pages
+class _device_of:
+    """Makes the device of the tensors current for one call (launches go to the current device)
+    and refuses tensors of different devices."""
+
+    def __init__(self, first, *others):
+        import torch
+        if not first.is_cuda:
+            raise ValueError(f"expected a CUDA tensor, got one on {first.device}")
+        for t in others:
+            if t is not None and t.device != first.device:
+                raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+        self._guard = None
+        if first.device.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(first.device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+_ROPE_SCALINGS = {"none": FA_ROPE_NONE, "linear": FA_ROPE_LINEAR, "ntk": FA_ROPE_NTK, "bands": FA_ROPE_BANDS}
+
+
+def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, original_len=0, low=1.0, high=32.0,
+                     device="cuda"):
+    """float64 [rot_dim / 2] angular frequencies on `device`, for rope(); made once and kept.
+    scaling: "none", "linear", "ntk" or "bands" (see fa_rope_scaling in include/fa.h)."""
+    import torch
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling: expected one of {sorted(_ROPE_SCALINGS)}, got {scaling!r}")
+    return torch.tensor(fa_rope_frequencies(rot_dim, theta, _ROPE_SCALINGS[scaling], factor, original_len, low, high),
+                        dtype=torch.float64, device=device)
+
+
+def _row_stride(t, what: str) -> int:
+    """Elements between rows of [..., H, d] whose heads are dense and whose rows are evenly
+    spaced (a dense tensor, or q or k inside a packed [..., 3, H, d] one)."""
+    H, d = t.shape[-2], t.shape[-1]
+    ok = t.stride(-1) == 1 and (H == 1 or t.stride(-2) == d)
+    step = H * d
+    lead = [(n, s) for n, s in zip(t.shape[:-2], t.stride()[:-2]) if n != 1]
+    if lead:
+        step = lead[-1][1]
+        for (n0, s0), (n1, s1) in zip(lead, lead[1:]):
+            ok = ok and s0 == n1 * s1
+    if not ok or step < H * d:
+        raise ValueError(f"{what}: expected dense heads and evenly spaced rows, got strides {tuple(t.stride())} for "
+                         f"shape {tuple(t.shape)}")
+    return step
+
+
+def _rope(q, k, freqs, positions, interleaved, amplitude, q_out, k_out, stream, backward):
+    import torch
+    dtypes = {torch.bfloat16: FA_BF16, torch.float32: FA_F32}
+    _require("q", q.dim() in (3, 4) and q.dtype in dtypes,
+             f"bf16 or fp32 [B, N, Hq, d] or [total, Hq, d], got {q.dtype} {tuple(q.shape)}")
+    Hq, d = q.shape[-2], q.shape[-1]
+    rows = q.numel() // max(1, Hq * d)
+    period = q.shape[-3]
+    if k is not None:
+        _require("k", k.dtype == q.dtype and k.dim() == q.dim() and k.shape[:-2] == q.shape[:-2] and k.shape[-1] == d,
+                 f"{q.dtype} {tuple(q.shape[:-2])} + (Hkv, {d}) like q, got {k.dtype} {tuple(k.shape)}")
+    elif k_out is not None:
+        raise ValueError("k_out given without k")
+    _require("freqs", freqs.dim() == 1 and freqs.dtype == torch.float64 and 0 < 2 * freqs.numel() <= d,
+             f"float64 [rot_dim / 2] with rot_dim <= {d}, got {freqs.dtype} {tuple(freqs.shape)}")
+    if positions is not None:
+        _require("positions", positions.numel() == rows and (positions.dim() == 1 or positions.shape == q.shape[:-2]),
+                 f"{tuple(q.shape[:-2])} or [{rows}], got shape {tuple(positions.shape)}")
+    _expect(q_out, q.shape, str(q.dtype), "q_out")
+    if k is not None:
+        _expect(k_out, k.shape, str(q.dtype), "k_out")
+    with _device_of(q, k, freqs, positions, q_out, k_out):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        if rows > 0:
+            pairs = [(q, "q"), (q_out, "q_out")] + ([(k, "k"), (k_out, "k_out")] if k is not None else [])
+            st = {w: _row_stride(t, w) for t, w in pairs}
+            fa_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                    None if k is None else k_out.data_ptr(), positions, freqs, rows, period, Hq,
+                    0 if k is None else k.shape[-2], d, 2 * freqs.numel(), interleaved, amplitude, backward,
+                    dtypes[q.dtype], st["q"], st.get("k", 0), st["q_out"], st.get("k_out", 0), stream)
+    return q_out, k_out
+
+
+def rope(q, k, freqs, positions=None, interleaved=False, amplitude=1.0, q_out=None, k_out=None, stream=None):
+    """q and k (or None) turned by their positions: [B, N, H, d] or packed [total, H, d], bf16 or
+    fp32; q and k may be slices of a packed qkv tensor.  freqs from rope_frequencies();
+    positions int32, one per row, or None: 0 .. N - 1 (0 .. total - 1).  q_out / k_out may be q / k
+    themselves.  Returns (q_out, k_out)."""
+    return _rope(q, k, freqs, positions, interleaved, amplitude, q_out, k_out, stream, False)
+
+
+def rope_backward(dq, dk, freqs, positions=None, interleaved=False, amplitude=1.0, q_out=None, k_out=None,
+                  stream=None):
+    """Gradients of rope()'s inputs from those of its outputs (same arguments as rope())."""
+    return _rope(dq, dk, freqs, positions, interleaved, amplitude, q_out, k_out, stream, True)
+
+
+def _cache8(k_pages, v_pages, k_scale, v_scale, block_table, seqlens):
+    """Checks an e4m3 paged cache; returns (B, num_pages, page_size, max_pages, Hkv, d, scale_block)."""
+    _same("k_pages, v_pages", k_pages, v_pages)
+    _same("k_scale, v_scale", k_scale, v_scale)
+    _require("k_pages", k_pages.dim() == 4 and str(k_pages.dtype) in ("torch.float8_e4m3fn", "torch.uint8"),
+             f"e4m3 (or bytes) [num_pages, page_size, Hkv, d], got {k_pages.dtype} {tuple(k_pages.shape)}")
+    num_pages, page_size, Hkv, d = k_pages.shape
+    _require("k_scale", k_scale.dim() == 3 and k_scale.shape[0] == num_pages and k_scale.shape[1] == Hkv and
+             str(k_scale.dtype) == "torch.float32" and k_scale.shape[2] > 0 and page_size % k_scale.shape[2] == 0,
+             f"float32 [{num_pages}, {Hkv}, page_size / scale_block], got {k_scale.dtype} {tuple(k_scale.shape)}")
+    _require("block_table", block_table.dim() == 2, f"[B, max_pages], got {tuple(block_table.shape)}")
+    B, maxp = block_table.shape
+    _lengths(seqlens, B, "seqlens")
+    return B, num_pages, page_size, maxp, Hkv, d, page_size // k_scale.shape[2]
+
+
+def cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, cu_seqlens=None, stream=None):
+    """Writes bf16 k, v [total, Hkv, d] into an e4m3 paged cache (pages [num_pages, page_size, Hkv,
+    d], scales float32 [num_pages, Hkv, page_size / scale_block]), in place.  seqlens [B]: lengths
+    with the new rows; cu_seqlens [B + 1]: the new rows of each sequence, or None: one each."""
+    _same("k, v", k, v)
+    _bf16("cache_append_fp8", k)
+    B, P, ps, maxp, Hkv, d, sb = _cache8(k_pages, v_pages, k_scale, v_scale, block_table, seqlens)
+    _require("k", k.dim() == 3 and k.shape[1] == Hkv and k.shape[2] == d,
+             f"[total, Hkv={Hkv}, d={d}], got shape {tuple(k.shape)}")
+    total = k.shape[0]
+    if cu_seqlens is None:
+        _require("k", total == B, f"one row for each of {B} sequences without cu_seqlens, got {total}")
+    else:
+        _require("cu_seqlens", cu_seqlens.dim() == 1 and cu_seqlens.numel() == B + 1,
+                 f"[B + 1 = {B + 1}] offsets, got shape {tuple(cu_seqlens.shape)}")
+    with _device_of(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, cu_seqlens):
+        fa_cache_append_fp8(k, v, cu_seqlens, block_table, seqlens, k_pages, v_pages, k_scale, v_scale, B, total, Hkv,
+                            P, ps, maxp, sb, d, stream)
+
+
+def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, scale=None, out=None, lse=None,
+                     workspace=None, stream=None):
+    """O, lse for the newest tokens of each sequence over an e4m3 paged cache (see
+    cache_append_fp8): q [B, Hq, d] gives lse [B, Hq]; q [B, Nq, Hq, d] (the Nq newest tokens,
+    causal among themselves) gives lse [B, Hq, Nq]."""
+    import torch
+    _bf16("decode_paged_fp8", q)
+    B, P, ps, maxp, Hkv, d, sb = _cache8(k_pages, v_pages, k_scale, v_scale, block_table, seqlens)
+    _require("q", q.dim() in (3, 4) and q.shape[0] == B and q.shape[-1] == d,
+             f"[B={B}, Hq, d={d}] or [B={B}, Nq, Hq, d={d}], got shape {tuple(q.shape)}")
+    Nq, Hq = (q.shape[1] if q.dim() == 4 else 1), q.shape[-2]
+    _require("heads", Hkv > 0 and Hq % Hkv == 0, f"Hq ({Hq}) a multiple of Hkv ({Hkv})")
+    lse_shape = (B, Hq) if q.dim() == 3 else (B, Hq, Nq)
+    if scale is None:
+        scale = d ** -0.5
+    _expect(out, q.shape, "torch.bfloat16", "out")
+    _expect(lse, lse_shape, "torch.float32", "lse")
+    with _device_of(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace):
+        if out is None:
+            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(max(fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d), 1), dtype=torch.uint8,
+                                    device=q.device)
+        fa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, B, Nq, Hq, Hkv, P,
+                            ps, maxp, sb, d, scale, workspace, workspace.numel() * workspace.element_size(), stream)
+    return out, lse
+
+
+def _paged_table(block_table, seqlens):
+    _require("block_table", block_table.dim() == 2, f"[B, max_pages], got {tuple(block_table.shape)}")
+    _lengths(seqlens, block_table.shape[0], "seqlens")
+    return block_table.shape
+
+
+def pages_fork(pools, block_table, seqlens, parent, page_size, num_pages=None, workspace=None, stream=None):
+    """Sequence i of the result continues sequence parent[i] (int32; -1: empty).  Full pages are
+    shared, a partly filled last page is copied for all but one of its heirs in every pool (a list
+    of tensors [num_pages, ...]).  Returns (block_table, seqlens, free_pages [num_pages], n_free
+    [1]); see fa_pages_fork in include/fa.h."""
+    import torch
+    B, maxp = _paged_table(block_table, seqlens)
+    _require("parent", parent.dim() == 1, f"[B_out], got shape {tuple(parent.shape)}")
+    if num_pages is None:
+        _require("pools", len(pools) > 0, "at least one pool, or num_pages")
+        num_pages = pools[0].shape[0]
+    R = parent.numel()
+    with _device_of(block_table, seqlens, parent, workspace, *pools):
+        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=block_table.device)  # noqa: E731
+        table, lens, free, n_free = new(R, maxp), new(R), new(num_pages), new(1)
+        if workspace is None:
+            workspace = torch.empty(fa_pages_workspace_size(num_pages, R), dtype=torch.uint8,
+                                    device=block_table.device)
+        fa_pages_fork(pools, block_table, seqlens, parent, table, lens, free, n_free, B, R, num_pages, page_size, maxp,
+                      workspace, workspace.numel() * workspace.element_size(), stream)
+    return table, lens, free, n_free
+
+
+def pages_compact(pools, block_table, seqlens, page_size, num_pages=None, workspace=None, stream=None):
+    """Moves the pages in use to the front of every pool.  Returns (block_table, n_live [1])."""
+    import torch
+    B, maxp = _paged_table(block_table, seqlens)
+    if num_pages is None:
+        _require("pools", len(pools) > 0, "at least one pool, or num_pages")
+        num_pages = pools[0].shape[0]
+    with _device_of(block_table, seqlens, workspace, *pools):
+        table = torch.empty((B, maxp), dtype=torch.int32, device=block_table.device)
+        n_live = torch.empty(1, dtype=torch.int32, device=block_table.device)
+        if workspace is None:
+            workspace = torch.empty(fa_pages_workspace_size(num_pages, 0), dtype=torch.uint8,
+                                    device=block_table.device)
+        fa_pages_compact(pools, block_table, seqlens, table, n_live, B, num_pages, page_size, maxp, workspace,
+                         workspace.numel() * workspace.element_size(), stream)
+    return table, n_live

@@ -9,8 +9,12 @@
 
 #include "../../include/fa.h"
 #include "fa_bwd_sm100.cuh"
+#include "fa_cache.cuh"
+#include "fa_decode_fp8.cuh"
 #include "fa_decode_sm100.cuh"
 #include "fa_fwd_sm100.cuh"
+#include "fa_pages.cuh"
+#include "fa_rope.cuh"
 
 namespace fa {
 
@@ -910,4 +914,345 @@ extern "C" fa_status fa_decode_noalloc(const void* q, const void* kcache, const 
   if (st != FA_OK) return st;
   return fa_decode(q, kcache, vcache, seqlens, o, lse, B, Hq, Hkv, Lmax, d, scale, split_len, scratch,
                    (size_t)FA_DECODE_NOALLOC_SCRATCH_BYTES, stream);
+}
+
+// ---------------------------------------------------------------------------------------
+// Rotary positions.
+namespace fa {
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+template <typename T, int D>
+fa_status launch_rope(const RopeParams& prm, cudaStream_t st) {
+  const long long units = prm.rows * prm.chunks;
+  fa_rope_kernel<T, D><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" fa_status fa_rope_frequencies(double* freqs, int rot_dim, double theta, fa_rope_scaling scaling,
+                                         double factor, double original_len, double low, double high) {
+  if (!freqs || rot_dim <= 0 || rot_dim % 2 != 0) return FA_ERR_INVALID_ARG;
+  if (!(theta > 0.0) || !std::isfinite(theta)) return FA_ERR_INVALID_ARG;
+  if (scaling != FA_ROPE_NONE && scaling != FA_ROPE_LINEAR && scaling != FA_ROPE_NTK && scaling != FA_ROPE_BANDS)
+    return FA_ERR_INVALID_ARG;
+  if (scaling != FA_ROPE_NONE && (!(factor > 0.0) || !std::isfinite(factor))) return FA_ERR_INVALID_ARG;
+  if (scaling == FA_ROPE_BANDS && (!(original_len > 0.0) || !std::isfinite(original_len) || !(low < high) ||
+                                   !std::isfinite(low) || !std::isfinite(high)))
+    return FA_ERR_INVALID_ARG;
+  const double two_pi = 6.28318530717958647693;
+  if (scaling == FA_ROPE_NTK && rot_dim > 2) theta *= std::pow(factor, (double)rot_dim / (rot_dim - 2));
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double w = std::pow(theta, -2.0 * i / rot_dim);
+    if (scaling == FA_ROPE_LINEAR) w /= factor;
+    if (scaling == FA_ROPE_BANDS) {
+      const double turns = original_len * w / two_pi;
+      const double keep = std::min(1.0, std::max(0.0, (turns - low) / (high - low)));
+      w *= keep + (1.0 - keep) / factor;
+    }
+    freqs[i] = w;
+  }
+  return FA_OK;
+}
+
+extern "C" fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+                             const double* freqs, long long rows, int period, int Hq, int Hk, int d, int rot_dim,
+                             int interleaved, float amplitude, int backward, fa_dtype dtype, long long q_stride,
+                             long long k_stride, long long q_out_stride, long long k_out_stride, void* stream) {
+  if (rows < 0 || Hq <= 0 || Hk < 0 || !q || !q_out || !freqs) return FA_ERR_INVALID_ARG;
+  if (Hk > 0 && (!k || !k_out)) return FA_ERR_INVALID_ARG;
+  if (dtype != FA_BF16 && dtype != FA_F32) return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(amplitude)) return FA_ERR_INVALID_ARG;
+  if (!positions && period <= 0) return FA_ERR_INVALID_ARG;
+  if (!aligned4(positions) || (reinterpret_cast<uintptr_t>(freqs) & 7u) != 0) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (rot_dim <= 0 || rot_dim > d || rot_dim % 2 != 0) return FA_ERR_INVALID_ARG;
+  const int es = dtype == FA_BF16 ? 2 : 4;
+  const void* ptrs[4] = {q, q_out, Hk > 0 ? k : q, Hk > 0 ? k_out : q_out};
+  const long long strides[4] = {q_stride, q_out_stride, Hk > 0 ? k_stride : q_stride,
+                                Hk > 0 ? k_out_stride : q_out_stride};
+  for (int i = 0; i < 4; ++i) {
+    const int h = i < 2 ? Hq : std::max(Hk, 1);
+    if (!aligned16(ptrs[i]) || strides[i] < (long long)h * d || strides[i] * es % 16 != 0) return FA_ERR_INVALID_ARG;
+  }
+  // written in place only over the very rows that were read
+  if ((q == q_out && q_stride != q_out_stride) || (Hk > 0 && k == k_out && k_stride != k_out_stride))
+    return FA_ERR_INVALID_ARG;
+  if (rows >= (1ll << 31) || (long long)Hq + Hk > 65535) return FA_ERR_UNSUPPORTED;
+  if (rows == 0) return FA_OK;
+  RopeParams prm{};
+  prm.x[0] = q;
+  prm.x[1] = k;
+  prm.y[0] = q_out;
+  prm.y[1] = k_out;
+  prm.xs[0] = q_stride;
+  prm.xs[1] = k_stride;
+  prm.ys[0] = q_out_stride;
+  prm.ys[1] = k_out_stride;
+  prm.heads[0] = Hq;
+  prm.heads[1] = Hk;
+  prm.positions = positions;
+  prm.freqs = freqs;
+  prm.rows = rows;
+  prm.period = period;
+  prm.rot = rot_dim;
+  prm.interleaved = interleaved ? 1 : 0;
+  prm.backward = backward ? 1 : 0;
+  prm.amplitude = amplitude;
+  prm.chunks = 1;
+  prm.per_chunk = Hq + Hk;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == FA_BF16)
+    return d == 64 ? launch_rope<__nv_bfloat16, 64>(prm, st) : launch_rope<__nv_bfloat16, 128>(prm, st);
+  return d == 64 ? launch_rope<float, 64>(prm, st) : launch_rope<float, 128>(prm, st);
+}
+
+// ---------------------------------------------------------------------------------------
+// The paged cache in e4m3.
+namespace fa {
+namespace {
+
+// What the append and the decode over the e4m3 cache check alike.
+fa_status check_cache8(const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
+                       const int32_t* block_table, const int32_t* seqlens, int B, int Hkv, int num_pages,
+                       int page_size, int max_pages, int scale_block, int d) {
+  if (!k_pages || !v_pages || !k_scale || !v_scale || !block_table || !seqlens) return FA_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(v_pages) || !aligned4(k_scale) || !aligned4(v_scale) ||
+      !aligned4(block_table) || !aligned4(seqlens))
+    return FA_ERR_INVALID_ARG;
+  if (B < 0 || Hkv <= 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0 || scale_block <= 0)
+    return FA_ERR_INVALID_ARG;
+  if ((page_size & (page_size - 1)) != 0 || page_size < 16) return FA_ERR_UNSUPPORTED;
+  if ((scale_block & (scale_block - 1)) != 0 || scale_block < 16 || scale_block > 256 || scale_block > page_size)
+    return FA_ERR_UNSUPPORTED;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if ((int64_t)num_pages * page_size >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  if ((int64_t)max_pages * page_size >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  if (B > 65535 || Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+template <int D>
+fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
+  const int wpu = (1 << prm.sb_shift) / 16;
+  const int warps = std::max(8, wpu), upc = warps / wpu;
+  const dim3 grid((unsigned)(prm.cu ? (prm.total >> prm.sb_shift) + 2ll * prm.B : prm.B),
+                  (unsigned)((prm.Hkv + upc - 1) / upc), 2);
+  fa_cache_append_kernel<D><<<grid, warps * 32, 0, st>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D>
+fa_status launch_decode_fp8(const Dec8Params& prm, cudaStream_t st) {
+  const dim3 grid(prm.Hq, prm.Nq, prm.B);
+  fa_decode_fp8_kernel<D><<<grid, 128, 0, st>>>(prm);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" fa_status fa_cache_append_fp8(const void* k, const void* v, const int32_t* cu_seqlens,
+                                         const int32_t* block_table, const int32_t* seqlens, void* k_pages,
+                                         void* v_pages, float* k_scale, float* v_scale, int B, int total, int Hkv,
+                                         int num_pages, int page_size, int max_pages_per_seq, int scale_block, int d,
+                                         void* stream) {
+  const fa_status ok = check_cache8(k_pages, v_pages, k_scale, v_scale, block_table, seqlens, B, Hkv, num_pages,
+                                    page_size, max_pages_per_seq, scale_block, d);
+  if (ok != FA_OK) return ok;
+  if (total < 0 || (!cu_seqlens && total != B) || !aligned4(cu_seqlens)) return FA_ERR_INVALID_ARG;
+  if (B == 0 || total == 0) return FA_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return FA_ERR_INVALID_ARG;
+  AppendParams prm{};
+  prm.src[0] = static_cast<const __nv_bfloat16*>(k);
+  prm.src[1] = static_cast<const __nv_bfloat16*>(v);
+  prm.pages[0] = static_cast<uint8_t*>(k_pages);
+  prm.pages[1] = static_cast<uint8_t*>(v_pages);
+  prm.scales[0] = k_scale;
+  prm.scales[1] = v_scale;
+  prm.cu = cu_seqlens;
+  prm.block_table = block_table;
+  prm.seqlens = seqlens;
+  prm.B = B;
+  prm.total = total;
+  prm.Hkv = Hkv;
+  prm.num_pages = num_pages;
+  prm.page_shift = __builtin_ctz((unsigned)page_size);
+  prm.max_pages = max_pages_per_seq;
+  prm.sb_shift = __builtin_ctz((unsigned)scale_block);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return d == 64 ? launch_append<64>(prm, st) : launch_append<128>(prm, st);
+}
+
+extern "C" size_t fa_decode_paged_fp8_workspace_size(int B, int Nq, int Hq, int Hkv, int d) {
+  if (B <= 0 || Nq <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return 0;
+  return 16;
+}
+
+extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
+                                         const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                         const int32_t* seqlens, void* o, float* lse, int B, int Nq, int Hq, int Hkv,
+                                         int num_pages, int page_size, int max_pages_per_seq, int scale_block, int d,
+                                         float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  const fa_status ok = check_cache8(k_pages, v_pages, k_scale, v_scale, block_table, seqlens, B, Hkv, num_pages,
+                                    page_size, max_pages_per_seq, scale_block, d);
+  if (ok != FA_OK) return ok;
+  if (Nq < 0 || Hq <= 0) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (Hq % Hkv != 0) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || Nq == 0) return FA_OK;
+  if (!q || !o || !aligned16(q) || !aligned16(o) || !aligned4(lse)) return FA_ERR_INVALID_ARG;
+  if (Nq > 65535 || Hq > 65535) return FA_ERR_UNSUPPORTED;
+  const size_t need = fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d);
+  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return FA_ERR_WORKSPACE;
+  Dec8Params prm{};
+  prm.q = static_cast<const __nv_bfloat16*>(q);
+  prm.pages[0] = static_cast<const uint8_t*>(k_pages);
+  prm.pages[1] = static_cast<const uint8_t*>(v_pages);
+  prm.scales[0] = k_scale;
+  prm.scales[1] = v_scale;
+  prm.block_table = block_table;
+  prm.seqlens = seqlens;
+  prm.o = static_cast<__nv_bfloat16*>(o);
+  prm.lse = lse;
+  prm.B = B;
+  prm.Nq = Nq;
+  prm.Hq = Hq;
+  prm.Hkv = Hkv;
+  prm.G = Hq / Hkv;
+  prm.num_pages = num_pages;
+  prm.page_shift = __builtin_ctz((unsigned)page_size);
+  prm.sb_shift = __builtin_ctz((unsigned)scale_block);
+  prm.max_pages = max_pages_per_seq;
+  prm.tau = (float)((double)scale * 1.4426950408889634074);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return d == 64 ? launch_decode_fp8<64>(prm, st) : launch_decode_fp8<128>(prm, st);
+}
+
+// ---------------------------------------------------------------------------------------
+// Pages of a cache.
+namespace fa {
+namespace {
+
+fa_status check_pages(const fa_pool* pools, int n_pools, const int32_t* block_table, const int32_t* seqlens, int B,
+                      int num_pages, int page_size, int max_pages) {
+  if (n_pools < 0 || (n_pools > 0 && !pools)) return FA_ERR_INVALID_ARG;
+  if (B < 0 || num_pages <= 0 || page_size <= 0 || max_pages <= 0) return FA_ERR_INVALID_ARG;
+  if (B > 0 && (!block_table || !seqlens || !aligned4(block_table) || !aligned4(seqlens))) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < n_pools; ++i)
+    if (!pools[i].base || pools[i].page_bytes == 0) return FA_ERR_INVALID_ARG;
+  if ((page_size & (page_size - 1)) != 0) return FA_ERR_UNSUPPORTED;
+  if (num_pages >= kFreeMark || (int64_t)max_pages * page_size >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+fa_status launch_copies(const fa_pool* pools, int n_pools, const int32_t* src, const int32_t* dst,
+                        const int32_t* count, cudaStream_t st) {
+  const int sms = sm_count_cached();
+  if (sms <= 0) return FA_ERR_CUDA;
+  for (int at = 0; at < n_pools; at += kMaxPools) {
+    PoolList list{};
+    list.n = std::min(kMaxPools, n_pools - at);
+    for (int i = 0; i < list.n; ++i) {
+      list.base[i] = static_cast<uint8_t*>(pools[at + i].base);
+      list.bytes[i] = pools[at + i].page_bytes;
+    }
+    pages_copy_kernel<<<sms * 8, 256, 0, st>>>(list, src, dst, count);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+extern "C" size_t fa_pages_workspace_size(int num_pages, int B_out) {
+  if (num_pages <= 0 || B_out < 0) return 0;
+  return align_up((size_t)num_pages * 4, 256) + align_up(16, 256) +
+         4 * align_up((size_t)std::max(num_pages / 2 + 1, B_out) * 4, 256);
+}
+
+extern "C" fa_status fa_pages_fork(const fa_pool* pools, int n_pools, const int32_t* block_table,
+                                   const int32_t* seqlens, const int32_t* parent, int32_t* block_table_out,
+                                   int32_t* seqlens_out, int32_t* free_pages, int32_t* n_free, int B, int B_out,
+                                   int num_pages, int page_size, int max_pages_per_seq, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  const fa_status ok = check_pages(pools, n_pools, block_table, seqlens, B, num_pages, page_size, max_pages_per_seq);
+  if (ok != FA_OK) return ok;
+  if (B_out < 0 || !free_pages || !n_free || !aligned4(free_pages) || !aligned4(n_free)) return FA_ERR_INVALID_ARG;
+  if (B_out > 0 && (!parent || !block_table_out || !seqlens_out || !aligned4(parent) || !aligned4(block_table_out) ||
+                    !aligned4(seqlens_out)))
+    return FA_ERR_INVALID_ARG;
+  if (B_out > 0 && (block_table_out == block_table || seqlens_out == seqlens)) return FA_ERR_INVALID_ARG;
+  const size_t need = fa_pages_workspace_size(num_pages, B_out);
+  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return FA_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t list = align_up((size_t)std::max(num_pages / 2 + 1, B_out) * 4, 256);
+  ForkParams prm{};
+  prm.table = block_table;
+  prm.lens = seqlens;
+  prm.parent = parent;
+  prm.table_out = block_table_out;
+  prm.lens_out = seqlens_out;
+  prm.free_pages = free_pages;
+  prm.n_free = n_free;
+  prm.mark = reinterpret_cast<int32_t*>(ws);
+  ws += align_up((size_t)num_pages * 4, 256);
+  prm.count = reinterpret_cast<int32_t*>(ws);
+  ws += 256;
+  prm.rank = reinterpret_cast<int32_t*>(ws);
+  prm.src = reinterpret_cast<int32_t*>(ws + list);
+  prm.dst = reinterpret_cast<int32_t*>(ws + 2 * list);
+  prm.B = B;
+  prm.R = B_out;
+  prm.max_pages = max_pages_per_seq;
+  prm.page_shift = __builtin_ctz((unsigned)page_size);
+  prm.num_pages = num_pages;
+  if (cudaMemsetAsync(prm.mark, 0x7F, (size_t)num_pages * 4, st) != cudaSuccess) return FA_ERR_CUDA;
+  if (B_out > 0) fork_mark_kernel<<<B_out, 256, 0, st>>>(prm);
+  fork_plan_kernel<<<1, 1024, 0, st>>>(prm);
+  if (B_out > 0) fork_write_kernel<<<B_out, 256, 0, st>>>(prm);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return launch_copies(pools, n_pools, prm.src, prm.dst, prm.count, st);
+}
+
+extern "C" fa_status fa_pages_compact(const fa_pool* pools, int n_pools, const int32_t* block_table,
+                                      const int32_t* seqlens, int32_t* block_table_out, int32_t* n_live, int B,
+                                      int num_pages, int page_size, int max_pages_per_seq, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  const fa_status ok = check_pages(pools, n_pools, block_table, seqlens, B, num_pages, page_size, max_pages_per_seq);
+  if (ok != FA_OK) return ok;
+  if (!n_live || !aligned4(n_live)) return FA_ERR_INVALID_ARG;
+  if (B > 0 && (!block_table_out || !aligned4(block_table_out) || block_table_out == block_table))
+    return FA_ERR_INVALID_ARG;
+  const size_t need = fa_pages_workspace_size(num_pages, 0);
+  if (!workspace || workspace_bytes < need || !aligned16(workspace)) return FA_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const size_t list = align_up((size_t)(num_pages / 2 + 1) * 4, 256);
+  CompactParams prm{};
+  prm.table = block_table;
+  prm.lens = seqlens;
+  prm.table_out = block_table_out;
+  prm.n_live = n_live;
+  prm.mark = reinterpret_cast<int32_t*>(ws);
+  ws += align_up((size_t)num_pages * 4, 256);
+  prm.count = reinterpret_cast<int32_t*>(ws);
+  ws += 256;
+  prm.src = reinterpret_cast<int32_t*>(ws);
+  prm.dst = reinterpret_cast<int32_t*>(ws + list);
+  prm.B = B;
+  prm.max_pages = max_pages_per_seq;
+  prm.page_shift = __builtin_ctz((unsigned)page_size);
+  prm.num_pages = num_pages;
+  if (cudaMemsetAsync(prm.mark, 0x7F, (size_t)num_pages * 4, st) != cudaSuccess) return FA_ERR_CUDA;
+  if (B > 0) compact_mark_kernel<<<B, 256, 0, st>>>(prm);
+  compact_plan_kernel<<<1, 1024, 0, st>>>(prm);
+  if (B > 0) compact_write_kernel<<<B, 256, 0, st>>>(prm);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return launch_copies(pools, n_pools, prm.src, prm.dst, prm.count, st);
 }

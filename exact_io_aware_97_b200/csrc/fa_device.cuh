@@ -19,6 +19,7 @@ constexpr unsigned int kErrTimeout = 1u;       // a bounded wait ran out
 constexpr unsigned int kErrBadPage = 2u;       // a block-table entry outside [0, num_pages)
 constexpr unsigned int kErrSmem = 4u;          // a kernel's shared-memory carve did not fit
 constexpr unsigned int kErrBadSeqlens = 8u;    // cu_seqlens not non-decreasing within [0, total]
+constexpr unsigned int kErrNoPages = 16u;      // too few free pages for the copies of a fork
 // A wait gives up after this many nanoseconds of %globaltimer (a correct kernel waits
 // microseconds at most); it then records kErrTimeout and reports failure to its caller.
 constexpr unsigned long long kWaitLimitNs = 4000000000ull;

@@ -18,6 +18,11 @@
  *              fa_bwd_varlen the same over packed variable-length sequences.
  *   fa_fwd_qkvpacked  fa_fwd reading q, k, v from one packed [.., 3, H, d] tensor.
  *   fa_fwd_fp8 the forward on e4m3 inputs with per-tensor scales.
+ *   fa_rope    rotary positions of q and k, and their gradients, around fa_fwd and fa_bwd.
+ *   fa_cache_append_fp8, fa_decode_paged_fp8  a paged cache held in e4m3 with a scale for each
+ *              block of tokens and head: writing new K/V rows, and attention over it.
+ *   fa_pages_fork, fa_pages_compact  sharing, copying, freeing and moving the pages of a paged
+ *              cache of any element type.
  *
  * Conventions for every entry point:
  *   - All tensor pointers are DEVICE pointers owned by the caller.  The library never
@@ -242,12 +247,144 @@ FA_EXPORT fa_status fa_decode_paged(const void* q, const void* k_pages, const vo
 FA_EXPORT size_t fa_decode_paged_workspace_size(int B, int Hq, int Hkv, int max_pages_per_seq, int page_size, int d,
                                                 int split_len);
 
+/* Rotary positions.  The first rot_dim columns of every head of q and k turn in pairs: pair i
+ * < rot_dim / 2 of a row at position p turns by the angle p * freqs[i],
+ *   y_a = amplitude (x_a cos - x_b sin),  y_b = amplitude (x_b cos + x_a sin),
+ * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) if `interleaved`; the other columns are
+ * copied.  backward != 0 gives the gradient: x is the gradient of y, y that of x (the same
+ * formula with -sin).  Angles are reduced in fp64, so far positions lose nothing; the products
+ * are fp32 and rounded once to the element type.
+ *
+ * q [rows, Hq, d], k [rows, Hk, d] (Hk may be 0: q alone), each row's heads dense and rows
+ * q_stride / k_stride elements apart (Hq * d when dense; 3 H d for q and k inside a packed
+ * [rows, 3, H, d] tensor); q_out, k_out likewise.  An output may be its input (same pointer and
+ * stride); it must not overlap either input in another way.  Element type FA_BF16 or FA_F32.
+ * positions: device int32 [rows], any values (negative ones turn backwards), or NULL: row r has
+ * position r % period (period = the length of each sequence of a fixed-length batch).
+ * freqs: device fp64 [rot_dim / 2], radians per position (fa_rope_frequencies gives the usual
+ * ones).  d 64 or 128; rot_dim even, 2 .. d.  Pointers 16-byte aligned (positions 4, freqs 8),
+ * strides multiples of 16 bytes.  No workspace. */
+FA_EXPORT fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+                            const double* freqs, long long rows, int period, int Hq, int Hk, int d, int rot_dim,
+                            int interleaved, float amplitude, int backward, fa_dtype dtype, long long q_stride,
+                            long long k_stride, long long q_out_stride, long long k_out_stride, void* stream);
+
+/* How fa_rope_frequencies stretches positions for contexts longer than the trained one. */
+typedef enum {
+  FA_ROPE_NONE = 0,   /* w_i = theta^(-2 i / rot_dim) */
+  FA_ROPE_LINEAR = 1, /* w_i / factor */
+  FA_ROPE_NTK = 2,    /* theta * factor^(rot_dim / (rot_dim - 2)) in place of theta (rot_dim > 2) */
+  FA_ROPE_BANDS = 3   /* by the turns over original_len positions, r_i = original_len w_i / 2 pi: above `high`
+                         kept, below `low` divided by factor, linear in r_i in between */
+} fa_rope_scaling;
+
+/* Writes rot_dim / 2 frequencies to HOST memory (fp64), to be copied to the device once. */
+FA_EXPORT fa_status fa_rope_frequencies(double* freqs, int rot_dim, double theta, fa_rope_scaling scaling,
+                                        double factor, double original_len, double low, double high);
+
+/* Appends K and V rows to a paged cache held in e4m3 with a scale for each block.
+ *
+ * k, v [total, Hkv, d] bf16: the new rows of all sequences, sequence b owning rows
+ * [cu_seqlens[b], cu_seqlens[b+1]) (device int32 [B + 1], starting at or above 0, never
+ * decreasing, ending at or below total), or one row each (cu_seqlens NULL, total == B).
+ * k_pages, v_pages [num_pages, page_size, Hkv, d] e4m3 bytes; k_scale, v_scale fp32
+ * [num_pages, Hkv, page_size / scale_block]: the value of an element is (its e4m3 value) * (the
+ * scale of its block of scale_block rows and head).  block_table int32 [B, max_pages_per_seq] as
+ * in fa_decode_paged; seqlens: device int32 [B], lengths INCLUDING the new rows (the same array
+ * then goes to fa_decode_paged_fp8): n new rows of sequence b become its tokens seqlens[b] - n ..
+ * seqlens[b] - 1.
+ * A block that receives rows gets the scale max(s, s'), with s' the least power of two (at least
+ * 2^-126) for which no new |x| exceeds 448 s' (0 if all are 0) and s its scale so far if it
+ * already holds rows of the sequence, else 0; new elements are stored as x / scale, rounded to
+ * nearest even; if the scale grew, the rows held already are multiplied by old / new and rounded
+ * again.  A new row that is not finite makes the scale of its blocks NaN.  Rows past a
+ * sequence's end, and scales of blocks that receive nothing, are left as they were.
+ * Pages that receive rows must belong to one sequence each (fa_pages_fork sees to that).
+ * A sequence whose offsets or length cannot be used (see above; n > seqlens[b]; seqlens[b] >
+ * max_pages_per_seq * page_size) and a page outside [0, num_pages) are skipped and recorded:
+ * fa_last_device_error then returns FA_ERR_INVALID_ARG.
+ * page_size a power of two >= 16; scale_block a power of two, 16 .. min(256, page_size); d 64 or
+ * 128; k, v and the pages 16-byte aligned, the rest 4; num_pages * page_size < 2^31.  No
+ * workspace. */
+FA_EXPORT fa_status fa_cache_append_fp8(const void* k, const void* v, const int32_t* cu_seqlens,
+                                        const int32_t* block_table, const int32_t* seqlens, void* k_pages,
+                                        void* v_pages, float* k_scale, float* v_scale, int B, int total, int Hkv,
+                                        int num_pages, int page_size, int max_pages_per_seq, int scale_block, int d,
+                                        void* stream);
+
+/* Decode over a paged cache in e4m3 (as fa_cache_append_fp8 writes it), for one or more new
+ * query tokens per sequence.
+ *
+ * q [B, Nq, Hq, d] bf16: the Nq newest tokens of each sequence, whose K and V rows are in the
+ * cache already; o likewise; lse [B, Hq, Nq] fp32 (may be NULL).  Query i of sequence b sees
+ * cache rows j <= seqlens[b] - Nq + i (every row for Nq = 1); a query that sees no row gets o = 0
+ * and lse = -inf.  Cache, scales, block_table and seqlens as in fa_cache_append_fp8 (any fp32
+ * scales); lengths below 0 count as 0, larger ones than max_pages_per_seq * page_size as that.
+ * Rows past a sequence's end may hold anything.  An entry of the table outside [0, num_pages) is
+ * read as page 0 and recorded (FA_ERR_INVALID_ARG from fa_last_device_error).
+ * The stored values are exact in the products; P times the V scale is rounded to fp16 with its
+ * own running maximum, sums are fp32, o is rounded to bf16.
+ * Hq a multiple of Hkv; d 64 or 128; sizes as in fa_cache_append_fp8.  workspace: at least
+ * fa_decode_paged_fp8_workspace_size(...) bytes, 16-byte aligned, not initialised; calls that
+ * share one must not overlap on the GPU. */
+FA_EXPORT fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
+                                        const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                        const int32_t* seqlens, void* o, float* lse, int B, int Nq, int Hq, int Hkv,
+                                        int num_pages, int page_size, int max_pages_per_seq, int scale_block, int d,
+                                        float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+FA_EXPORT size_t fa_decode_paged_fp8_workspace_size(int B, int Nq, int Hq, int Hkv, int d);
+
+/* One array of a paged cache (K or V pages or their scales, of one layer): num_pages pages of
+ * page_bytes bytes each, in device memory. */
+typedef struct {
+  void* base;
+  size_t page_bytes;
+} fa_pool;
+
+/* Forks, drops and reorders the sequences of a paged cache.
+ *
+ * New sequence i (of B_out) continues sequence parent[i] (device int32 [B_out], entries in
+ * [0, B), or -1 for an empty sequence): seqlens_out[i] = seqlens[parent[i]], and its row of
+ * block_table_out names the same pages, except that a last page that is not full is kept by the
+ * first new sequence that ends in it only, and copied to a free page for every other one (for
+ * all of them if some new sequence holds that page full).  Sequences without a successor are
+ * dropped.  A page is in use if it is among the first ceil(len / page_size) entries of a new
+ * sequence; free_pages [num_pages] receives the other pages in ascending order, without those
+ * that the copies took (the lowest ones, in the order of the new sequences), then -1;
+ * n_free [1] their number.  Entries of a row past the sequence's pages become -1.
+ * Pages are copied in every pool of `pools` (a HOST array of n_pools; any element types; 0 pools:
+ * tables only).  block_table [B, max_pages_per_seq], block_table_out [B_out, max_pages_per_seq],
+ * all device int32; outputs must not overlap inputs.  page_size is a power of two.
+ * Recorded for fa_last_device_error (FA_ERR_INVALID_ARG): a parent outside [-1, B) (taken as
+ * -1), a length that is negative or past the table (taken as 0), an entry outside [0, num_pages)
+ * (passed on, never copied), and too few free pages (those new sequences become empty).
+ * workspace: at least fa_pages_workspace_size(num_pages, B_out) bytes, 16-byte aligned, not
+ * initialised; calls that share one must not overlap on the GPU. */
+FA_EXPORT fa_status fa_pages_fork(const fa_pool* pools, int n_pools, const int32_t* block_table,
+                                  const int32_t* seqlens, const int32_t* parent, int32_t* block_table_out,
+                                  int32_t* seqlens_out, int32_t* free_pages, int32_t* n_free, int B, int B_out,
+                                  int num_pages, int page_size, int max_pages_per_seq, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Moves the pages in use to the front of the pool: of n_live pages in use (n_live [1], device),
+ * the k-th at or past index n_live is copied to the k-th free page before it, in every pool, and
+ * block_table_out names the new places (-1 past each sequence's pages).  Pages from n_live on are
+ * free afterwards.  Arguments, checks and workspace (fa_pages_workspace_size(num_pages, 0)) as in
+ * fa_pages_fork. */
+FA_EXPORT fa_status fa_pages_compact(const fa_pool* pools, int n_pools, const int32_t* block_table,
+                                     const int32_t* seqlens, int32_t* block_table_out, int32_t* n_live, int B,
+                                     int num_pages, int page_size, int max_pages_per_seq, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+FA_EXPORT size_t fa_pages_workspace_size(int num_pages, int B_out);
+
 /* Takes the device-side error record (read and cleared in one atomic exchange, on `stream`),
  * waits for `stream`, and returns FA_ERR_TIMEOUT if any kernel of this library recorded a
  * device-side timeout since the previous call, else FA_ERR_CUDA if a kernel found its shared
  * memory carve-out too small, else FA_ERR_INVALID_ARG if a kernel recorded an invalid
  * device-side input (a block-table entry out of range, a cu_seqlens that fa_fwd or
- * fa_bwd_varlen cannot use); FA_ERR_CUDA if the stream reports an error; else FA_OK.
+ * fa_bwd_varlen cannot use, what fa_cache_append_fp8 and the fa_pages calls name); FA_ERR_CUDA if the stream reports an error; else FA_OK.
  * The record is shared by all kernels of the library on the device (all streams); a timeout
  * stops only the kernel whose wait ran out, and later launches run normally whether or not
  * the record has been taken. */

@@ -1,0 +1,379 @@
+"""The e4m3 paged cache on the GPU: fa_cache_append_fp8 bit for bit against the 64-bit model of
+cache8.py (scales are powers of two, so nothing else is rounded than the codes, to nearest even),
+and fa_decode_paged_fp8 against attention in 64 bits over the stored values.
+
+Tolerance of o: half a bf16 step of the value (2^-8); of the weights p * scale 2^-11 relative (fp16)
+or 2^-25 of the largest one below fp16's normal range, so 2^-11 sum p|v| + 2^-25 sum|v|; and 2^-17
+(1 + t) relative for the fp32 scores (d = 128 products of size t in all, 2^-24 each, and the fp32
+exponentials).  lse: 2^-17 (1 + t)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache8
+from exact_io_aware_97_b200 import binding as fa
+
+pytestmark = pytest.mark.gpu
+
+
+def check(o, lse, ref, q_shape):
+    r_o, r_lse, o_abs, v_sum, t_abs = ref
+    got = o.double().cpu().numpy().reshape(r_o.shape)
+    gl = lse.double().cpu().numpy().reshape(r_lse.shape)
+    assert not np.isnan(got).any()
+    t = t_abs.transpose(0, 2, 1)[..., None]
+    tol = 2.0 ** -8 * np.abs(r_o) + (2.0 ** -11 + 2.0 ** -17 * (1 + t)) * o_abs + 2.0 ** -25 * v_sum
+    bad = np.abs(got - r_o) > tol
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3], np.abs(got - r_o).max())
+    none = np.isneginf(r_lse)
+    assert np.array_equal(np.isneginf(gl), none)
+    assert np.all(np.abs(gl[~none] - r_lse[~none]) <= 2.0 ** -17 * (1 + t_abs[~none]))
+
+
+CASES = [
+    # lens, Nq, Hq, Hkv, d, page_size, scale_block
+    ([1], 1, 1, 1, 64, 16, 16),
+    ([37, 0, 16], 1, 12, 12, 64, 16, 16),
+    ([1000, 1, 0, 333, 64], 1, 32, 4, 128, 16, 16),
+    ([65, 64, 700], 1, 16, 2, 64, 32, 16),
+    ([2047, 130], 1, 8, 8, 128, 64, 32),
+    ([1, 127, 128, 129, 900], 1, 64, 4, 128, 128, 128),
+    ([700, 300], 1, 40, 2, 128, 256, 64),       # 20 heads of a group
+    ([513, 512], 1, 33, 1, 64, 512, 256),       # 33 heads of a group
+    ([300, 5, 0, 2, 129], 5, 16, 2, 128, 16, 16),  # new tokens that see nothing
+    ([64, 65, 66], 3, 7, 1, 64, 32, 32),
+    ([400, 70], 9, 12, 4, 128, 64, 64),
+    ([150, 40], 40, 4, 2, 64, 64, 16),
+    ([3000, 10], 2, 8, 1, 128, 16, 16),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=[f"{'_'.join(map(str, c[0]))}-n{c[1]}-h{c[2]}_{c[3]}-d{c[4]}-p{c[5]}_{c[6]}"
+                                             for c in CASES])
+def test_decode_fp8_matches_64_bits(case):
+    lens, Nq, Hq, H, d, ps, sb = case
+    rng = np.random.default_rng(5001)
+    kc, ks, vc, vs, table = cache8.build(rng, lens, ps, sb, H, d)
+    q = torch.from_numpy(rng.standard_normal((len(lens), Nq, Hq, d))).cuda().bfloat16()
+    dkc, dks, dvc, dvs, dt, dl = cache8.to_device(kc, ks, vc, vs, table, lens)
+    ref = cache8.attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, lens, sb, 1 / math.sqrt(d))
+    ws = torch.full((fa.fa_decode_paged_fp8_workspace_size(len(lens), Nq, Hq, H, d),), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    o, lse = fa.decode_paged_fp8(q, dkc, dvc, dks, dvs, dt, dl, workspace=ws)
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_error() == fa.FA_OK
+    check(o, lse, ref, q.shape)
+    # the workspace, used once, gives the same bits again; so does the 3-D form for one token
+    o2, lse2 = fa.decode_paged_fp8(q if Nq > 1 else q[:, 0], dkc, dvc, dks, dvs, dt, dl, workspace=ws)
+    assert torch.equal(o2.view_as(o), o) and torch.equal(lse2.view_as(lse), lse)
+
+
+@pytest.mark.parametrize("sb", [16, 64])
+def test_decode_fp8_scales_of_very_different_size(sb):
+    """V scales from 2^-40 to 2^30 and K scales that swamp some blocks: weights are taken relative
+    to the largest product of probability and scale, so the small blocks keep their bits."""
+    rng = np.random.default_rng(5002)
+    lens, H, d, ps = [400, 77], 2, 128, 64
+    kc, ks, vc, vs, table = cache8.build(rng, lens, ps, sb, H, d, spread=0.0)
+    vs *= np.exp2(rng.integers(-40, 31, vs.shape))
+    ks *= np.exp2(rng.integers(-6, 2, ks.shape))
+    # the block with the largest scale is one that softmax gives nothing
+    for b in range(2):
+        vs[table[b, 0], :, 0] = 2.0 ** 30
+        ks[table[b, 0], :, 0] = 0.0
+    q = torch.from_numpy(rng.standard_normal((2, 1, 8, d)) * 4).cuda().bfloat16()
+    dev = cache8.to_device(kc, ks, vc, vs, table, lens)
+    ref = cache8.attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, lens, sb, 1.0)
+    o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5], scale=1.0)
+    # weights below 2^-14 of the largest product lose bits; that product is at most max p * scale
+    r_o, r_lse, o_abs, v_sum, t_abs = ref
+    got = o.double().cpu().numpy()
+    t = t_abs.transpose(0, 2, 1)[..., None]
+    n = np.array(lens).reshape(2, 1, 1, 1)
+    # 2^-25 of the largest weight (<= o_abs_max / |code| >= 2^-9 ...): bounded by n * 2^-25 * 448 * w,
+    # where w <= sum of weights; o_abs carries that sum times the codes
+    wsum = _weight_max(q.double().cpu().numpy(), kc, ks, vs, table, lens, sb)
+    tol = 2.0 ** -8 * np.abs(r_o) + (2.0 ** -11 + 2.0 ** -17 * (1 + t)) * o_abs + n * 2.0 ** -25 * 448 * wsum
+    assert np.all(np.abs(got - r_o) <= tol)
+    check_lse = np.abs(lse.double().cpu().numpy() - r_lse)
+    assert np.all(check_lse <= 2.0 ** -17 * (1 + t_abs))
+
+
+def _weight_max(q, kc, ks, vs, table, lens, sb):
+    """Largest p_j * scale_j / sum p of each query, [B, 1, Hq, 1]."""
+    B, _, Hq, _ = q.shape
+    H, ps = kc.shape[2], kc.shape[1]
+    out = np.zeros((B, 1, Hq, 1))
+    for b in range(B):
+        k = cache8.gather(kc, ks, table[b], lens[b], sb)
+        j = np.arange(lens[b])
+        s = vs[table[b, j // ps], :, j % ps // sb]
+        for h in range(Hq):
+            t = k[:, h // (Hq // H)] @ q[b, 0, h]
+            p = np.exp(t - t.max())
+            out[b, 0, h] = (p * s[:, h // (Hq // H)]).max() / p.sum()
+    return out
+
+
+def test_decode_fp8_extreme_queries_and_zero_scales():
+    """Queries of 2^-60 and 2^60 times a scale that undoes it, a zero query (mean of V), K scale 0."""
+    rng = np.random.default_rng(5003)
+    lens, H, d, ps, sb = [90], 1, 64, 16, 16
+    kc, ks, vc, vs, table = cache8.build(rng, lens, ps, sb, H, d, spread=0.5)
+    ks[table[0, 1], 0, 0] = 0.0
+    base = rng.standard_normal((1, 1, 3, d))
+    dev = cache8.to_device(kc, ks, vc, vs, table, lens)
+    for e in (-60, 0, 60):
+        q = torch.from_numpy(base).cuda().bfloat16()
+        q[:, :, 2] = 0
+        q = (q.float() * 2.0 ** e).bfloat16()
+        scale = 0.125 * 2.0 ** -e
+        ref = cache8.attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, lens, sb, scale)
+        o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5], scale=scale)
+        check(o, lse, ref, q.shape)
+
+
+def test_decode_fp8_nan_reaches_only_what_attends_to_it():
+    rng = np.random.default_rng(5004)
+    lens, H, d, ps, sb = [40, 40], 2, 64, 16, 16
+    kc, ks, vc, vs, table = cache8.build(rng, lens, ps, sb, H, d)
+    q = torch.from_numpy(rng.standard_normal((2, 4, d))).cuda().bfloat16()
+    clean = cache8.to_device(kc, ks, vc, vs, table, lens)
+    o0, l0 = fa.decode_paged_fp8(q, clean[0], clean[2], clean[1], clean[3], clean[4], clean[5])
+    for w in ("k code", "v code", "k scale", "v scale"):
+        a = [kc.copy(), ks.copy(), vc.copy(), vs.copy()]
+        page = table[0, 1]
+        if w == "k code":
+            a[0][page, 3, 1, 5] = 0x7F
+        elif w == "v code":
+            a[2][page, 3, 1, 5] = 0xFF
+        elif w == "k scale":
+            a[1][page, 1, 0] = np.nan
+        else:
+            a[3][page, 1, 0] = np.nan
+        dev = cache8.to_device(*a, table, lens)
+        o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5])
+        # heads 2, 3 of sequence 0 read K/V head 1; a V code spoils its column only
+        assert torch.isnan(o[0, 2:]).all() if w != "v code" else torch.isnan(o[0, 2:, 5]).all(), w
+        assert torch.equal(o[0, :2], o0[0, :2]) and torch.equal(o[1], o0[1]), w
+        if w.startswith("k"):
+            assert torch.isnan(lse[0, 2:]).all(), w
+        else:
+            assert torch.equal(lse, l0), w
+    assert fa.fa_last_device_error() == fa.FA_OK
+
+
+def test_decode_fp8_reports_bad_page_and_clamps_lengths():
+    rng = np.random.default_rng(5005)
+    lens, H, d, ps, sb = [60, 30], 1, 64, 16, 16
+    kc, ks, vc, vs, table = cache8.build(rng, lens, ps, sb, H, d)
+    q = torch.from_numpy(rng.standard_normal((2, 4, d))).cuda().bfloat16()
+    dev = cache8.to_device(kc, ks, vc, vs, table, [60, -7])
+    o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5])
+    assert torch.all(o[1] == 0) and torch.isneginf(lse[1]).all() and fa.fa_last_device_error() == fa.FA_OK
+    bad = table.copy()
+    bad[1, 1] = kc.shape[0]
+    dev = cache8.to_device(np.zeros_like(kc), np.zeros_like(ks), np.zeros_like(vc), np.zeros_like(vs), bad, lens)
+    fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5])
+    assert fa.fa_last_device_error() == fa.FA_ERR_INVALID_ARG
+    assert fa.fa_last_device_error() == fa.FA_OK
+
+
+APPENDS = [
+    # old lengths, new lengths, Hkv, d, page_size, scale_block
+    ([0], [1], 1, 64, 16, 16),
+    ([15, 16, 17, 0], [1, 1, 1, 1], 8, 128, 16, 16),
+    ([0, 5, 31, 40], [100, 0, 33, 7], 3, 128, 32, 16),
+    ([3, 0], [300, 129], 2, 64, 64, 64),
+    ([200, 0, 1], [60, 256, 700], 5, 128, 256, 256),
+    ([127, 128], [2, 1], 4, 64, 128, 128),
+    ([9] * 40, [3] * 40, 1, 128, 16, 16),
+]
+
+
+def _append_problem(rng, old, new, H, d, ps, sb, grow=1.0):
+    lens = [a + b for a, b in zip(old, new)]
+    kc, ks, vc, vs, table = cache8.build(rng, old, ps, sb, H, d, extra=0)
+    need = sum((n + ps - 1) // ps for n in lens) + 2
+    P = kc.shape[0]
+    extra = need - P + 1
+
+    def pad(a, v):
+        return np.concatenate([a, np.full((max(extra, 0), *a.shape[1:]), v, a.dtype)])
+    kc, vc, ks, vs = pad(kc, 0x7F), pad(vc, 0x7F), pad(ks, np.nan), pad(vs, np.nan)
+    free = [p for p in range(kc.shape[0]) if p not in set(table[table >= 0].tolist())]
+    full = np.full((len(lens), max((n + ps - 1) // ps for n in lens) + 1), -1, np.int32)
+    for b, n in enumerate(lens):
+        had = (old[b] + ps - 1) // ps
+        full[b, :had] = table[b, :had]
+        for t in range(had, (n + ps - 1) // ps):
+            full[b, t] = free.pop()
+    total = sum(new)
+    xs = []
+    for _ in range(2):
+        x = rng.standard_normal((total, H, d)) * np.exp2(rng.uniform(-3, 3, (total, H, 1))) * grow
+        xs.append(torch.from_numpy(x).bfloat16())
+    return kc, ks, vc, vs, full, lens, xs
+
+
+def _run_append(kc, ks, vc, vs, table, lens, cu, xs):
+    dev = cache8.to_device(kc, ks, vc, vs, table, lens)
+    fa.cache_append_fp8(xs[0].cuda(), xs[1].cuda(), dev[0], dev[2], dev[1], dev[3], dev[4], dev[5],
+                        None if cu is None else torch.from_numpy(np.array(cu, np.int32)).cuda())
+    torch.cuda.synchronize()
+    return dev
+
+
+def _same(dev, kc, ks, vc, vs):
+    for t, a in ((dev[0], kc), (dev[2], vc)):
+        assert np.array_equal(t.view(torch.uint8).cpu().numpy(), a)
+    for t, a in ((dev[1], ks), (dev[3], vs)):
+        np.testing.assert_array_equal(t.cpu().numpy().astype(np.float64), a.astype(np.float32).astype(np.float64))
+
+
+@pytest.mark.parametrize("grow", [0.01, 1.0, 1e4], ids=["smaller", "alike", "larger"])
+@pytest.mark.parametrize("case", APPENDS, ids=[f"{len(c[0])}seq_{sum(c[1])}new_p{c[4]}_{c[5]}" for c in APPENDS])
+def test_append_is_the_model_bit_for_bit(case, grow):
+    old, new, H, d, ps, sb = case
+    kc, ks, vc, vs, table, lens, xs = _append_problem(np.random.default_rng(5006), old, new, H, d, ps, sb, grow)
+    cu = [0] + np.cumsum(new).tolist()
+    dev = _run_append(kc, ks, vc, vs, table, lens, cu, xs)
+    for codes, scales, x in ((kc, ks, xs[0]), (vc, vs, xs[1])):
+        cache8.append(codes, scales, x.double().numpy(), table, lens, cu, sb)
+    _same(dev, kc, ks, vc, vs)
+    assert fa.fa_last_device_error() == fa.FA_OK
+    if all(n == 1 for n in new):  # without offsets: one row each, the same bits
+        kc2, ks2, vc2, vs2, table2, lens2, xs2 = _append_problem(np.random.default_rng(5006), old, new, H, d, ps, sb,
+                                                                 grow)
+        _same(_run_append(kc2, ks2, vc2, vs2, table2, lens2, None, xs2), kc, ks, vc, vs)
+
+
+def test_append_special_values():
+    """Zeros, signed zeros, the type's extremes, subnormals, and rows that are not finite."""
+    rng = np.random.default_rng(5007)
+    old, new, H, d, ps, sb = [5, 0, 3], [20, 16, 2], 2, 64, 32, 16
+    kc, ks, vc, vs, table, lens, xs = _append_problem(rng, old, new, H, d, ps, sb)
+    big = float(torch.finfo(torch.bfloat16).max)
+    xs[0][:3] = 0.0
+    xs[0][1, 0] = -0.0
+    xs[0][3, 1, 7] = big
+    xs[0][12, 0, 0] = -big
+    xs[1][:20] = torch.tensor(2.0 ** -133).bfloat16() * torch.sign(xs[1][:20].float()).bfloat16()
+    xs[1][20:36, 0] = 0.0
+    xs[1][36, 0, 1] = float("nan")
+    xs[1][37, 1, 2] = float("inf")
+    cu = [0, 20, 36, 38]
+    dev = _run_append(kc, ks, vc, vs, table, lens, cu, xs)
+    for codes, scales, x in ((kc, ks, xs[0]), (vc, vs, xs[1])):
+        cache8.append(codes, scales, x.double().numpy(), table, lens, cu, sb)
+    _same(dev, kc, ks, vc, vs)
+    assert np.isnan(vs[table[2, 0], :, 0]).all()
+
+
+def test_append_token_by_token_reads_like_at_once():
+    """Power-of-two scales: a code that was rescaled differs from one written at once only below
+    the smallest normal e4m3 value (2^-6 of its scale), by at most half a step there each time the
+    scale grew (2^-10 of the final scale each, under 2^-9 in all)."""
+    rng = np.random.default_rng(5008)
+    H, d, ps, sb, n = 2, 128, 32, 32, 70
+    kc, ks, vc, vs, table, lens, xs = _append_problem(rng, [0], [n], H, d, ps, sb)
+    once = _run_append(kc, ks, vc, vs, table, lens, [0, n], xs)
+    step = cache8.to_device(kc, ks, vc, vs, table, lens)
+    k, v = xs[0].cuda(), xs[1].cuda()
+    for i in range(n):
+        at = torch.tensor([i + 1], dtype=torch.int32, device="cuda")
+        fa.cache_append_fp8(k[i:i + 1], v[i:i + 1], step[0], step[2], step[1], step[3], step[4], at)
+    assert torch.equal(once[1].nan_to_num(-1), step[1].nan_to_num(-1))
+    for w in (0, 2):
+        a, b = (cache8.gather(x[w].view(torch.uint8).cpu().numpy(), x[w + 1].double().cpu().numpy(), table[0], n, sb)
+                for x in (once, step))
+        s = np.repeat(once[w + 1].double().cpu().numpy()[table[0, :3], :, 0], 32, 0)[:n][..., None]
+        assert np.all(np.abs(a - b) <= 2.0 ** -9 * s)
+        assert np.all((a == b) | (np.abs(a) < 2.0 ** -5 * s))
+
+
+def test_append_skips_and_records_what_it_cannot_use():
+    rng = np.random.default_rng(5009)
+    H, d, ps, sb = 1, 64, 16, 16
+    for what in ("length", "page", "offsets", "table"):
+        kc, ks, vc, vs, table, lens, xs = _append_problem(rng, [4, 20], [3, 30], H, d, ps, sb)
+        cu, mlens, mtable = [0, 3, 33], list(lens), table.copy()
+        if what == "length":
+            mlens[0] = 2  # fewer than the 3 new rows
+        elif what == "page":
+            mtable[0, 0] = kc.shape[0] + 5
+        elif what == "table":
+            mlens[0] = table.shape[1] * ps + 1
+        else:
+            cu = [5, 3, 33]
+        dev = _run_append(kc, ks, vc, vs, mtable, mlens, cu, xs)
+        assert fa.fa_last_device_error() == fa.FA_ERR_INVALID_ARG, what
+        for codes, scales, x in ((kc, ks, xs[0]), (vc, vs, xs[1])):  # the second sequence is served
+            cache8.append(codes, scales, x.double().numpy(), table, [0, lens[1]], [3, 3, 33], sb)
+        _same(dev, kc, ks, vc, vs)
+    assert fa.fa_last_device_error() == fa.FA_OK
+
+
+def test_prefill_then_decode_through_the_cache():
+    """The whole path: rope, forward, append of the prompt, then steps of rope, append and decode,
+    against attention in 64 bits over what the cache holds; once more through a captured graph on
+    another stream."""
+    rng = np.random.default_rng(5010)
+    H, Hq, d, ps, sb, steps = 2, 8, 128, 32, 16, 5
+    new = [50, 1, 64]
+    lens = list(new)
+    maxp = 4
+    table = rng.permutation(3 * maxp).reshape(3, maxp).astype(np.int32)
+    P = 3 * maxp
+    kp = torch.full((P, ps, H, d), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    vp = kp.clone()
+    ks = torch.full((P, H, ps // sb), float("nan"), device="cuda")
+    vs = ks.clone()
+    dt = torch.from_numpy(table).cuda()
+    freqs = fa.rope_frequencies(d, 10000.0, "linear", 2.0)
+    cu = torch.tensor([0, 50, 51, 115], dtype=torch.int32, device="cuda")
+    pos = torch.cat([torch.arange(n) for n in new]).int().cuda()
+    q, k, v = (torch.from_numpy(rng.standard_normal((115, h, d))).cuda().bfloat16() for h in (Hq, H, H))
+    q, k = fa.rope(q, k, freqs, pos)
+    fa.forward(q, k, v, causal=True, cu_seqlens=cu)
+    seqlens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    fa.cache_append_fp8(k, v, kp, vp, ks, vs, dt, seqlens, cu)
+
+    sq, sk, sv = (torch.zeros(3, h, d, dtype=torch.bfloat16, device="cuda") for h in (Hq, H, H))
+
+    def step():
+        seqlens.add_(1)
+        a, b = fa.rope(sq, sk, freqs, seqlens - 1)
+        fa.cache_append_fp8(b, sv, kp, vp, ks, vs, dt, seqlens)
+        return (a, *fa.decode_paged_fp8(a, kp, vp, ks, vs, dt, seqlens))
+
+    def verify(a, o, lse):
+        ln = seqlens.cpu().numpy()
+        ref = cache8.attend(a.double().cpu().numpy()[:, None], kp.view(torch.uint8).cpu().numpy(),
+                            ks.double().cpu().numpy(), vp.view(torch.uint8).cpu().numpy(), vs.double().cpu().numpy(),
+                            table, ln, sb, 1 / math.sqrt(d))
+        check(o[:, None], lse[..., None], ref, None)
+
+    def feed():
+        for t in (sq, sk, sv):
+            t.copy_(torch.from_numpy(rng.standard_normal(tuple(t.shape))))
+
+    for _ in range(steps):
+        feed()
+        verify(*step())
+    g = torch.cuda.CUDAGraph()
+    was = seqlens.clone()
+    with torch.cuda.graph(g):
+        out = step()
+    seqlens.copy_(was)
+    for _ in range(3):
+        feed()
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            g.replay()
+        s.synchronize()
+        verify(*out)
+    assert fa.fa_last_device_error() == fa.FA_OK
