@@ -1045,10 +1045,33 @@ fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-template <int D>
-fa_status launch_decode_fp8(const Dec8Params& prm, cudaStream_t st) {
-  const dim3 grid(prm.Hq, prm.Nq, prm.B);
-  fa_decode_fp8_kernel<D><<<grid, 128, 0, st>>>(prm);
+// One wave of CTAs: what a device without a known SM count would be given is the B200's.
+int dec8_ctas(int rows) {
+  const int sms = sm_count_cached();
+  return (sms > 0 ? sms : 148) * (rows <= 32 ? 2 : 1);
+}
+int dec8_tile(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+template <int D, int MT, int RG>
+fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& prm, cudaStream_t st) {
+  using C = Dec8Cfg<D, MT, RG>;
+  CUtensorMap maps[2];
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return FA_ERR_CUDA;
+  const cuuint64_t dims[3] = {D, (cuuint64_t)prm.Hkv, (cuuint64_t)prm.num_pages << prm.page_shift};
+  const cuuint64_t strides[2] = {D, (cuuint64_t)prm.Hkv * D};
+  const cuuint32_t box[3] = {D, 1, (cuuint32_t)prm.box}, estr[3] = {1, 1, 1};
+  for (int w = 0; w < 2; ++w)
+    if (enc(&maps[w], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w ? vp : kp), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return FA_ERR_CUDA;
+  auto kern = fa_decode_fp8_kernel<D, MT, RG>;
+  if (set_smem(kern, C::kSmem) != cudaSuccess) return FA_ERR_CUDA;
+  const int ctas = dec8_ctas(prm.rows);
+  kern<<<ctas, C::kThreads, C::kSmem, st>>>(maps[0], maps[1], prm);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  fa_decode_fp8_combine_kernel<D, C::kRows><<<dim3(ctas, (std::min(prm.rows, C::kRows) + 3) / 4), 128, 0, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -1088,8 +1111,12 @@ extern "C" fa_status fa_cache_append_fp8(const void* k, const void* v, const int
 }
 
 extern "C" size_t fa_decode_paged_fp8_workspace_size(int B, int Nq, int Hq, int Hkv, int d) {
-  if (B <= 0 || Nq <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0) return 0;
-  return 16;
+  if (B <= 0 || Nq <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0) return 0;
+  // two parts per CTA (sums, then m and l) and a descriptor per CTA
+  const int64_t rows = (int64_t)Nq * (Hq / Hkv);
+  const int tile = rows > 32 ? 64 : dec8_tile((int)rows);
+  const size_t ctas = (size_t)dec8_ctas(tile);
+  return align_up(2 * ctas * tile * d * 4, 256) + align_up(2 * ctas * tile * 8, 256) + align_up(ctas * 16, 256);
 }
 
 extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
@@ -1108,10 +1135,10 @@ extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, con
   if (Nq > 65535 || Hq > 65535) return FA_ERR_UNSUPPORTED;
   const size_t need = fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d);
   if (!workspace || workspace_bytes < need || !aligned16(workspace)) return FA_ERR_WORKSPACE;
+  const int64_t rows = (int64_t)Nq * (Hq / Hkv);
+  if (rows * Hkv >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
   Dec8Params prm{};
   prm.q = static_cast<const __nv_bfloat16*>(q);
-  prm.pages[0] = static_cast<const uint8_t*>(k_pages);
-  prm.pages[1] = static_cast<const uint8_t*>(v_pages);
   prm.scales[0] = k_scale;
   prm.scales[1] = v_scale;
   prm.block_table = block_table;
@@ -1128,8 +1155,24 @@ extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, con
   prm.sb_shift = __builtin_ctz((unsigned)scale_block);
   prm.max_pages = max_pages_per_seq;
   prm.tau = (float)((double)scale * 1.4426950408889634074);
+  prm.rows = (int)rows;
+  const int tile = dec8_tile(prm.rows);
+  prm.tiles = (prm.rows + tile - 1) / tile;
+  prm.box = std::min(page_size, kDec8Keys);
+  const size_t ctas = (size_t)dec8_ctas(prm.rows);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  prm.ws_acc = reinterpret_cast<float*>(ws);
+  ws += align_up(2 * ctas * tile * d * 4, 256);
+  prm.ws_ml = reinterpret_cast<float2*>(ws);
+  prm.ws_desc = reinterpret_cast<int4*>(ws + align_up(2 * ctas * tile * 8, 256));
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return d == 64 ? launch_decode_fp8<64>(prm, st) : launch_decode_fp8<128>(prm, st);
+  if (d == 64)
+    return tile == 16   ? launch_decode_fp8<64, 1, 1>(k_pages, v_pages, prm, st)
+           : tile == 32 ? launch_decode_fp8<64, 2, 1>(k_pages, v_pages, prm, st)
+                        : launch_decode_fp8<64, 2, 2>(k_pages, v_pages, prm, st);
+  return tile == 16   ? launch_decode_fp8<128, 1, 1>(k_pages, v_pages, prm, st)
+         : tile == 32 ? launch_decode_fp8<128, 2, 1>(k_pages, v_pages, prm, st)
+                      : launch_decode_fp8<128, 2, 2>(k_pages, v_pages, prm, st);
 }
 
 // ---------------------------------------------------------------------------------------

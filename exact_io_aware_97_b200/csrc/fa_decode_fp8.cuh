@@ -6,95 +6,639 @@
 //   t_j = scale * sk_j * (q . k_j),  p_j = e^(t_j - m),  o = sum_j p_j sv_j v_j / sum_j p_j,
 // where k_j, v_j are the stored e4m3 values and sk_j, sv_j the scales of their blocks.
 //
-// One CTA takes one (sequence, query token, query head): its four warps walk the rows with a
-// running maximum and sum each and merge in shared memory.
+// Bound by HBM: 2 d bytes per cache row and K/V head are read once.  What decides whether the
+// stream is kept up is the work per byte, twice that of a bf16 cache.
+//
+// Partition.  The Nq * G query rows of one K/V head form tiles of R rows; a unit is (sequence,
+// K/V head, tile) and is cut into chunks of 64 cache rows.  All units' chunks, one after the
+// other, are dealt to the CTAs of one wave in equal contiguous shares, whatever the lengths, so
+// every CTA streams the same number of bytes.  A CTA writes the output of units that lie in its
+// share whole; of at most two others (its first and its last) it writes partial sums, which
+// fa_decode_fp8_combine_kernel merges with the m / l rule.
+//
+// Products.  e4m3 values are exact in fp16, so K and V are widened in registers (one conversion
+// for two values, after ldmatrix) and multiplied on m16n8k16 fp16 tensor-core products with fp32
+// sums.  A query row is scaled by a power of two into [1, 2) at its largest element, which keeps
+// its bf16 bits in fp16.  The weights p_j sv_j go through fp16 (11 bits; p alone in bf16, as over
+// a bf16 cache, has 8) relative to their own running maximum, so neither a scale far from the
+// others' nor a small p loses bits; p itself is summed in fp32 for l.  A warp owns 16 consecutive
+// rows of each chunk, which lie in one scale block: one K and one V scale per warp and chunk.
 #pragma once
 
 #include <cuda_fp16.h>
 
 #include "fa_cache.cuh"
+#include "fa_decode_sm100.cuh"
 #include "fa_device.cuh"
 
 namespace fa {
 
 struct Dec8Params {
   const __nv_bfloat16* q;  // [B, Nq, Hq, D]
-  const uint8_t* pages[2];
   const float* scales[2];  // [num_pages, Hkv, page_size >> sb_shift]
   const int32_t* block_table;
   const int32_t* seqlens;
   __nv_bfloat16* o;
-  float* lse;  // [B, Hq, Nq] or null
-  int B, Nq, Hq, Hkv, G, num_pages, page_shift, sb_shift, max_pages;
+  float* lse;      // [B, Hq, Nq] or null
+  float* ws_acc;   // [2 * CTAs][R][D]
+  float2* ws_ml;   // [2 * CTAs][R]: m (base 2), l
+  int4* ws_desc;   // [CTAs]: the unit whose first part is this CTA's last segment (see combine)
+  int B, Nq, Hq, Hkv, G, rows, tiles;  // rows = Nq * G, tiles = ceil(rows / R)
+  int num_pages, page_shift, sb_shift, max_pages, box;
   float tau;  // scale * log2(e)
 };
 
+constexpr int kDec8Keys = 64;  // cache rows of a chunk
+
+template <int D, int MT, int RG>
+struct Dec8Cfg {
+  static constexpr int kRows = 16 * MT * RG;       // R: query rows of a unit
+  static constexpr int kWarps = 4 * RG;            // compute warps: 4 row slices of the chunk x RG row groups
+  // A warp with two row tiles needs more registers than its share: the producer then is a warp of
+  // a warpgroup of its own, which gives registers up (threads x registers of a CTA: MT = 2, RG = 1:
+  // 128 x 208 + 128 x 40 <= 256 x 128; RG = 2: 256 x 224 + 128 x 40 <= 384 x 168).
+  static constexpr bool kSplitRegs = MT > 1;
+  static constexpr int kComputeRegs = RG == 1 ? 208 : 224;
+  static constexpr int kThreads = (kWarps + (kSplitRegs ? 4 : 1)) * 32;
+  static constexpr int kCtas = RG == 1 ? 2 : 1;    // per SM
+  static constexpr int kHalf = kDec8Keys * D;      // bytes of K (or V) of a chunk
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = (D == 128) ? (RG == 1 ? 4 : 7) : (RG == 1 ? 6 : 12);
+  static constexpr int kMergeFloats = RG * (4 * 16 * D + 2 * 4 * 16);
+  static constexpr int kQBytes = MT == 1 ? 0 : RG * MT * (D / 16) * 32 * 16;
+  static constexpr int kSmem = 1024 + kStages * kStage + kMergeFloats * 4 + kQBytes + kStages * 8 * 4 +
+                               2 * kStages * 8 + 64;
+};
+
+// Position in the sequence of chunks: sequence b, offset u among its units' chunks.
+struct Dec8Seg {
+  int b, len, chunks;  // sequence, its length and chunks per unit
+  int unit;            // K/V head * tiles + tile
+  int c0, c1;          // chunks [c0, c1)
+};
+
+struct Dec8Walk {
+  long long left, u;
+  int b;
+  __device__ __forceinline__ bool next(const Dec8Params& p, Dec8Seg& s) {
+    if (left <= 0) return false;
+    int len;
+    for (;; ++b) {  // left > 0: some sequence from b on holds rows
+      const long long cap = (long long)p.max_pages << p.page_shift;
+      len = (int)min((long long)max(__ldg(p.seqlens + b), 0), cap);
+      if (len > 0) break;
+    }
+    s.b = b;
+    s.len = len;
+    s.chunks = (len + kDec8Keys - 1) / kDec8Keys;
+    s.unit = (int)(u / s.chunks);
+    s.c0 = (int)(u - (long long)s.unit * s.chunks);
+    s.c1 = (int)min((long long)s.chunks, s.c0 + left);
+    left -= s.c1 - s.c0;
+    u += s.c1 - s.c0;
+    if (u == (long long)s.chunks * p.Hkv * p.tiles) {
+      ++b;
+      u = 0;
+    }
+    return true;
+  }
+};
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four e4m3 bytes to two fp16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Byte offset of the 16-byte unit `unit` of row `row` in a tile of D-byte rows stored by TMA with
+// the 128-byte (D = 128) or 64-byte (D = 64) swizzle.
 template <int D>
-__global__ void __launch_bounds__(128) fa_decode_fp8_kernel(const Dec8Params p) {
+__device__ __forceinline__ uint32_t dec8_offset(int row, int unit) {
+  return row * D + ((D == 128 ? unit ^ (row & 7) : unit ^ ((row >> 1) & 3)) << 4);
+}
+
+template <int D, int MT, int RG>
+__global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, RG>::kCtas)
+    fa_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const Dec8Params p) {
+  using C = Dec8Cfg<D, MT, RG>;
+  constexpr int NS = C::kStages, KS = D / 16, R = C::kRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* merge = reinterpret_cast<float*>(ring + NS * C::kStage);
+  uint4* sm_q = reinterpret_cast<uint4*>(merge + C::kMergeFloats);
+  float* sm_scale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(sm_q) + C::kQBytes);  // [NS][2][4]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm_scale + NS * 8);
+  uint64_t* empty = full + NS;
+  __shared__ long long sm_scan[C::kThreads / 32], sm_u;
+  __shared__ int sm_b;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full + s, 1 + 8);  // the producer's expect_tx, and eight lanes' scales
+      mbar_init(empty + s, C::kWarps);
+    }
+    fence_barrier_init();
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+
+  // This CTA's share of all chunks: prefix sums over the sequences.
+  const long long cap = (long long)p.max_pages << p.page_shift;
+  const int per = (p.B + C::kThreads - 1) / C::kThreads;
+  const int b_lo = min(threadIdx.x * per, p.B), b_hi = min(b_lo + per, p.B);
+  auto chunks_of = [&](int b) {
+    return (int)((min((long long)max(__ldg(p.seqlens + b), 0), cap) + kDec8Keys - 1) / kDec8Keys);
+  };
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += chunks_of(b);
+  long long incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  if (lane == 31) sm_scan[warp] = incl;
+  __syncthreads();
+  long long before = 0, all = 0;
+  for (int w = 0; w < C::kThreads / 32; ++w) {
+    before += w < warp ? sm_scan[w] : 0;
+    all += sm_scan[w];
+  }
+  before += incl - mine;
+  const long long HR = (long long)p.Hkv * p.tiles, T = all * HR;
+  const long long ctas = min((long long)gridDim.x, T);  // each of these has at least one chunk
+  const bool busy = blockIdx.x < ctas;
+  const long long begin = busy ? blockIdx.x * T / ctas : 0, end = busy ? (blockIdx.x + 1) * T / ctas : 0;
+  if (begin < end && before * HR <= begin && begin < (before + mine) * HR) {
+    long long at = before * HR;
+    int b = b_lo;
+    for (;; ++b) {
+      const long long n = chunks_of(b) * HR;
+      if (begin < at + n) break;
+      at += n;
+    }
+    sm_b = b;
+    sm_u = begin - at;
+  }
+  if (threadIdx.x == 0) p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+  Dec8Walk walk{end - begin, begin < end ? sm_u : 0, begin < end ? sm_b : 0};
+  Dec8Seg seg;
+
+  if (warp >= C::kWarps) {
+    // ------------------------------------------------------------ producer
+    if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    // Lanes 0..7: (K or V, 16-row slice of the chunk).  Each fetches the scale of its slice, and
+    // the lanes at the head of a page's rows its box of them; slices past the end are left out.
+    // The table entry of the next chunk is loaded while this one is issued.
+    if (warp == C::kWarps && lane < 8) {
+      const int which = lane >> 2, sub = lane & 3;
+      const uint64_t pol = policy_evict_first();
+      const int psm = (1 << p.page_shift) - 1, nb_shift = p.page_shift - p.sb_shift;
+      const bool leads = (16 * sub) % p.box == 0;
+      long long g = 0;  // stages issued
+      bool ok = true;
+      while (ok && walk.next(p, seg)) {
+        const int kvh = seg.unit / p.tiles;
+        const int32_t* bt = p.block_table + (long long)seg.b * p.max_pages;
+        int tok = seg.c0 * kDec8Keys + 16 * sub;
+        int page_next = tok < seg.len ? __ldg(bt + (tok >> p.page_shift)) : 0;
+        for (int c = seg.c0; c < seg.c1; ++c, ++g, tok += kDec8Keys) {
+          int page = page_next;
+          const bool here = tok < seg.len;
+          if (c + 1 < seg.c1 && tok + kDec8Keys < seg.len) page_next = __ldg(bt + ((tok + kDec8Keys) >> p.page_shift));
+          if (page < 0 || page >= p.num_pages) {
+            atomicOr(&g_error_word, kErrBadPage);
+            page = 0;
+          }
+          const int slot = (int)(g % NS);
+          if (g >= NS && !mbar_wait(empty + slot, (uint32_t)((g / NS) - 1) & 1u)) ok = false;
+          ok = __all_sync(0xffu, ok);
+          if (!ok) break;
+          uint8_t* st = ring + slot * C::kStage;
+          if (lane == 0) {
+            const int rows = min(kDec8Keys, (seg.len - c * kDec8Keys + p.box - 1) / p.box * p.box);
+            mbar_arrive_expect_tx(full + slot, 2 * rows * D);
+          }
+          __syncwarp(0xffu);
+          const int r = tok & psm;
+          if (here) {
+            if (leads)
+              tma_load_3d_hint(st + which * C::kHalf + 16 * sub * D, which ? &tmV : &tmK, 0, kvh,
+                               (page << p.page_shift) + r, full + slot, pol);
+            const float* src = p.scales[which] + (((long long)page * p.Hkv + kvh) << nb_shift) + (r >> p.sb_shift);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sm_scale + slot * 8 + lane)),
+                         "l"(src)
+                         : "memory");
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + slot))
+                         : "memory");
+          } else {
+            mbar_arrive(full + slot);
+          }
+        }
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- compute warps
+  if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kComputeRegs));
+  const int slice = warp & 3, rg = warp >> 2;  // 16-row slice of the chunk, row group of the tile
+  const int g = lane >> 2, tig = lane & 3;
+  const int mi = lane >> 3, rr = lane & 7;
+  long long stage = 0;
+  bool ok = true;
+
+  // sequences without rows: o = 0, lse = -inf
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (min((long long)__ldg(p.seqlens + b), cap) > 0) continue;
+    const long long n = (long long)p.Nq * p.Hq;
+    for (long long k = threadIdx.x; k < n * D / 8; k += C::kWarps * 32)
+      reinterpret_cast<uint4*>(p.o)[(long long)b * (n * D / 8) + k] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse)
+      for (long long k = threadIdx.x; k < n; k += C::kWarps * 32) p.lse[b * n + k] = -INFINITY;
+  }
+
+  while (walk.next(p, seg)) {
+    const int kvh = seg.unit / p.tiles, tile = seg.unit - kvh * p.tiles;
+    const int row0 = tile * R + rg * 16 * MT;  // first query row of this warp
+    // rows [16 mt + g + 8 hr]: query token and head, how many cache rows it sees, its factor
+    int limit[MT][2];
+    float fac[MT][2];
+    uint32_t qa[MT == 1 ? KS : 1][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const int row = row0 + 16 * mt + g + 8 * hr;
+        const bool in = row < p.rows;
+        const int i = in ? row / p.G : 0, h = kvh * p.G + (in ? row - i * p.G : 0);
+        limit[mt][hr] = in ? seg.len - p.Nq + 1 + i : seg.len;
+        const uint2* src =
+            reinterpret_cast<const uint2*>(p.q + (((long long)seg.b * p.Nq + i) * p.Hq + h) * D) + tig;
+        uint2 x[KS];
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          x[k] = in ? __ldg(src + 4 * k) : make_uint2(0u, 0u);
+          top = max(max(top, max((x[k].x << 16) & 0x7FFF0000u, x[k].x & 0x7FFF0000u)),
+                    max((x[k].y << 16) & 0x7FFF0000u, x[k].y & 0x7FFF0000u));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^-e with e the exponent of the largest element (0 for a zero row or one that is not finite)
+        const int be = (top == 0u || top >= 0x7F800000u) ? 127 : max((int)(top >> 23), 1);
+        const float down = be >= 254 ? 5.877471754111438e-39f : __uint_as_float((uint32_t)(254 - be) << 23);
+        fac[mt][hr] = p.tau * __uint_as_float((uint32_t)be << 23);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          const uint32_t lo = pack_f16x2(__uint_as_float(x[k].x << 16) * down,
+                                         __uint_as_float(x[k].x & 0xFFFF0000u) * down);
+          const uint32_t hi = pack_f16x2(__uint_as_float(x[k].y << 16) * down,
+                                         __uint_as_float(x[k].y & 0xFFFF0000u) * down);
+          if constexpr (MT == 1) {
+            qa[k][hr] = lo;      // A fragment: row g + 8 hr, columns 16 k + 4 tig + 0, 1
+            qa[k][2 + hr] = hi;  // and + 2, 3 (the order that ldmatrix gives the K bytes in)
+          } else if (slice == 0) {
+            uint32_t* to = reinterpret_cast<uint32_t*>(sm_q + ((rg * MT + mt) * KS + k) * 32 + lane);
+            to[hr] = lo;
+            to[2 + hr] = hi;
+          }
+        }
+      }
+    if constexpr (MT > 1) asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
+    const int first_limit = seg.len - p.Nq + 1 + min(row0, p.rows - 1) / p.G;
+    const bool idle = row0 >= p.rows;  // a row group without rows
+
+    float acc[MT][D / 8][4];
+    float m_r[MT][2], l_r[MT][2], w_r[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) acc[mt][n][0] = acc[mt][n][1] = acc[mt][n][2] = acc[mt][n][3] = 0.f;
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        m_r[mt][hr] = w_r[mt][hr] = -INFINITY;
+        l_r[mt][hr] = 0.f;
+      }
+    }
+
+    for (int c = seg.c0; c < seg.c1; ++c, ++stage) {
+      const int slot = (int)(stage % NS);
+      if (ok && !mbar_wait(full + slot, (uint32_t)(stage / NS) & 1u)) ok = false;
+      const int j0 = c * kDec8Keys + 16 * slice;
+      if (ok && !idle && j0 < seg.len) {
+        const uint32_t kb = smem_u32(ring + slot * C::kStage), vb = kb + C::kHalf;
+        const float sk = sm_scale[slot * 8 + slice];
+        const float lsv = __log2f(sm_scale[slot * 8 + 4 + slice]);
+        const bool ends = j0 + 16 > seg.len;         // rows past the end in this slice
+        const bool partly = j0 + 16 > first_limit;   // rows that some query does not see
+        if (ends) {
+          // Those rows may hold NaN codes: as zeros they add nothing.
+          for (int u = lane; u < 16 * KS; u += 32)
+            if (j0 + (u & 15) >= seg.len)
+              *reinterpret_cast<uint4*>(ring + slot * C::kStage + C::kHalf + (16 * slice + (u & 15)) * D +
+                                        (u >> 4) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          __syncwarp();
+        }
+        if (partly) {
+          // A NaN code of V may be for some queries only (0 * NaN would reach the others): put the
+          // NaN into the sums of those that see it and a zero in its place.
+          uint8_t* vs = ring + slot * C::kStage + C::kHalf;
+          uint32_t nan = 0;
+          for (int u = lane; u < 16 * D / 4; u += 32) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(vs + 16 * slice * D + 4 * u);
+            nan |= ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+          }
+          if (__any_sync(0xffffffffu, nan != 0)) {
+            const float bad = __uint_as_float(0x7FC00000u);
+            for (int r = 0; r < 16 && j0 + r < seg.len; ++r)
+#pragma unroll
+              for (int k = 0; k < KS; ++k) {
+                const uint32_t w =
+                    *reinterpret_cast<const uint32_t*>(vs + dec8_offset<D>(16 * slice + r, k) + 4 * tig);
+                const uint32_t n4 = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                if (n4 == 0) continue;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                  for (int hr = 0; hr < 2; ++hr)
+                    if (j0 + r < limit[mt][hr])
+#pragma unroll
+                      for (int x = 0; x < 4; ++x)
+                        if ((n4 >> (8 * x + 7)) & 1u) acc[mt][2 * k + (x & 1)][2 * hr + (x >> 1)] = bad;
+              }
+            __syncwarp();
+            for (int u = lane; u < 16 * D; u += 32)
+              if ((vs[16 * slice * D + u] & 0x7Fu) == 0x7Fu) vs[16 * slice * D + u] = 0;
+            __syncwarp();
+          }
+        }
+        float sc[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[mt][0][e] = sc[mt][1][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+          // matrices: rows 0..7 and 8..15 of the slice, units k and k + 1
+          uint32_t w0, w1, w2, w3, b0, b1;
+          ldsm_x4(kb + dec8_offset<D>(16 * slice + (mi & 1) * 8 + rr, k + (mi >> 1)), w0, w1, w2, w3);
+          const uint32_t ws[4] = {w0, w1, w2, w3};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            e4m3x4_to_f16(ws[x], b0, b1);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              if constexpr (MT == 1) {
+                mma_f16_16816(sc[0][x & 1], qa[k + (x >> 1)], b0, b1);
+              } else {
+                const uint4 a4 = sm_q[((rg * MT + mt) * KS + k + (x >> 1)) * 32 + lane];
+                const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
+                mma_f16_16816(sc[mt][x & 1], a, b0, b1);
+              }
+            }
+          }
+        }
+        uint32_t pa[MT][4];
+        bool moved = false;
+        float aw[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hr = 0; hr < 2; ++hr) {
+            const float f = fac[mt][hr] * sk;
+            float t[4] = {sc[mt][0][2 * hr] * f, sc[mt][0][2 * hr + 1] * f, sc[mt][1][2 * hr] * f,
+                          sc[mt][1][2 * hr + 1] * f};
+            if (partly) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (j0 + (x >> 1) * 8 + 2 * tig + (x & 1) >= limit[mt][hr]) t[x] = -INFINITY;
+            }
+            float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float m_new = fmaxf(m_r[mt][hr], mx), w_new = fmaxf(w_r[mt][hr], mx + lsv);
+            const float ms = m_new == -INFINITY ? 0.f : m_new;
+            const float wr = w_new == -INFINITY ? 0.f : w_new;
+            l_r[mt][hr] *= ex2_approx(m_r[mt][hr] - ms);
+            aw[mt][hr] = ex2_approx(w_r[mt][hr] - wr);
+            moved |= w_new != w_r[mt][hr];
+            m_r[mt][hr] = m_new;
+            w_r[mt][hr] = w_new;
+            const float wref = wr - lsv;
+            float w[4], sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              sum += ex2_approx(t[x] - ms);
+              w[x] = ex2_approx(t[x] - wref);
+            }
+            if (partly) {  // a NaN scale is not for rows that the query does not see
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (j0 + (x >> 1) * 8 + 2 * tig + (x & 1) >= limit[mt][hr]) w[x] = 0.f;
+            }
+            l_r[mt][hr] += sum;
+            pa[mt][hr] = pack_f16x2(w[0], w[1]);
+            pa[mt][2 + hr] = pack_f16x2(w[2], w[3]);
+          }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+              acc[mt][n][0] *= aw[mt][0];
+              acc[mt][n][1] *= aw[mt][0];
+              acc[mt][n][2] *= aw[mt][1];
+              acc[mt][n][3] *= aw[mt][1];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < KS; k += 2) {
+          // transposed: a register holds bytes (2 g, 2 g + 1) of the unit for rows 2 tig and 2 tig + 1
+          uint32_t w0, w1, w2, w3, e0, o0, e1, o1;
+          ldsm_x4_t(vb + dec8_offset<D>(16 * slice + (mi & 1) * 8 + rr, k + (mi >> 1)), w0, w1, w2, w3);
+          const uint32_t ws[4] = {w0, w1, w2, w3};
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            e4m3x4_to_f16(__byte_perm(ws[2 * x], 0u, 0x3120), e0, o0);
+            e4m3x4_to_f16(__byte_perm(ws[2 * x + 1], 0u, 0x3120), e1, o1);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma_f16_16816(acc[mt][2 * (k + x)], pa[mt], e0, e1);      // columns 16 (k + x) + 2 n
+              mma_f16_16816(acc[mt][2 * (k + x) + 1], pa[mt], o0, o1);  // and + 2 n + 1
+            }
+          }
+        }
+      }
+      // The slot is refilled by TMA (the async proxy) once every warp has arrived; the fence
+      // orders this warp's generic-proxy reads and writes of it before that.
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + slot);
+    }
+
+    // Merge the four slices of each row group, 16 rows at a time, and write them out.
+    float* mg_o = merge + rg * (4 * 16 * D + 2 * 4 * 16);
+    float* mg_m = mg_o + 4 * 16 * D;
+    float* mg_l = mg_m + 4 * 16;
+    const bool whole = seg.c0 == 0 && seg.c1 == seg.chunks;
+    const int part = 2 * blockIdx.x + (seg.c0 == 0 ? 1 : 0);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        float l = l_r[mt][hr];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        const float m = m_r[mt][hr];
+        // weights so far are relative to 2^w_r: relative to 2^m from here on
+        const float e = w_r[mt][hr] == -INFINITY ? 0.f : ex2_approx(w_r[mt][hr] - m);
+        if (tig == 0) {
+          mg_m[slice * 16 + g + 8 * hr] = m;
+          mg_l[slice * 16 + g + 8 * hr] = l;
+        }
+        float* to = mg_o + (slice * 16 + g + 8 * hr) * D + 4 * tig;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          *reinterpret_cast<float4*>(to + 16 * k) =
+              make_float4(acc[mt][2 * k][2 * hr] * e, acc[mt][2 * k + 1][2 * hr] * e,
+                          acc[mt][2 * k][2 * hr + 1] * e, acc[mt][2 * k + 1][2 * hr + 1] * e);
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
+      for (int idx = threadIdx.x & 127; idx < 16 * (D / 4); idx += 128) {
+        const int r = idx / (D / 4), col = 4 * (idx - r * (D / 4));
+        const int row = row0 + 16 * mt + r;
+        if (row >= p.rows) break;
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, mg_m[w * 16 + r]);
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float mw = mg_m[w * 16 + r];
+          const float e = mw == -INFINITY ? 0.f : ex2_approx(mw - M);  // 0 * NaN stays NaN
+          L += e * mg_l[w * 16 + r];
+          const float4 x = *reinterpret_cast<const float4*>(mg_o + (w * 16 + r) * D + col);
+          A.x += e * x.x;
+          A.y += e * x.y;
+          A.z += e * x.z;
+          A.w += e * x.w;
+        }
+        if (whole) {
+          const int i = row / p.G, h = kvh * p.G + row - i * p.G;
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          *reinterpret_cast<uint2*>(p.o + (((long long)seg.b * p.Nq + i) * p.Hq + h) * D + col) =
+              make_uint2(pack_bf16x2(A.x * inv, A.y * inv), pack_bf16x2(A.z * inv, A.w * inv));
+          if (col == 0 && p.lse)
+            p.lse[((long long)seg.b * p.Hq + h) * p.Nq + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+        } else {
+          const long long slot = (long long)part * R + rg * 16 * MT + 16 * mt + r;
+          *reinterpret_cast<float4*>(p.ws_acc + slot * D + col) = A;
+          if (col == 0) p.ws_ml[slot] = make_float2(M, L);
+        }
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
+    }
+    if (!whole && seg.c0 == 0 && threadIdx.x == 0) {
+      // the parts after this one: the CTAs whose shares begin before the unit ends
+      const long long stop = end + (seg.chunks - seg.c1);
+      int parts = 1;
+      while (blockIdx.x + parts < ctas && (blockIdx.x + parts) * T / ctas < stop) ++parts;
+      p.ws_desc[blockIdx.x] = make_int4(parts, seg.b, kvh, tile);
+    }
+  }
+}
+
+// Merges the parts of the unit that begins in CTA x's last segment: its part 2 x + 1, then the
+// first parts 2 (x + 1), 2 (x + 2), ...  A warp per query row, or four when there are many parts.
+template <int D, int R>
+__global__ void __launch_bounds__(128) fa_decode_fp8_combine_kernel(const Dec8Params p) {
   constexpr int V = D / 32;
   __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.x, i = blockIdx.y, b = blockIdx.z, kvh = h / p.G;
-  const long long cap = (long long)p.max_pages << p.page_shift;
-  const int len = (int)min((long long)max(__ldg(p.seqlens + b), 0), cap);
-  const int n = len - p.Nq + 1 + i;  // rows this query sees (may be <= 0)
-  const long long qrow = ((long long)b * p.Nq + i) * p.Hq + h;
-  float q[V], acc[V];
+  const int x = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 d = p.ws_desc[x];
+  const int parts = d.x;
+  if (parts == 0) return;
+  const bool wide = parts > 8;
+  for (int k = 0; k < (wide ? 4 : 1); ++k) {
+    const int r = blockIdx.y * 4 + (wide ? k : warp), row = d.w * R + r;
+    const bool in = row < p.rows;
+    float M = -INFINITY, L = 0.f, a[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    q[v] = __bfloat162float(p.q[qrow * D + lane * V + v]);
-    acc[v] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  const int psm = (1 << p.page_shift) - 1, nb_shift = p.page_shift - p.sb_shift;
-  for (int j = warp; j < n; j += 4) {
-    int page = __ldg(p.block_table + (long long)b * p.max_pages + (j >> p.page_shift));
-    if (page < 0 || page >= p.num_pages) {
-      atomicOr(&g_error_word, kErrBadPage);
-      page = 0;
+    for (int v = 0; v < V; ++v) a[v] = 0.f;
+    if (in) {
+      const int step = wide ? 4 : 1;
+#pragma unroll 4
+      for (int s = wide ? warp : 0; s < parts; s += step) {
+        const long long slot = (long long)(2 * (x + s) + (s == 0 ? 1 : 0)) * R + r;
+        const float2 ml = p.ws_ml[slot];
+        float y[V];
+        if constexpr (V == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(p.ws_acc + slot * D + lane * 4);
+          y[0] = f.x, y[1] = f.y, y[2] = f.z, y[3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(p.ws_acc + slot * D + lane * 2);
+          y[0] = f.x, y[1] = f.y;
+        }
+        const float m_new = fmaxf(M, ml.x);
+        const float ms = m_new == -INFINITY ? 0.f : m_new;
+        const float e0 = ex2_approx(M - ms), e1 = ex2_approx(ml.x - ms);
+        L = L * e0 + ml.y * e1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] = a[v] * e0 + y[v] * e1;
+        M = m_new;
+      }
     }
-    const int r = j & psm;
-    const long long at = ((((long long)page << p.page_shift) + r) * p.Hkv + kvh) * D + lane * V;
-    const long long sat = (((long long)page * p.Hkv + kvh) << nb_shift) + (r >> p.sb_shift);
-    float s = 0.f;
+    if (wide) {
+      if (lane == 0) {
+        sm_m[warp] = M;
+        sm_l[warp] = L;
+      }
 #pragma unroll
-    for (int v = 0; v < V; ++v) s = fmaf(q[v], e4m3_value(p.pages[0][at + v]), s);
+      for (int v = 0; v < V; ++v) sm_o[warp][lane * V + v] = a[v];
+      __syncthreads();
+      M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+      L = 0.f;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    const float t = s * (p.scales[0][sat] * p.tau);
-    const float m_new = fmaxf(m, t);
-    const float alpha = (m_new == -INFINITY) ? 1.f : exp2f(m - m_new);
-    const float pj = exp2f(t - ((m_new == -INFINITY) ? 0.f : m_new));
-    l = l * alpha + pj;
-    const float w = pj * p.scales[1][sat];
+      for (int v = 0; v < V; ++v) a[v] = 0.f;
+      const float ms = M == -INFINITY ? 0.f : M;
+      for (int w = 0; w < 4; ++w) {
+        const float e = ex2_approx(sm_m[w] - ms);
+        L += e * sm_l[w];
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = fmaf(w, e4m3_value(p.pages[1][at + v]), acc[v] * alpha);
-    m = m_new;
+        for (int v = 0; v < V; ++v) a[v] += e * sm_o[w][lane * V + v];
+      }
+      __syncthreads();
+    }
+    if (!in || (wide && warp != 0)) continue;
+    const int i = row / p.G, h = d.z * p.G + row - i * p.G;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    __nv_bfloat16* to = p.o + (((long long)d.y * p.Nq + i) * p.Hq + h) * D + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(to + v) = pack_bf16x2(a[v] * inv, a[v + 1] * inv);
+    if (lane == 0 && p.lse)
+      p.lse[((long long)d.y * p.Hq + h) * p.Nq + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   }
-  if (lane == 0) {
-    sm_m[warp] = m;
-    sm_l[warp] = l;
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) sm_o[warp][lane * V + v] = acc[v];
-  __syncthreads();
-  if (warp != 0) return;
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < 4; ++w) M = fmaxf(M, sm_m[w]);
-  float a[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) a[v] = 0.f;
-  for (int w = 0; w < 4; ++w) {
-    const float e = (M == -INFINITY) ? (sm_l[w] == 0.f ? 0.f : 1.f) : exp2f(sm_m[w] - M);
-    L += e * sm_l[w];
-#pragma unroll
-    for (int v = 0; v < V; ++v) a[v] += e * sm_o[w][lane * V + v];
-  }
-  const float inv = L == 0.f ? 0.f : 1.f / L;  // a row that sees nothing: o = 0, lse = -inf
-#pragma unroll
-  for (int v = 0; v < V; ++v) p.o[qrow * D + lane * V + v] = __float2bfloat16_rn(a[v] * inv);
-  if (lane == 0 && p.lse)
-    p.lse[((long long)b * p.Hq + h) * p.Nq + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 }  // namespace fa
