@@ -170,7 +170,10 @@ def _bf16(what: str, *ts) -> None:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream or None
+        if not torch.cuda.is_initialized():
+            return torch.cuda.current_stream().cuda_stream or None
+        # the raw handle of torch.cuda.current_stream(), without building the Stream object
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
@@ -576,28 +579,38 @@ def forward_fp8(q8, k8, v8, descale_q, descale_k, descale_v, causal=False, scale
 
 
 # ------------------------------------------------------------------ rotary positions, 8-bit cache, pages
-class _device_of:
-    """Makes the device of the tensors current for one call (launches go to the current device)
-    and refuses tensors of different devices."""
+def _home(first, *others) -> int:
+    """Index of the device that holds every tensor (launches go to the current device, so the
+    calls below make it current)."""
+    idx = first.get_device()
+    if idx < 0:
+        raise ValueError(f"expected a CUDA tensor, got one on {first.device}")
+    for t in others:
+        if t is not None and t.get_device() != idx:
+            raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
+    return idx
 
-    def __init__(self, first, *others):
-        import torch
-        if not first.is_cuda:
-            raise ValueError(f"expected a CUDA tensor, got one on {first.device}")
-        for t in others:
-            if t is not None and t.device != first.device:
-                raise ValueError(f"tensors on different devices: {first.device} and {t.device}")
-        self._guard = None
-        if first.device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(first.device)
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
+def _at(idx: int, call):
+    import torch
+    if idx == torch._C._cuda_getDevice():
+        return call()
+    with torch.cuda.device(idx):
+        return call()
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+
+def _dense(**tensors) -> None:
+    for what, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{what}: expected a contiguous tensor, got strides {tuple(t.stride())} for shape "
+                             f"{tuple(t.shape)}")
+
+
+def _is_i32(**tensors) -> None:
+    import torch
+    for what, t in tensors.items():
+        if t is not None and t.dtype != torch.int32:
+            raise ValueError(f"{what}: expected an int32 tensor, got {t.dtype}")
 
 
 _ROPE_SCALINGS = {"none": FA_ROPE_NONE, "linear": FA_ROPE_LINEAR, "ntk": FA_ROPE_NTK, "bands": FA_ROPE_BANDS}
@@ -617,7 +630,9 @@ def rope_frequencies(rot_dim, theta=10000.0, scaling="none", factor=1.0, origina
 def _row_stride(t, what: str) -> int:
     """Elements between rows of [..., H, d] whose heads are dense and whose rows are evenly
     spaced (a dense tensor, or q or k inside a packed [..., 3, H, d] one)."""
-    H, d = t.shape[-2], t.shape[-1]
+    H, d = t.shape[-2:]
+    if t.is_contiguous():
+        return H * d
     ok = t.stride(-1) == 1 and (H == 1 or t.stride(-2) == d)
     step = H * d
     lead = [(n, s) for n, s in zip(t.shape[:-2], t.stride()[:-2]) if n != 1]
@@ -633,38 +648,49 @@ def _row_stride(t, what: str) -> int:
 
 def _rope(q, k, freqs, positions, interleaved, amplitude, q_out, k_out, stream, backward):
     import torch
-    dtypes = {torch.bfloat16: FA_BF16, torch.float32: FA_F32}
-    _require("q", q.dim() in (3, 4) and q.dtype in dtypes,
-             f"bf16 or fp32 [B, N, Hq, d] or [total, Hq, d], got {q.dtype} {tuple(q.shape)}")
-    Hq, d = q.shape[-2], q.shape[-1]
+    if q.dim() not in (3, 4) or q.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"q: expected bf16 or fp32 [B, N, Hq, d] or [total, Hq, d], got {q.dtype} {tuple(q.shape)}")
+    shape = q.shape
+    Hq, d = shape[-2:]
     rows = q.numel() // max(1, Hq * d)
-    period = q.shape[-3]
     if k is not None:
-        _require("k", k.dtype == q.dtype and k.dim() == q.dim() and k.shape[:-2] == q.shape[:-2] and k.shape[-1] == d,
-                 f"{q.dtype} {tuple(q.shape[:-2])} + (Hkv, {d}) like q, got {k.dtype} {tuple(k.shape)}")
+        if k.dtype != q.dtype or k.dim() != q.dim() or k.shape[:-2] != shape[:-2] or k.shape[-1] != d:
+            raise ValueError(f"k: expected {q.dtype} {tuple(shape[:-2])} + (Hkv, {d}) like q, got {k.dtype} "
+                             f"{tuple(k.shape)}")
     elif k_out is not None:
         raise ValueError("k_out given without k")
-    _require("freqs", freqs.dim() == 1 and freqs.dtype == torch.float64 and 0 < 2 * freqs.numel() <= d,
-             f"float64 [rot_dim / 2] with rot_dim <= {d}, got {freqs.dtype} {tuple(freqs.shape)}")
-    if positions is not None:
-        _require("positions", positions.numel() == rows and (positions.dim() == 1 or positions.shape == q.shape[:-2]),
-                 f"{tuple(q.shape[:-2])} or [{rows}], got shape {tuple(positions.shape)}")
-    _expect(q_out, q.shape, str(q.dtype), "q_out")
-    if k is not None:
-        _expect(k_out, k.shape, str(q.dtype), "k_out")
-    with _device_of(q, k, freqs, positions, q_out, k_out):
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    rot = 2 * freqs.numel()
+    if freqs.dim() != 1 or freqs.dtype != torch.float64 or not 0 < rot <= d:
+        raise ValueError(f"freqs: expected float64 [rot_dim / 2] with rot_dim <= {d}, got {freqs.dtype} "
+                         f"{tuple(freqs.shape)}")
+    if positions is not None and (positions.numel() != rows or
+                                  (positions.dim() != 1 and positions.shape != shape[:-2])):
+        raise ValueError(f"positions: expected {tuple(shape[:-2])} or [{rows}], got shape {tuple(positions.shape)}")
+    for t, like, what in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t is not None and (t.shape != like.shape or t.dtype != like.dtype):
+            raise ValueError(f"{what}: expected {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
+    idx = _home(q, k, freqs, positions, q_out, k_out)
+    _dense(freqs=freqs, positions=positions)
+    _is_i32(positions=positions)
+
+    def call():
+        yq = q_out if q_out is not None else torch.empty(shape, dtype=q.dtype, device=q.device)
+        yk = k_out
+        if yk is None and k is not None:
+            yk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
         if rows > 0:
-            pairs = [(q, "q"), (q_out, "q_out")] + ([(k, "k"), (k_out, "k_out")] if k is not None else [])
-            st = {w: _row_stride(t, w) for t, w in pairs}
-            fa_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
-                    None if k is None else k_out.data_ptr(), positions, freqs, rows, period, Hq,
-                    0 if k is None else k.shape[-2], d, 2 * freqs.numel(), interleaved, amplitude, backward,
-                    dtypes[q.dtype], st["q"], st.get("k", 0), st["q_out"], st.get("k_out", 0), stream)
-    return q_out, k_out
+            sq, syq, sk, syk = _row_stride(q, "q"), _row_stride(yq, "q_out"), 0, 0
+            if k is not None:
+                sk, syk = _row_stride(k, "k"), _row_stride(yk, "k_out")
+            st = load().fa_rope(q.data_ptr(), None if k is None else k.data_ptr(), yq.data_ptr(),
+                                None if k is None else yk.data_ptr(),
+                                None if positions is None else positions.data_ptr(), freqs.data_ptr(), rows, shape[-3],
+                                Hq, 0 if k is None else k.shape[-2], d, rot, 1 if interleaved else 0, amplitude,
+                                1 if backward else 0, FA_BF16 if q.dtype == torch.bfloat16 else FA_F32, sq, sk, syq,
+                                syk, _stream(stream))
+            _check(st, "fa_rope")
+        return yq, yk
+    return _at(idx, call)
 
 
 def rope(q, k, freqs, positions=None, interleaved=False, amplitude=1.0, q_out=None, k_out=None, stream=None):
@@ -683,38 +709,57 @@ def rope_backward(dq, dk, freqs, positions=None, interleaved=False, amplitude=1.
 
 def _cache8(k_pages, v_pages, k_scale, v_scale, block_table, seqlens):
     """Checks an e4m3 paged cache; returns (B, num_pages, page_size, max_pages, Hkv, d, scale_block)."""
-    _same("k_pages, v_pages", k_pages, v_pages)
-    _same("k_scale, v_scale", k_scale, v_scale)
-    _require("k_pages", k_pages.dim() == 4 and str(k_pages.dtype) in ("torch.float8_e4m3fn", "torch.uint8"),
-             f"e4m3 (or bytes) [num_pages, page_size, Hkv, d], got {k_pages.dtype} {tuple(k_pages.shape)}")
+    import torch
+    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.dim() != 4 or \
+            k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise ValueError(f"k_pages, v_pages: expected two e4m3 (or byte) [num_pages, page_size, Hkv, d], got "
+                         f"{k_pages.dtype} {tuple(k_pages.shape)} and {v_pages.dtype} {tuple(v_pages.shape)}")
     num_pages, page_size, Hkv, d = k_pages.shape
-    _require("k_scale", k_scale.dim() == 3 and k_scale.shape[0] == num_pages and k_scale.shape[1] == Hkv and
-             str(k_scale.dtype) == "torch.float32" and k_scale.shape[2] > 0 and page_size % k_scale.shape[2] == 0,
-             f"float32 [{num_pages}, {Hkv}, page_size / scale_block], got {k_scale.dtype} {tuple(k_scale.shape)}")
-    _require("block_table", block_table.dim() == 2, f"[B, max_pages], got {tuple(block_table.shape)}")
+    ks = k_scale.shape
+    if ks != v_scale.shape or len(ks) != 3 or ks[0] != num_pages or ks[1] != Hkv or ks[2] <= 0 or \
+            page_size % ks[2] != 0 or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise ValueError(f"k_scale, v_scale: expected two float32 [{num_pages}, {Hkv}, page_size / scale_block], got "
+                         f"{k_scale.dtype} {tuple(ks)} and {v_scale.dtype} {tuple(v_scale.shape)}")
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table: expected [B, max_pages], got {tuple(block_table.shape)}")
     B, maxp = block_table.shape
-    _lengths(seqlens, B, "seqlens")
-    return B, num_pages, page_size, maxp, Hkv, d, page_size // k_scale.shape[2]
+    if seqlens.dim() != 1 or seqlens.shape[0] != B:
+        raise ValueError(f"seqlens: expected {B} entries, got shape {tuple(seqlens.shape)}")
+    _is_i32(block_table=block_table, seqlens=seqlens)
+    _dense(k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
+           seqlens=seqlens)
+    return B, num_pages, page_size, maxp, Hkv, d, page_size // ks[2]
 
 
 def cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, cu_seqlens=None, stream=None):
     """Writes bf16 k, v [total, Hkv, d] into an e4m3 paged cache (pages [num_pages, page_size, Hkv,
     d], scales float32 [num_pages, Hkv, page_size / scale_block]), in place.  seqlens [B]: lengths
     with the new rows; cu_seqlens [B + 1]: the new rows of each sequence, or None: one each."""
-    _same("k, v", k, v)
-    _bf16("cache_append_fp8", k)
+    import torch
+    if k.shape != v.shape or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise ValueError(f"k, v: expected two bf16 tensors of one shape, got {k.dtype} {tuple(k.shape)} and {v.dtype} "
+                         f"{tuple(v.shape)}")
     B, P, ps, maxp, Hkv, d, sb = _cache8(k_pages, v_pages, k_scale, v_scale, block_table, seqlens)
-    _require("k", k.dim() == 3 and k.shape[1] == Hkv and k.shape[2] == d,
-             f"[total, Hkv={Hkv}, d={d}], got shape {tuple(k.shape)}")
+    if k.dim() != 3 or k.shape[1] != Hkv or k.shape[2] != d:
+        raise ValueError(f"k: expected [total, Hkv={Hkv}, d={d}], got shape {tuple(k.shape)}")
     total = k.shape[0]
     if cu_seqlens is None:
-        _require("k", total == B, f"one row for each of {B} sequences without cu_seqlens, got {total}")
-    else:
-        _require("cu_seqlens", cu_seqlens.dim() == 1 and cu_seqlens.numel() == B + 1,
-                 f"[B + 1 = {B + 1}] offsets, got shape {tuple(cu_seqlens.shape)}")
-    with _device_of(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, cu_seqlens):
-        fa_cache_append_fp8(k, v, cu_seqlens, block_table, seqlens, k_pages, v_pages, k_scale, v_scale, B, total, Hkv,
-                            P, ps, maxp, sb, d, stream)
+        if total != B:
+            raise ValueError(f"k: expected one row for each of {B} sequences without cu_seqlens, got {total}")
+    elif cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != B + 1:
+        raise ValueError(f"cu_seqlens: expected [B + 1 = {B + 1}] offsets, got shape {tuple(cu_seqlens.shape)}")
+    idx = _home(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, cu_seqlens)
+    _is_i32(cu_seqlens=cu_seqlens)
+    _dense(k=k, v=v, cu_seqlens=cu_seqlens)
+
+    def call():
+        _check(load().fa_cache_append_fp8(k.data_ptr(), v.data_ptr(),
+                                          None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                                          block_table.data_ptr(), seqlens.data_ptr(), k_pages.data_ptr(),
+                                          v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, total, Hkv, P,
+                                          ps, maxp, sb, d, _stream(stream)), "fa_cache_append_fp8")
+    if B > 0 and total > 0:
+        _at(idx, call)
 
 
 def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, scale=None, out=None, lse=None,
@@ -723,34 +768,54 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens
     cache_append_fp8): q [B, Hq, d] gives lse [B, Hq]; q [B, Nq, Hq, d] (the Nq newest tokens,
     causal among themselves) gives lse [B, Hq, Nq]."""
     import torch
-    _bf16("decode_paged_fp8", q)
+    if q.dtype != torch.bfloat16:
+        raise ValueError(f"decode_paged_fp8: expected bf16 tensors, got {q.dtype}")
     B, P, ps, maxp, Hkv, d, sb = _cache8(k_pages, v_pages, k_scale, v_scale, block_table, seqlens)
-    _require("q", q.dim() in (3, 4) and q.shape[0] == B and q.shape[-1] == d,
-             f"[B={B}, Hq, d={d}] or [B={B}, Nq, Hq, d={d}], got shape {tuple(q.shape)}")
-    Nq, Hq = (q.shape[1] if q.dim() == 4 else 1), q.shape[-2]
+    shape = q.shape
+    if q.dim() not in (3, 4) or shape[0] != B or shape[-1] != d:
+        raise ValueError(f"q: expected [B={B}, Hq, d={d}] or [B={B}, Nq, Hq, d={d}], got shape {tuple(shape)}")
+    Nq, Hq = (shape[1] if q.dim() == 4 else 1), shape[-2]
     _require("heads", Hkv > 0 and Hq % Hkv == 0, f"Hq ({Hq}) a multiple of Hkv ({Hkv})")
     lse_shape = (B, Hq) if q.dim() == 3 else (B, Hq, Nq)
     if scale is None:
         scale = d ** -0.5
-    _expect(out, q.shape, "torch.bfloat16", "out")
+    _expect(out, shape, "torch.bfloat16", "out")
     _expect(lse, lse_shape, "torch.float32", "lse")
-    with _device_of(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace):
-        if out is None:
-            out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+    idx = _home(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace)
+    _dense(q=q, out=out, lse=lse, workspace=workspace)
+
+    def call():
+        lib = load()
+        o = out if out is not None else torch.empty_like(q)
+        ml = lse if lse is not None else torch.empty(lse_shape, dtype=torch.float32, device=q.device)
         if workspace is None:
-            workspace = torch.empty(max(fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d), 1), dtype=torch.uint8,
-                                    device=q.device)
-        fa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, B, Nq, Hq, Hkv, P,
-                            ps, maxp, sb, d, scale, workspace, workspace.numel() * workspace.element_size(), stream)
-    return out, lse
+            nbytes = lib.fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d)
+            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        else:
+            ws, nbytes = workspace, workspace.numel() * workspace.element_size()
+        if B > 0 and Nq > 0 and Hq > 0:
+            _check(lib.fa_decode_paged_fp8(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+                                           v_scale.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
+                                           o.data_ptr(), ml.data_ptr(), B, Nq, Hq, Hkv, P, ps, maxp, sb, d, scale,
+                                           ws.data_ptr(), nbytes, _stream(stream)), "fa_decode_paged_fp8")
+        return o, ml
+    return _at(idx, call)
 
 
-def _paged_table(block_table, seqlens):
-    _require("block_table", block_table.dim() == 2, f"[B, max_pages], got {tuple(block_table.shape)}")
-    _lengths(seqlens, block_table.shape[0], "seqlens")
-    return block_table.shape
+def _paged_table(pools, block_table, seqlens, num_pages):
+    """Checks the table of a paged cache of any element type; returns (B, max_pages, num_pages)."""
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table: expected [B, max_pages], got {tuple(block_table.shape)}")
+    B, maxp = block_table.shape
+    if seqlens.dim() != 1 or seqlens.shape[0] != B:
+        raise ValueError(f"seqlens: expected {B} entries, got shape {tuple(seqlens.shape)}")
+    if num_pages is None:
+        if not len(pools):
+            raise ValueError("pools: expected at least one pool, or num_pages")
+        num_pages = pools[0].shape[0]
+    _is_i32(block_table=block_table, seqlens=seqlens)
+    _dense(block_table=block_table, seqlens=seqlens)
+    return B, maxp, num_pages
 
 
 def pages_fork(pools, block_table, seqlens, parent, page_size, num_pages=None, workspace=None, stream=None):
@@ -759,36 +824,40 @@ def pages_fork(pools, block_table, seqlens, parent, page_size, num_pages=None, w
     of tensors [num_pages, ...]).  Returns (block_table, seqlens, free_pages [num_pages], n_free
     [1]); see fa_pages_fork in include/fa.h."""
     import torch
-    B, maxp = _paged_table(block_table, seqlens)
-    _require("parent", parent.dim() == 1, f"[B_out], got shape {tuple(parent.shape)}")
-    if num_pages is None:
-        _require("pools", len(pools) > 0, "at least one pool, or num_pages")
-        num_pages = pools[0].shape[0]
-    R = parent.numel()
-    with _device_of(block_table, seqlens, parent, workspace, *pools):
-        new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=block_table.device)  # noqa: E731
-        table, lens, free, n_free = new(R, maxp), new(R), new(num_pages), new(1)
-        if workspace is None:
-            workspace = torch.empty(fa_pages_workspace_size(num_pages, R), dtype=torch.uint8,
-                                    device=block_table.device)
+    B, maxp, num_pages = _paged_table(pools, block_table, seqlens, num_pages)
+    if parent.dim() != 1:
+        raise ValueError(f"parent: expected [B_out], got shape {tuple(parent.shape)}")
+    R = parent.shape[0]
+    _is_i32(parent=parent)
+    _dense(parent=parent, workspace=workspace)
+
+    def call():
+        # one allocation for the four results
+        buf = torch.empty(R * (maxp + 1) + num_pages + 1, dtype=torch.int32, device=block_table.device)
+        table, lens, free, n_free = buf.split([R * maxp, R, num_pages, 1])
+        table = table.view(R, maxp)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(fa_pages_workspace_size(num_pages, R), dtype=torch.uint8, device=block_table.device)
         fa_pages_fork(pools, block_table, seqlens, parent, table, lens, free, n_free, B, R, num_pages, page_size, maxp,
-                      workspace, workspace.numel() * workspace.element_size(), stream)
-    return table, lens, free, n_free
+                      ws, ws.numel() * ws.element_size(), stream)
+        return table, lens, free, n_free
+    return _at(_home(block_table, seqlens, parent, workspace, *pools), call)
 
 
 def pages_compact(pools, block_table, seqlens, page_size, num_pages=None, workspace=None, stream=None):
     """Moves the pages in use to the front of every pool.  Returns (block_table, n_live [1])."""
     import torch
-    B, maxp = _paged_table(block_table, seqlens)
-    if num_pages is None:
-        _require("pools", len(pools) > 0, "at least one pool, or num_pages")
-        num_pages = pools[0].shape[0]
-    with _device_of(block_table, seqlens, workspace, *pools):
+    B, maxp, num_pages = _paged_table(pools, block_table, seqlens, num_pages)
+    _dense(workspace=workspace)
+
+    def call():
         table = torch.empty((B, maxp), dtype=torch.int32, device=block_table.device)
         n_live = torch.empty(1, dtype=torch.int32, device=block_table.device)
-        if workspace is None:
-            workspace = torch.empty(fa_pages_workspace_size(num_pages, 0), dtype=torch.uint8,
-                                    device=block_table.device)
-        fa_pages_compact(pools, block_table, seqlens, table, n_live, B, num_pages, page_size, maxp, workspace,
-                         workspace.numel() * workspace.element_size(), stream)
-    return table, n_live
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(fa_pages_workspace_size(num_pages), dtype=torch.uint8, device=block_table.device)
+        fa_pages_compact(pools, block_table, seqlens, table, n_live, B, num_pages, page_size, maxp, ws,
+                         ws.numel() * ws.element_size(), stream)
+        return table, n_live
+    return _at(_home(block_table, seqlens, workspace, *pools), call)

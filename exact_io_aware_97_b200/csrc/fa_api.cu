@@ -3,6 +3,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -204,6 +206,17 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 template <class K>
 cudaError_t set_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// set_smem, once for each device (a call on this path is a few microseconds altogether).
+template <class K>
+bool set_smem_once(K kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  if (done.load(std::memory_order_relaxed) >> dev & 1u) return true;
+  if (set_smem(kernel, bytes) != cudaSuccess) return false;
+  done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  return true;
 }
 
 template <int D, bool F32>
@@ -924,9 +937,24 @@ namespace {
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 template <typename T, int D>
-fa_status launch_rope(const RopeParams& prm, cudaStream_t st) {
-  const long long units = prm.rows * prm.chunks;
-  fa_rope_kernel<T, D><<<(unsigned)((units + 7) / 8), 256, 0, st>>>(prm);
+fa_status launch_rope(RopeParams prm, cudaStream_t st) {
+  constexpr int V = RopeVec<T>::N, heads_at_once = 32 / (D / (2 * V));
+  const int sms = sm_count_cached();
+  if (sms <= 0) return FA_ERR_CUDA;
+  // Runs of heads: one for each row when the rows alone fill the GPU, else as many as give
+  // each SM 32 warps, down to the heads that a warp covers at once.
+  const int nh = prm.heads[0] + prm.heads[1], groups = (nh + heads_at_once - 1) / heads_at_once;
+  const long long want = std::max(1ll, (sms * 32ll) / prm.rows);
+  const int per = (int)((groups + std::min<long long>(want, groups) - 1) / std::min<long long>(want, groups));
+  prm.per_chunk = per * heads_at_once;
+  prm.chunks = (nh + prm.per_chunk - 1) / prm.per_chunk;
+  const unsigned blocks = (unsigned)((prm.rows * prm.chunks + 7) / 8);
+  if (prm.interleaved)
+    fa_rope_vec_kernel<T, D, true><<<blocks, 256, 0, st>>>(prm);
+  else if (prm.rot / 2 % V == 0)
+    fa_rope_vec_kernel<T, D, false><<<blocks, 256, 0, st>>>(prm);
+  else
+    fa_rope_kernel<T, D><<<blocks, 256, 0, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -1002,8 +1030,6 @@ extern "C" fa_status fa_rope(const void* q, const void* k, void* q_out, void* k_
   prm.interleaved = interleaved ? 1 : 0;
   prm.backward = backward ? 1 : 0;
   prm.amplitude = amplitude;
-  prm.chunks = 1;
-  prm.per_chunk = Hq + Hk;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (dtype == FA_BF16)
     return d == 64 ? launch_rope<__nv_bfloat16, 64>(prm, st) : launch_rope<__nv_bfloat16, 128>(prm, st);
@@ -1067,7 +1093,8 @@ fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& pr
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return FA_ERR_CUDA;
   auto kern = fa_decode_fp8_kernel<D, MT, RG>;
-  if (set_smem(kern, C::kSmem) != cudaSuccess) return FA_ERR_CUDA;
+  static std::atomic<uint64_t> smem_set{0};  // a bit for each device
+  if (!set_smem_once(kern, C::kSmem, smem_set)) return FA_ERR_CUDA;
   const int ctas = dec8_ctas(prm.rows);
   kern<<<ctas, C::kThreads, C::kSmem, st>>>(maps[0], maps[1], prm);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;

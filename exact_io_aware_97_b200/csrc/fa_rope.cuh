@@ -82,4 +82,123 @@ __global__ void __launch_bounds__(256) fa_rope_kernel(const RopeParams p) {
   }
 }
 
+// Rows in 16-byte vectors.  A lane owns one slot of a head, two vectors: columns that turn
+// together (half layout), neighbours (interleaved), or neighbours that are copied.  The lanes of
+// a warp cover 32 / slots heads at a time; each computes a share of its slot's sines and cosines
+// and gets the rest from the lanes of the same slot.  Half layout: rot / 2 is a multiple of the
+// vector (else fa_rope_kernel).
+template <typename T>
+struct RopeVec;
+template <>
+struct RopeVec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = (&w.x)[j];
+      x[2 * j] = __uint_as_float(u << 16);
+      x[2 * j + 1] = __uint_as_float(u & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
+  }
+};
+template <>
+struct RopeVec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = __uint_as_float((&w.x)[j]);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  }
+};
+
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(256) fa_rope_vec_kernel(const RopeParams p) {
+  using X = RopeVec<T>;
+  constexpr int V = X::N, kSlots = D / (2 * V), kHeads = 32 / kSlots, kShare = V / kHeads, kUnroll = 4;
+  const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, slot = lane % kSlots, sub = lane / kSlots;
+  const long long row = unit / p.chunks;
+  if (row >= p.rows) return;
+  const int h0 = (int)(unit - row * p.chunks) * p.per_chunk;
+  const int nh = p.heads[0] + p.heads[1], h1 = min(h0 + p.per_chunk, nh);
+  const int np = p.rot / 2;
+  const double pos = rope_pos(p, row);
+  float2 own[kShare];
+#pragma unroll
+  for (int j = 0; j < kShare; ++j) {
+    const int i = slot * V + sub * kShare + j;
+    own[j] = i < np ? rope_cs(p, i, pos) : make_float2(1.f, 0.f);
+  }
+  float c[V], s[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int from = (j / kShare) * kSlots + slot;
+    c[j] = __shfl_sync(0xffffffffu, own[j % kShare].x, from);
+    s[j] = __shfl_sync(0xffffffffu, own[j % kShare].y, from);
+  }
+  const int pairs = min(max(np - slot * V, 0), V);  // of this slot that turn
+  int ca, cb;                                       // first columns of the two vectors
+  if (INTER) {
+    ca = slot * 2 * V;
+    cb = ca + V;
+  } else {
+    ca = pairs ? slot * V : p.rot + (slot - np / V) * 2 * V;
+    cb = pairs ? ca + np : ca + V;
+  }
+  const T* const xq = static_cast<const T*>(p.x[0]) + row * p.xs[0];
+  const T* const xk = static_cast<const T*>(p.x[1]) + row * p.xs[1] - (long long)p.heads[0] * D;
+  T* const yq = static_cast<T*>(p.y[0]) + row * p.ys[0];
+  T* const yk = static_cast<T*>(p.y[1]) + row * p.ys[1] - (long long)p.heads[0] * D;
+  for (int h = h0 + sub; h < h1; h += kHeads * kUnroll) {
+    uint4 wa[kUnroll], wb[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int hh = h + u * kHeads;
+      if (hh < h1) {
+        const T* x = (hh < p.heads[0] ? xq : xk) + (long long)hh * D;
+        wa[u] = *reinterpret_cast<const uint4*>(x + ca);
+        wb[u] = *reinterpret_cast<const uint4*>(x + cb);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int hh = h + u * kHeads;
+      if (hh >= h1) continue;
+      if (pairs) {
+        float a[V], b[V];
+        X::unpack(wa[u], a);
+        X::unpack(wb[u], b);
+        if (INTER) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            float& x0 = 2 * j < V ? a[(2 * j) % V] : b[(2 * j) % V];
+            float& x1 = 2 * j < V ? a[(2 * j + 1) % V] : b[(2 * j + 1) % V];
+            const float y0 = fmaf(x0, c[j], -x1 * s[j]), y1 = fmaf(x1, c[j], x0 * s[j]);
+            x0 = j < pairs ? y0 : x0;
+            x1 = j < pairs ? y1 : x1;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float x0 = a[j], x1 = b[j];
+            a[j] = fmaf(x0, c[j], -x1 * s[j]);
+            b[j] = fmaf(x1, c[j], x0 * s[j]);
+          }
+        }
+        wa[u] = X::pack(a);
+        wb[u] = X::pack(b);
+      }
+      T* y = (hh < p.heads[0] ? yq : yk) + (long long)hh * D;
+      *reinterpret_cast<uint4*>(y + ca) = wa[u];
+      *reinterpret_cast<uint4*>(y + cb) = wb[u];
+    }
+  }
+}
+
 }  // namespace fa

@@ -161,7 +161,7 @@ def test_binding_refuses_before_the_library(lib):
     bt, sl = torch.zeros(3, 2, dtype=i32), torch.zeros(3, dtype=i32)
     x = torch.zeros(3, 2, 64, dtype=bf)
     good = [x, x, kp, kp, ks, ks, bt, sl]
-    for at, bad, match in ((0, x[:2], "k, v"), (2, kp.float(), "pages"), (3, kp[:5], "pages"), (4, ks[:, :1], "scale"),
+    for at, bad, match in ((0, x[:2], "k, v"), (2, kp.float(), "pages"), (3, kp[:5], "pages"), (4, ks[:, :1], "k_scale"),
                            (7, sl[:2], "seqlens"), (6, bt[0], "block_table"), (0, x.float(), "k, v")):
         args = list(good)
         args[at] = bad
