@@ -1066,7 +1066,7 @@ fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
   const int wpu = (1 << prm.sb_shift) / 16;
   const int warps = std::max(8, wpu), upc = warps / wpu;
   const dim3 grid((unsigned)(prm.cu ? (prm.total >> prm.sb_shift) + 2ll * prm.B : prm.B),
-                  (unsigned)((prm.Hkv + upc - 1) / upc), 2);
+                  (unsigned)((prm.Hkv + upc - 1) / upc));
   fa_cache_append_kernel<D><<<grid, warps * 32, 0, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

@@ -61,20 +61,31 @@ __device__ __forceinline__ int append_find(const int32_t* cu, int B, int sb_shif
   return lo;
 }
 
+// Two e4m3 pairs of x / s, with x / s as x * inv where s is a power of two (the same value, since
+// the product is exact up to its one rounding) and by division otherwise.
+__device__ __forceinline__ uint32_t quant4(uint32_t w0, uint32_t w1, float s, float inv, bool pow2) {
+  float x[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xFFFF0000u), __uint_as_float(w1 << 16),
+                __uint_as_float(w1 & 0xFFFF0000u)};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = pow2 ? x[j] * inv : __fdiv_rn(x[j], s);
+  return e4m3x4(x[0], x[1], x[2], x[3]);
+}
+
+// A CTA takes one block of rows for blockDim.x / 32 / (scale_block / 16) heads, K and V.  The rows
+// are loaded as soon as the sequence is known, before the page and the scale.
 template <int D>
 __global__ void __launch_bounds__(512) fa_cache_append_kernel(const AppendParams p) {
-  __shared__ uint32_t sm_max[16];
-  constexpr int kLanes = D / 8;           // lanes of one row (8 values each)
-  constexpr int kRows = 32 / kLanes;      // rows of one pass of a warp
+  __shared__ uint32_t sm_max[2][16];
+  constexpr int kLanes = D / 8;       // lanes of one row (8 values each)
+  constexpr int kRows = 32 / kLanes;  // rows of one pass of a warp
   constexpr int kPass = 16 / kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wpu = (1 << p.sb_shift) >> 4;  // warps of a unit
-  const int upc = (blockDim.x >> 5) / wpu;  // units (heads) of a CTA
+  const int wpu = (1 << p.sb_shift) >> 4;   // warps of a unit
+  const int upc = (blockDim.x >> 5) / wpu;  // heads of a CTA
   const int head = blockIdx.y * upc + warp / wpu;
-  const int which = blockIdx.z;
   const int ps = 1 << p.page_shift;
 
-  if (p.cu && blockIdx.x == 0 && blockIdx.y == 0 && which == 0) {
+  if (p.cu && blockIdx.x == 0 && blockIdx.y == 0) {
     bool bad = threadIdx.x == 0 && (__ldg(p.cu) < 0 || __ldg(p.cu + p.B) > p.total);
     for (int b = threadIdx.x; b < p.B; b += blockDim.x) bad |= __ldg(p.cu + b) > __ldg(p.cu + b + 1);
     if (bad) atomicOr(&g_error_word, kErrBadSeqlens);
@@ -91,74 +102,84 @@ __global__ void __launch_bounds__(512) fa_cache_append_kernel(const AppendParams
     if (threadIdx.x == 0) atomicOr(&g_error_word, kErrBadSeqlens);
     return;
   }
-  const int old = len - n;                                    // rows before the new ones
+  const int old = len - n;                                     // rows before the new ones
   const int blk0 = ((old >> p.sb_shift) + idx) << p.sb_shift;  // first position of the block
   if (blk0 >= len) return;
   const int page = __ldg(p.block_table + (long long)b * p.max_pages + (blk0 >> p.page_shift));
+  const bool alive = head < p.Hkv;
+  const int r0 = (warp % wpu) * 16 + lane / kLanes, col = (lane % kLanes) * 8;
+  const long long pitch = (long long)p.Hkv * D;
+
+  uint4 x[2][kPass];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const __nv_bfloat16* src = p.src[w] + (long long)(start + blk0 - old) * pitch + head * D + col;
+#pragma unroll
+    for (int k = 0; k < kPass; ++k) {
+      const int r = r0 + k * kRows, pos = blk0 + r;
+      x[w][k] = make_uint4(0u, 0u, 0u, 0u);
+      if (alive && pos >= old && pos < len) x[w][k] = __ldcs(reinterpret_cast<const uint4*>(src + r * pitch));
+    }
+  }
   if (page < 0 || page >= p.num_pages) {
     if (threadIdx.x == 0) atomicOr(&g_error_word, kErrBadPage);
     return;
   }
-  const bool alive = head < p.Hkv;
   const int row_in_page = blk0 & (ps - 1);
-  float* scale = p.scales[which] + ((long long)page * p.Hkv + head) * (ps >> p.sb_shift) + (row_in_page >> p.sb_shift);
-  const float s_old = (alive && blk0 < old) ? *scale : 0.f;
-  const int r0 = (warp % wpu) * 16 + lane / kLanes, col = (lane % kLanes) * 8;
-  const __nv_bfloat16* src = p.src[which] + ((long long)(start + blk0 - old) * p.Hkv + head) * D + col;
-  uint8_t* dst = p.pages[which] + (((long long)page * ps + row_in_page) * p.Hkv + head) * D + col;
-
-  uint4 x[kPass];
-  uint32_t top = 0;  // largest |x| as bits: the order of non-negative floats, NaN and inf on top
-#pragma unroll
-  for (int k = 0; k < kPass; ++k) {
-    const int r = r0 + k * kRows, pos = blk0 + r;
-    x[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (alive && pos >= old && pos < len)
-      x[k] = *reinterpret_cast<const uint4*>(src + (long long)r * p.Hkv * D);
+  const long long at_scale =
+      ((long long)page * p.Hkv + head) * (ps >> p.sb_shift) + (row_in_page >> p.sb_shift);
+  float s_old[2] = {0.f, 0.f};
+  if (alive && blk0 < old) {
+    s_old[0] = p.scales[0][at_scale];
+    s_old[1] = p.scales[1][at_scale];
   }
+  // largest |x| as bits: the order of non-negative floats, NaN and infinity on top
+  uint32_t top[2];
 #pragma unroll
-  for (int k = 0; k < kPass; ++k)
+  for (int w = 0; w < 2; ++w) {
+    uint32_t t2 = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t w = (&x[k].x)[j];
-      top = max(top, max((w << 16) & 0x7FFF0000u, w & 0x7FFF0000u));
-    }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) sm_max[warp] = top;
-  __syncthreads();
-  for (int w = warp / wpu * wpu; w < (warp / wpu + 1) * wpu; ++w) top = max(top, sm_max[w]);
+    for (int k = 0; k < kPass; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) t2 = __vmaxu2(t2, (&x[w][k].x)[j] & 0x7FFF7FFFu);
+    top[w] = __reduce_max_sync(0xffffffffu, max(t2 << 16, t2 & 0xFFFF0000u));
+    if (wpu > 1 && lane == 0) sm_max[w][warp] = top[w];
+  }
+  __syncthreads();  // (also: every warp has read the old scale before one writes the new one)
   if (!alive) return;
-  const float nan = __uint_as_float(0x7FC00000u);
-  float s = top >= 0x7F800000u ? nan : top == 0u ? 0.f : pow2_scale(__uint_as_float(top));
-  s = (s != s || s_old != s_old) ? nan : fmaxf(s, s_old);
-  const float ratio = s > s_old ? s_old / s : 1.f;
+  const int first = warp / wpu * wpu;
 #pragma unroll
-  for (int k = 0; k < kPass; ++k) {
-    const int r = r0 + k * kRows, pos = blk0 + r;
-    uint8_t* to = dst + (long long)r * p.Hkv * D;
-    if (pos >= old && pos < len) {
-      uint32_t out[2];
+  for (int w = 0; w < 2; ++w) {
+    if (wpu > 1)
+      for (int k = 0; k < wpu; ++k) top[w] = max(top[w], sm_max[w][first + k]);
+    const float nan = __uint_as_float(0x7FC00000u);
+    float s = top[w] >= 0x7F800000u ? nan : top[w] == 0u ? 0.f : pow2_scale(__uint_as_float(top[w]));
+    s = (s != s || s_old[w] != s_old[w]) ? nan : fmaxf(s, s_old[w]);
+    const float ratio = s > s_old[w] ? s_old[w] / s : 1.f, inv = __fdiv_rn(1.f, s);
+    const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0u && s > 0.f;
+    uint8_t* dst = p.pages[w] + ((long long)page * ps + row_in_page) * pitch + head * D + col;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t w0 = (&x[k].x)[2 * j], w1 = (&x[k].x)[2 * j + 1];
-        const float a = __uint_as_float(w0 << 16), bq = __uint_as_float(w0 & 0xFFFF0000u);
-        const float c = __uint_as_float(w1 << 16), dq = __uint_as_float(w1 & 0xFFFF0000u);
-        out[j] = s == 0.f ? 0u : e4m3x4(__fdiv_rn(a, s), __fdiv_rn(bq, s), __fdiv_rn(c, s), __fdiv_rn(dq, s));
+    for (int k = 0; k < kPass; ++k) {
+      const int r = r0 + k * kRows, pos = blk0 + r;
+      uint2* to = reinterpret_cast<uint2*>(dst + r * pitch);
+      if (pos >= old && pos < len) {
+        const uint4 v = x[w][k];
+        *to = s == 0.f ? make_uint2(0u, 0u)
+                       : make_uint2(quant4(v.x, v.y, s, inv, pow2), quant4(v.z, v.w, s, inv, pow2));
+      } else if (pos < old && ratio != 1.f) {
+        const uint2 v = *to;
+        uint32_t out[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t c = j ? v.y : v.x;
+          out[j] = e4m3x4(e4m3_value(c & 255u) * ratio, e4m3_value((c >> 8) & 255u) * ratio,
+                          e4m3_value((c >> 16) & 255u) * ratio, e4m3_value(c >> 24) * ratio);
+        }
+        *to = make_uint2(out[0], out[1]);
       }
-      *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
-    } else if (pos < old && ratio != 1.f) {
-      const uint2 w = *reinterpret_cast<const uint2*>(to);
-      uint32_t out[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t v = j ? w.y : w.x;
-        out[j] = e4m3x4(e4m3_value(v & 255u) * ratio, e4m3_value((v >> 8) & 255u) * ratio,
-                        e4m3_value((v >> 16) & 255u) * ratio, e4m3_value(v >> 24) * ratio);
-      }
-      *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
     }
+    if (warp == first && lane == 0) p.scales[w][at_scale] = s;
   }
-  if (warp % wpu == 0 && lane == 0) *scale = s;
 }
 
 }  // namespace fa
