@@ -48,26 +48,30 @@ struct Dec8Params {
   float tau;  // scale * log2(e)
 };
 
-constexpr int kDec8Keys = 64;  // cache rows of a chunk
+constexpr int kDec8Keys = 128;  // cache rows of a chunk
+constexpr float kDec8Low = -3e38f;  // running maxima before anything was seen
 
 template <int D, int MT, int RG>
 struct Dec8Cfg {
   static constexpr int kRows = 16 * MT * RG;       // R: query rows of a unit
-  static constexpr int kWarps = 4 * RG;            // compute warps: 4 row slices of the chunk x RG row groups
+  static constexpr int kWarps = 4 * RG;            // compute warps: 4 slices of 32 rows of the chunk x RG row groups
+  // 16-row tiles of the cache that a warp takes at once: two where the registers allow it, for
+  // twice the independent chains (one at a time: 128 us instead of KTWO us on the 32K decode)
+  static constexpr int kTiles = MT == 1 ? 2 : 1;
   // A warp with two row tiles needs more registers than its share: the producer then is a warp of
   // a warpgroup of its own, which gives registers up (threads x registers of a CTA: MT = 2, RG = 1:
   // 128 x 208 + 128 x 40 <= 256 x 128; RG = 2: 256 x 224 + 128 x 40 <= 384 x 168).
   static constexpr bool kSplitRegs = MT > 1;
   static constexpr int kComputeRegs = RG == 1 ? 208 : 224;
   static constexpr int kThreads = (kWarps + (kSplitRegs ? 4 : 1)) * 32;
-  static constexpr int kCtas = RG == 1 ? 2 : 1;    // per SM
-  static constexpr int kHalf = kDec8Keys * D;      // bytes of K (or V) of a chunk
-  static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = (D == 128) ? (RG == 1 ? 4 : 7) : (RG == 1 ? 6 : 12);
-  static constexpr int kMergeFloats = RG * (4 * 16 * D + 2 * 4 * 16);
+  static constexpr int kCtas = RG == 1 ? 2 : 1;     // per SM
+  static constexpr int kHalf = kDec8Keys * D;       // bytes of K (or V) of a chunk
+  static constexpr int kStage = 2 * kHalf;          // also the size of the merge of 16 rows of 4 slices
+  static_assert(kStage >= 4 * 16 * D * 4, "a stage holds the sums of 16 query rows of the four slices");
+  static constexpr int kStages = (D == 128 ? 3 : 6) * (RG == 1 ? 1 : 2);
   static constexpr int kQBytes = MT == 1 ? 0 : RG * MT * (D / 16) * 32 * 16;
-  static constexpr int kSmem = 1024 + kStages * kStage + kMergeFloats * 4 + kQBytes + kStages * 8 * 4 +
-                               2 * kStages * 8 + 64;
+  static constexpr int kSmem = 1024 + kStages * kStage + kQBytes + RG * 4 * 16 * 8 + kStages * 16 * 4 +
+                               2 * kStages * 8;
 };
 
 // Position in the sequence of chunks: sequence b, offset u among its units' chunks.
@@ -133,6 +137,52 @@ __device__ __forceinline__ uint32_t dec8_offset(int row, int unit) {
   return row * D + ((D == 128 ? unit ^ (row & 7) : unit ^ ((row >> 1) & 3)) << 4);
 }
 
+// V codes of a warp's rows [j0, j0 + n) that some query does not see (`vs`: the first of them in
+// shared memory).  Rows past the end may hold anything and become zeros.  Returns whether a row
+// before the end holds a NaN code.
+template <int D>
+__device__ __noinline__ bool dec8_clean_v(uint8_t* vs, int j0, int n, int len) {
+  constexpr int KS = D / 16;
+  uint32_t nan = 0;
+  for (int u = threadIdx.x & 31; u < n * KS; u += 32) {
+    uint4* at = reinterpret_cast<uint4*>(vs + u * 16);
+    if (j0 + u / KS >= len) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+      const uint4 w = *at;
+      nan |= ((w.x & 0x7F7F7F7Fu) + 0x01010101u) | ((w.y & 0x7F7F7F7Fu) + 0x01010101u) |
+             ((w.z & 0x7F7F7F7Fu) + 0x01010101u) | ((w.w & 0x7F7F7F7Fu) + 0x01010101u);
+    }
+  }
+  __syncwarp();
+  return __any_sync(0xffffffffu, (nan & 0x80808080u) != 0u);
+}
+
+// A NaN code may be for some queries only, but 0 * NaN would reach the others: it goes straight
+// into the sums of those that see its row, and becomes a zero code.  Rare, so a call.
+template <int D, int MT>
+__device__ __noinline__ void dec8_nan_v(uint8_t* vs, int j0, int n, int len, const int (&limit)[MT][2],
+                                        float (&acc)[MT][D / 8][4]) {
+  const int lane = threadIdx.x & 31, tig = lane & 3;
+  for (int r = 0; r < n && j0 + r < len; ++r)
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(vs + dec8_offset<D>(r, k) + 4 * tig);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)  // columns 16 k + 4 tig + x
+        if (((w >> (8 * x)) & 0x7Fu) == 0x7Fu)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hr = 0; hr < 2; ++hr)
+              if (j0 + r < limit[mt][hr]) acc[mt][2 * k + (x & 1)][2 * hr + (x >> 1)] = __uint_as_float(0x7FC00000u);
+    }
+  __syncwarp();
+  for (int u = lane; u < n * D; u += 32)
+    if ((vs[u] & 0x7Fu) == 0x7Fu) vs[u] = 0;
+  __syncwarp();
+}
+
 template <int D, int MT, int RG>
 __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, RG>::kCtas)
     fa_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -143,17 +193,17 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* merge = reinterpret_cast<float*>(ring + NS * C::kStage);
-  uint4* sm_q = reinterpret_cast<uint4*>(merge + C::kMergeFloats);
-  float* sm_scale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(sm_q) + C::kQBytes);  // [NS][2][4]
-  uint64_t* full = reinterpret_cast<uint64_t*>(sm_scale + NS * 8);
+  uint4* sm_q = reinterpret_cast<uint4*>(ring + NS * C::kStage);
+  float2* sm_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(sm_q) + C::kQBytes);  // [RG][4][16]
+  float* sm_scale = reinterpret_cast<float*>(sm_ml + RG * 4 * 16);                           // [NS][2][8]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm_scale + NS * 16);
   uint64_t* empty = full + NS;
   __shared__ long long sm_scan[C::kThreads / 32], sm_u;
   __shared__ int sm_b;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      mbar_init(full + s, 1 + 8);  // the producer's expect_tx, and eight lanes' scales
+      mbar_init(full + s, 1 + 16);  // the producer's expect_tx, and sixteen lanes' scales
       mbar_init(empty + s, C::kWarps);
     }
     fence_barrier_init();
@@ -207,22 +257,23 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
   if (warp >= C::kWarps) {
     // ------------------------------------------------------------ producer
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    // Lanes 0..7: (K or V, 16-row slice of the chunk).  Each fetches the scale of its slice, and
+    // Lanes 0..15: (K or V, 16-row slice of the chunk).  Each fetches the scale of its slice, and
     // the lanes at the head of a page's rows its box of them; slices past the end are left out.
     // The table entry of the next chunk is loaded while this one is issued.
-    if (warp == C::kWarps && lane < 8) {
-      const int which = lane >> 2, sub = lane & 3;
+    if (warp == C::kWarps && lane < 16) {
+      const int which = lane >> 3, sub = lane & 7;
       const uint64_t pol = policy_evict_first();
       const int psm = (1 << p.page_shift) - 1, nb_shift = p.page_shift - p.sb_shift;
       const bool leads = (16 * sub) % p.box == 0;
-      long long g = 0;  // stages issued
+      int slot = 0;
+      uint32_t phase = 1;  // of the slot's release: the first round finds it free
       bool ok = true;
       while (ok && walk.next(p, seg)) {
         const int kvh = seg.unit / p.tiles;
         const int32_t* bt = p.block_table + (long long)seg.b * p.max_pages;
         int tok = seg.c0 * kDec8Keys + 16 * sub;
         int page_next = tok < seg.len ? __ldg(bt + (tok >> p.page_shift)) : 0;
-        for (int c = seg.c0; c < seg.c1; ++c, ++g, tok += kDec8Keys) {
+        for (int c = seg.c0; c < seg.c1; ++c, tok += kDec8Keys) {
           int page = page_next;
           const bool here = tok < seg.len;
           if (c + 1 < seg.c1 && tok + kDec8Keys < seg.len) page_next = __ldg(bt + ((tok + kDec8Keys) >> p.page_shift));
@@ -230,30 +281,30 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
             atomicOr(&g_error_word, kErrBadPage);
             page = 0;
           }
-          const int slot = (int)(g % NS);
-          if (g >= NS && !mbar_wait(empty + slot, (uint32_t)((g / NS) - 1) & 1u)) ok = false;
-          ok = __all_sync(0xffu, ok);
+          ok = __all_sync(0xffffu, mbar_wait(empty + slot, phase));
           if (!ok) break;
           uint8_t* st = ring + slot * C::kStage;
           if (lane == 0) {
             const int rows = min(kDec8Keys, (seg.len - c * kDec8Keys + p.box - 1) / p.box * p.box);
             mbar_arrive_expect_tx(full + slot, 2 * rows * D);
           }
-          __syncwarp(0xffu);
+          __syncwarp(0xffffu);
           const int r = tok & psm;
           if (here) {
             if (leads)
               tma_load_3d_hint(st + which * C::kHalf + 16 * sub * D, which ? &tmV : &tmK, 0, kvh,
                                (page << p.page_shift) + r, full + slot, pol);
             const float* src = p.scales[which] + (((long long)page * p.Hkv + kvh) << nb_shift) + (r >> p.sb_shift);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sm_scale + slot * 8 + lane)),
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sm_scale + slot * 16 + lane)),
                          "l"(src)
                          : "memory");
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + slot))
                          : "memory");
           } else {
+            sm_scale[slot * 16 + lane] = 0.f;  // a tile past the end may share a warp's step with one before it
             mbar_arrive(full + slot);
           }
+          if (++slot == NS) slot = 0, phase ^= 1u;
         }
       }
     }
@@ -262,10 +313,14 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
 
   // -------------------------------------------------------------- compute warps
   if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kComputeRegs));
-  const int slice = warp & 3, rg = warp >> 2;  // 16-row slice of the chunk, row group of the tile
+  constexpr int KT = C::kTiles;
+  const int slice = warp & 3, rg = warp >> 2;  // 32-row slice of the chunk, row group of the tile
   const int g = lane >> 2, tig = lane & 3;
-  const int mi = lane >> 3, rr = lane & 7;
-  long long stage = 0;
+  // ldmatrix addresses of this lane within a tile: row (lane & 7) + 8 * ((lane >> 3) & 1), unit
+  // lane >> 4 of a pair of units; the swizzle makes the pair 2 k an exclusive or with 2 k.
+  const uint32_t ld_off = dec8_offset<D>((lane & 7) + (lane & 8), lane >> 4);
+  int slot = 0;
+  uint32_t phase = 0;
   bool ok = true;
 
   // sequences without rows: o = 0, lse = -inf
@@ -330,235 +385,259 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
     const bool idle = row0 >= p.rows;  // a row group without rows
 
     float acc[MT][D / 8][4];
-    float m_r[MT][2], l_r[MT][2], w_r[MT][2];
+    float m_r[MT][2], l_r[MT][2], w_r[MT][2];  // running maxima of t and of t + log2(sv); sum of p
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) acc[mt][n][0] = acc[mt][n][1] = acc[mt][n][2] = acc[mt][n][3] = 0.f;
 #pragma unroll
       for (int hr = 0; hr < 2; ++hr) {
-        m_r[mt][hr] = w_r[mt][hr] = -INFINITY;
+        m_r[mt][hr] = w_r[mt][hr] = kDec8Low;
         l_r[mt][hr] = 0.f;
       }
     }
 
-    for (int c = seg.c0; c < seg.c1; ++c, ++stage) {
-      const int slot = (int)(stage % NS);
-      if (ok && !mbar_wait(full + slot, (uint32_t)(stage / NS) & 1u)) ok = false;
-      const int j0 = c * kDec8Keys + 16 * slice;
-      if (ok && !idle && j0 < seg.len) {
-        const uint32_t kb = smem_u32(ring + slot * C::kStage), vb = kb + C::kHalf;
-        const float sk = sm_scale[slot * 8 + slice];
-        const float lsv = __log2f(sm_scale[slot * 8 + 4 + slice]);
-        const bool ends = j0 + 16 > seg.len;         // rows past the end in this slice
-        const bool partly = j0 + 16 > first_limit;   // rows that some query does not see
-        if (ends) {
-          // Those rows may hold NaN codes: as zeros they add nothing.
-          for (int u = lane; u < 16 * KS; u += 32)
-            if (j0 + (u & 15) >= seg.len)
-              *reinterpret_cast<uint4*>(ring + slot * C::kStage + C::kHalf + (16 * slice + (u & 15)) * D +
-                                        (u >> 4) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          __syncwarp();
-        }
-        if (partly) {
-          // A NaN code of V may be for some queries only (0 * NaN would reach the others): put the
-          // NaN into the sums of those that see it and a zero in its place.
-          uint8_t* vs = ring + slot * C::kStage + C::kHalf;
-          uint32_t nan = 0;
-          for (int u = lane; u < 16 * D / 4; u += 32) {
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(vs + 16 * slice * D + 4 * u);
-            nan |= ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-          }
-          if (__any_sync(0xffffffffu, nan != 0)) {
-            const float bad = __uint_as_float(0x7FC00000u);
-            for (int r = 0; r < 16 && j0 + r < seg.len; ++r)
+    for (int c = seg.c0; c < seg.c1; ++c) {
+      if (ok && !mbar_wait(full + slot, phase)) ok = false;
+      uint8_t* const st = ring + slot * C::kStage;
+      const int jw = c * kDec8Keys + 32 * slice;
+      if (ok && !idle && jw < seg.len) {
 #pragma unroll
-              for (int k = 0; k < KS; ++k) {
-                const uint32_t w =
-                    *reinterpret_cast<const uint32_t*>(vs + dec8_offset<D>(16 * slice + r, k) + 4 * tig);
-                const uint32_t n4 = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                if (n4 == 0) continue;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                  for (int hr = 0; hr < 2; ++hr)
-                    if (j0 + r < limit[mt][hr])
-#pragma unroll
-                      for (int x = 0; x < 4; ++x)
-                        if ((n4 >> (8 * x + 7)) & 1u) acc[mt][2 * k + (x & 1)][2 * hr + (x >> 1)] = bad;
-              }
-            __syncwarp();
-            for (int u = lane; u < 16 * D; u += 32)
-              if ((vs[16 * slice * D + u] & 0x7Fu) == 0x7Fu) vs[16 * slice * D + u] = 0;
-            __syncwarp();
-          }
-        }
-        float sc[MT][2][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[mt][0][e] = sc[mt][1][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < KS; k += 2) {
-          // matrices: rows 0..7 and 8..15 of the slice, units k and k + 1
-          uint32_t w0, w1, w2, w3, b0, b1;
-          ldsm_x4(kb + dec8_offset<D>(16 * slice + (mi & 1) * 8 + rr, k + (mi >> 1)), w0, w1, w2, w3);
-          const uint32_t ws[4] = {w0, w1, w2, w3};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            e4m3x4_to_f16(ws[x], b0, b1);
+        for (int t0 = 0; t0 < 2; t0 += KT) {
+          const int j0 = jw + 16 * t0, r0 = 32 * slice + 16 * t0;  // first row: in the sequence, in the chunk
+          if (KT == 1 && j0 >= seg.len) break;
+          const bool partly = j0 + 16 * KT > first_limit;  // rows past the end, or that some query does not see
+          if (partly && dec8_clean_v<D>(st + C::kHalf + r0 * D, j0, 16 * KT, seg.len)) {
+            // copies, so that the sums themselves stay in registers
+            int lim[MT][2];
+            float sums[MT][D / 8][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              if constexpr (MT == 1) {
-                mma_f16_16816(sc[0][x & 1], qa[k + (x >> 1)], b0, b1);
-              } else {
-                const uint4 a4 = sm_q[((rg * MT + mt) * KS + k + (x >> 1)) * 32 + lane];
-                const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
-                mma_f16_16816(sc[mt][x & 1], a, b0, b1);
-              }
+              lim[mt][0] = limit[mt][0], lim[mt][1] = limit[mt][1];
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sums[mt][n][e] = acc[mt][n][e];
             }
+            dec8_nan_v<D, MT>(st + C::kHalf + r0 * D, j0, 16 * KT, seg.len, lim, sums);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mt][n][e] = sums[mt][n][e];
           }
-        }
-        uint32_t pa[MT][4];
-        bool moved = false;
-        float aw[MT][2];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int hr = 0; hr < 2; ++hr) {
-            const float f = fac[mt][hr] * sk;
-            float t[4] = {sc[mt][0][2 * hr] * f, sc[mt][0][2 * hr + 1] * f, sc[mt][1][2 * hr] * f,
-                          sc[mt][1][2 * hr + 1] * f};
-            if (partly) {
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (j0 + (x >> 1) * 8 + 2 * tig + (x & 1) >= limit[mt][hr]) t[x] = -INFINITY;
-            }
-            float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float m_new = fmaxf(m_r[mt][hr], mx), w_new = fmaxf(w_r[mt][hr], mx + lsv);
-            const float ms = m_new == -INFINITY ? 0.f : m_new;
-            const float wr = w_new == -INFINITY ? 0.f : w_new;
-            l_r[mt][hr] *= ex2_approx(m_r[mt][hr] - ms);
-            aw[mt][hr] = ex2_approx(w_r[mt][hr] - wr);
-            moved |= w_new != w_r[mt][hr];
-            m_r[mt][hr] = m_new;
-            w_r[mt][hr] = w_new;
-            const float wref = wr - lsv;
-            float w[4], sum = 0.f;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              sum += ex2_approx(t[x] - ms);
-              w[x] = ex2_approx(t[x] - wref);
-            }
-            if (partly) {  // a NaN scale is not for rows that the query does not see
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                if (j0 + (x >> 1) * 8 + 2 * tig + (x & 1) >= limit[mt][hr]) w[x] = 0.f;
-            }
-            l_r[mt][hr] += sum;
-            pa[mt][hr] = pack_f16x2(w[0], w[1]);
-            pa[mt][2 + hr] = pack_f16x2(w[2], w[3]);
-          }
-        if (__any_sync(0xffffffffu, moved)) {
+          const uint32_t kb = smem_u32(st + r0 * D) + ld_off, vb = kb + C::kHalf;
+          float sc[MT][2 * KT][4];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-              acc[mt][n][0] *= aw[mt][0];
-              acc[mt][n][1] *= aw[mt][0];
-              acc[mt][n][2] *= aw[mt][1];
-              acc[mt][n][3] *= aw[mt][1];
+            for (int n = 0; n < 2 * KT; ++n) sc[mt][n][0] = sc[mt][n][1] = sc[mt][n][2] = sc[mt][n][3] = 0.f;
+#pragma unroll
+          for (int k = 0; k < KS; k += 2)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+              // matrices: rows 0..7 and 8..15 of the tile, units k and k + 1
+              uint32_t w[4], b0, b1;
+              ldsm_x4((kb + kt * 16 * D) ^ (k << 4), w[0], w[1], w[2], w[3]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                e4m3x4_to_f16(w[x], b0, b1);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                  if constexpr (MT == 1) {
+                    mma_f16_16816(sc[0][2 * kt + (x & 1)], qa[k + (x >> 1)], b0, b1);
+                  } else {
+                    const uint4 a4 = sm_q[((rg * MT + mt) * KS + k + (x >> 1)) * 32 + lane];
+                    const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
+                    mma_f16_16816(sc[mt][2 * kt + (x & 1)], a, b0, b1);
+                  }
+                }
+              }
             }
-        }
+          float sk[KT], lsv[KT];
 #pragma unroll
-        for (int k = 0; k < KS; k += 2) {
-          // transposed: a register holds bytes (2 g, 2 g + 1) of the unit for rows 2 tig and 2 tig + 1
-          uint32_t w0, w1, w2, w3, e0, o0, e1, o1;
-          ldsm_x4_t(vb + dec8_offset<D>(16 * slice + (mi & 1) * 8 + rr, k + (mi >> 1)), w0, w1, w2, w3);
-          const uint32_t ws[4] = {w0, w1, w2, w3};
+          for (int kt = 0; kt < KT; ++kt) {
+            sk[kt] = sm_scale[slot * 16 + 2 * slice + t0 + kt];
+            lsv[kt] = __log2f(sm_scale[slot * 16 + 8 + 2 * slice + t0 + kt]);
+          }
+          // Scores to fp16 weights.  sc is scaled to t = sc * f inside the exponent (f >= 0).
+          uint32_t pa[MT][KT][4];
+          float mx[MT][2][KT], f[MT][2][KT];
+          bool moved = false;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            e4m3x4_to_f16(__byte_perm(ws[2 * x], 0u, 0x3120), e0, o0);
-            e4m3x4_to_f16(__byte_perm(ws[2 * x + 1], 0u, 0x3120), e1, o1);
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hr = 0; hr < 2; ++hr)
+#pragma unroll
+              for (int kt = 0; kt < KT; ++kt) {
+                float* s0 = &sc[mt][2 * kt][2 * hr];
+                float* s1 = &sc[mt][2 * kt + 1][2 * hr];
+                if (partly) {
+                  const int j = j0 + 16 * kt + 2 * tig, lim = limit[mt][hr];
+                  s0[0] = j < lim ? s0[0] : -INFINITY;
+                  s0[1] = j + 1 < lim ? s0[1] : -INFINITY;
+                  s1[0] = j + 8 < lim ? s1[0] : -INFINITY;
+                  s1[1] = j + 9 < lim ? s1[1] : -INFINITY;
+                }
+                float x = fmaxf(fmax3(s0[0], s0[1], s1[0]), s1[1]);
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                f[mt][hr][kt] = fac[mt][hr] * sk[kt];
+                x *= f[mt][hr][kt];
+                mx[mt][hr][kt] = x;
+                moved |= x > m_r[mt][hr] || x + lsv[kt] > w_r[mt][hr];
+              }
+          if (__any_sync(0xffffffffu, moved)) {
+            // some maximum rises: bring the sums to the new references (NaN never raises one)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              mma_f16_16816(acc[mt][2 * (k + x)], pa[mt], e0, e1);      // columns 16 (k + x) + 2 n
-              mma_f16_16816(acc[mt][2 * (k + x) + 1], pa[mt], o0, o1);  // and + 2 n + 1
+              float aw[2];
+#pragma unroll
+              for (int hr = 0; hr < 2; ++hr) {
+                float m = m_r[mt][hr], w = w_r[mt][hr];
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                  m = fmaxf(m, mx[mt][hr][kt]);
+                  w = fmaxf(w, mx[mt][hr][kt] + lsv[kt]);
+                }
+                l_r[mt][hr] *= ex2_approx(m_r[mt][hr] - m);
+                aw[hr] = ex2_approx(w_r[mt][hr] - w);
+                m_r[mt][hr] = m;
+                w_r[mt][hr] = w;
+              }
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                acc[mt][n][0] *= aw[0];
+                acc[mt][n][1] *= aw[0];
+                acc[mt][n][2] *= aw[1];
+                acc[mt][n][3] *= aw[1];
+              }
             }
           }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hr = 0; hr < 2; ++hr)
+#pragma unroll
+              for (int kt = 0; kt < KT; ++kt) {
+                // p = 2^(t - m); the weight is p times cw = sv 2^(m - w), at most 1 (the bound keeps
+                // 0 * cw at 0 where a scale dwarfs the ones that m came from)
+                const float ec = m_r[mt][hr] - w_r[mt][hr] + lsv[kt];
+                const float cw = ex2_approx(ec > 126.f ? 126.f : ec);  // NaN stays
+                const float ff = f[mt][hr][kt], m = m_r[mt][hr];
+                float p0 = ex2_approx(fmaf(sc[mt][2 * kt][2 * hr], ff, -m));
+                float p1 = ex2_approx(fmaf(sc[mt][2 * kt][2 * hr + 1], ff, -m));
+                float p2 = ex2_approx(fmaf(sc[mt][2 * kt + 1][2 * hr], ff, -m));
+                float p3 = ex2_approx(fmaf(sc[mt][2 * kt + 1][2 * hr + 1], ff, -m));
+                float w0 = p0 * cw, w1 = p1 * cw, w2 = p2 * cw, w3 = p3 * cw;
+                if (partly) {  // a zero or NaN scale says nothing about rows that are not seen
+                  const int j = j0 + 16 * kt + 2 * tig, lim = limit[mt][hr];
+                  if (j >= lim) p0 = w0 = 0.f;
+                  if (j + 1 >= lim) p1 = w1 = 0.f;
+                  if (j + 8 >= lim) p2 = w2 = 0.f;
+                  if (j + 9 >= lim) p3 = w3 = 0.f;
+                }
+                l_r[mt][hr] += (p0 + p1) + (p2 + p3);
+                pa[mt][kt][hr] = pack_f16x2(w0, w1);
+                pa[mt][kt][2 + hr] = pack_f16x2(w2, w3);
+              }
+#pragma unroll
+          for (int k = 0; k < KS; k += 2)
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+              // transposed: a register holds bytes (2 g, 2 g + 1) of the unit for rows 2 tig and 2 tig + 1
+              uint32_t w[4], e0, o0, e1, o1;
+              ldsm_x4_t((vb + kt * 16 * D) ^ (k << 4), w[0], w[1], w[2], w[3]);
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                e4m3x4_to_f16(__byte_perm(w[2 * x], 0u, 0x3120), e0, o0);
+                e4m3x4_to_f16(__byte_perm(w[2 * x + 1], 0u, 0x3120), e1, o1);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                  mma_f16_16816(acc[mt][2 * (k + x)], pa[mt][kt], e0, e1);      // columns 16 (k + x) + 2 n
+                  mma_f16_16816(acc[mt][2 * (k + x) + 1], pa[mt][kt], o0, o1);  // and + 2 n + 1
+                }
+              }
+            }
         }
       }
+      if (c + 1 == seg.c1) break;  // the last slot is kept for the merge
       // The slot is refilled by TMA (the async proxy) once every warp has arrived; the fence
       // orders this warp's generic-proxy reads and writes of it before that.
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(empty + slot);
+      if (++slot == NS) slot = 0, phase ^= 1u;
     }
 
-    // Merge the four slices of each row group, 16 rows at a time, and write them out.
-    float* mg_o = merge + rg * (4 * 16 * D + 2 * 4 * 16);
-    float* mg_m = mg_o + 4 * 16 * D;
-    float* mg_l = mg_m + 4 * 16;
+    // Merge the four slices of each row group through the last slot, 16 rows at a time, and write
+    // them out.
     const bool whole = seg.c0 == 0 && seg.c1 == seg.chunks;
     const int part = 2 * blockIdx.x + (seg.c0 == 0 ? 1 : 0);
+    float* const mg = reinterpret_cast<float*>(ring + slot * C::kStage);
+    float2* const ml = sm_ml + rg * 64;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int hr = 0; hr < 2; ++hr) {
-        float l = l_r[mt][hr];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const float m = m_r[mt][hr];
-        // weights so far are relative to 2^w_r: relative to 2^m from here on
-        const float e = w_r[mt][hr] == -INFINITY ? 0.f : ex2_approx(w_r[mt][hr] - m);
-        if (tig == 0) {
-          mg_m[slice * 16 + g + 8 * hr] = m;
-          mg_l[slice * 16 + g + 8 * hr] = l;
+      for (int turn = 0; turn < RG; ++turn) {  // the slot holds one row group's sums
+        asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
+        if (turn == rg) {
+#pragma unroll
+          for (int hr = 0; hr < 2; ++hr) {
+            float l = l_r[mt][hr];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            // weights so far are relative to 2^w_r: relative to 2^m from here on
+            const float e = ex2_approx(w_r[mt][hr] - m_r[mt][hr]);
+            if (tig == 0) ml[slice * 16 + g + 8 * hr] = make_float2(m_r[mt][hr], l);
+            float* to = mg + (slice * 16 + g + 8 * hr) * D + 4 * tig;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+              *reinterpret_cast<float4*>(to + 16 * k) =
+                  make_float4(acc[mt][2 * k][2 * hr] * e, acc[mt][2 * k + 1][2 * hr] * e,
+                              acc[mt][2 * k][2 * hr + 1] * e, acc[mt][2 * k + 1][2 * hr + 1] * e);
+          }
         }
-        float* to = mg_o + (slice * 16 + g + 8 * hr) * D + 4 * tig;
+        asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
+        const int row_at = tile * R + (turn * MT + mt) * 16;  // of the rows now in the slot
+        for (int idx = threadIdx.x; idx < 16 * (D / 4); idx += C::kWarps * 32) {
+          const int r = idx / (D / 4), col = 4 * (idx - r * (D / 4));
+          const int row = row_at + r;
+          if (row >= p.rows) break;
+          const float2* from = sm_ml + turn * 64 + r;
+          const float M = fmaxf(fmaxf(from[0].x, from[16].x), fmaxf(from[32].x, from[48].x));
+          float L = 0.f;
+          float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-          *reinterpret_cast<float4*>(to + 16 * k) =
-              make_float4(acc[mt][2 * k][2 * hr] * e, acc[mt][2 * k + 1][2 * hr] * e,
-                          acc[mt][2 * k][2 * hr + 1] * e, acc[mt][2 * k + 1][2 * hr + 1] * e);
+          for (int w = 0; w < 4; ++w) {
+            const float e = ex2_approx(from[w * 16].x - M);
+            L += e * from[w * 16].y;
+            const float4 x = *reinterpret_cast<const float4*>(mg + (w * 16 + r) * D + col);
+            A.x += e * x.x;
+            A.y += e * x.y;
+            A.z += e * x.z;
+            A.w += e * x.w;
+          }
+          if (whole) {
+            const int i = row / p.G, h = kvh * p.G + row - i * p.G;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            *reinterpret_cast<uint2*>(p.o + (((long long)seg.b * p.Nq + i) * p.Hq + h) * D + col) =
+                make_uint2(pack_bf16x2(A.x * inv, A.y * inv), pack_bf16x2(A.z * inv, A.w * inv));
+            if (col == 0 && p.lse)
+              p.lse[((long long)seg.b * p.Hq + h) * p.Nq + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+          } else {
+            const long long at = (long long)part * R + row - tile * R;
+            *reinterpret_cast<float4*>(p.ws_acc + at * D + col) = A;
+            if (col == 0) p.ws_ml[at] = make_float2(M, L);
+          }
+        }
       }
-      asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
-      for (int idx = threadIdx.x & 127; idx < 16 * (D / 4); idx += 128) {
-        const int r = idx / (D / 4), col = 4 * (idx - r * (D / 4));
-        const int row = row0 + 16 * mt + r;
-        if (row >= p.rows) break;
-        float M = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) M = fmaxf(M, mg_m[w * 16 + r]);
-        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float mw = mg_m[w * 16 + r];
-          const float e = mw == -INFINITY ? 0.f : ex2_approx(mw - M);  // 0 * NaN stays NaN
-          L += e * mg_l[w * 16 + r];
-          const float4 x = *reinterpret_cast<const float4*>(mg_o + (w * 16 + r) * D + col);
-          A.x += e * x.x;
-          A.y += e * x.y;
-          A.z += e * x.z;
-          A.w += e * x.w;
-        }
-        if (whole) {
-          const int i = row / p.G, h = kvh * p.G + row - i * p.G;
-          const float inv = L == 0.f ? 0.f : 1.f / L;
-          *reinterpret_cast<uint2*>(p.o + (((long long)seg.b * p.Nq + i) * p.Hq + h) * D + col) =
-              make_uint2(pack_bf16x2(A.x * inv, A.y * inv), pack_bf16x2(A.z * inv, A.w * inv));
-          if (col == 0 && p.lse)
-            p.lse[((long long)seg.b * p.Hq + h) * p.Nq + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-        } else {
-          const long long slot = (long long)part * R + rg * 16 * MT + 16 * mt + r;
-          *reinterpret_cast<float4*>(p.ws_acc + slot * D + col) = A;
-          if (col == 0) p.ws_ml[slot] = make_float2(M, L);
-        }
-      }
-      asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
-    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + slot);
+    if (++slot == NS) slot = 0, phase ^= 1u;
+    if constexpr (MT > 1) asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");  // sm_q is free
     if (!whole && seg.c0 == 0 && threadIdx.x == 0) {
       // the parts after this one: the CTAs whose shares begin before the unit ends
       const long long stop = end + (seg.chunks - seg.c1);
@@ -583,7 +662,7 @@ __global__ void __launch_bounds__(128) fa_decode_fp8_combine_kernel(const Dec8Pa
   for (int k = 0; k < (wide ? 4 : 1); ++k) {
     const int r = blockIdx.y * 4 + (wide ? k : warp), row = d.w * R + r;
     const bool in = row < p.rows;
-    float M = -INFINITY, L = 0.f, a[V];
+    float M = kDec8Low, L = 0.f, a[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) a[v] = 0.f;
     if (in) {
@@ -601,8 +680,7 @@ __global__ void __launch_bounds__(128) fa_decode_fp8_combine_kernel(const Dec8Pa
           y[0] = f.x, y[1] = f.y;
         }
         const float m_new = fmaxf(M, ml.x);
-        const float ms = m_new == -INFINITY ? 0.f : m_new;
-        const float e0 = ex2_approx(M - ms), e1 = ex2_approx(ml.x - ms);
+        const float e0 = ex2_approx(M - m_new), e1 = ex2_approx(ml.x - m_new);
         L = L * e0 + ml.y * e1;
 #pragma unroll
         for (int v = 0; v < V; ++v) a[v] = a[v] * e0 + y[v] * e1;
@@ -621,9 +699,8 @@ __global__ void __launch_bounds__(128) fa_decode_fp8_combine_kernel(const Dec8Pa
       L = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) a[v] = 0.f;
-      const float ms = M == -INFINITY ? 0.f : M;
       for (int w = 0; w < 4; ++w) {
-        const float e = ex2_approx(sm_m[w] - ms);
+        const float e = ex2_approx(sm_m[w] - M);
         L += e * sm_l[w];
 #pragma unroll
         for (int v = 0; v < V; ++v) a[v] += e * sm_o[w][lane * V + v];

@@ -318,8 +318,8 @@ FA_EXPORT fa_status fa_cache_append_fp8(const void* k, const void* v, const int3
  * q [B, Nq, Hq, d] bf16: the Nq newest tokens of each sequence, whose K and V rows are in the
  * cache already; o likewise; lse [B, Hq, Nq] fp32 (may be NULL).  Query i of sequence b sees
  * cache rows j <= seqlens[b] - Nq + i (every row for Nq = 1); a query that sees no row gets o = 0
- * and lse = -inf.  Cache, scales, block_table and seqlens as in fa_cache_append_fp8 (any fp32
- * scales); lengths below 0 count as 0, larger ones than max_pages_per_seq * page_size as that.
+ * and lse = -inf.  Cache, scales, block_table and seqlens as in fa_cache_append_fp8 (fp32
+ * scales, none negative); lengths below 0 count as 0, larger ones than max_pages_per_seq * page_size as that.
  * Rows past a sequence's end may hold anything.  An entry of the table outside [0, num_pages) is
  * read as page 0 and recorded (FA_ERR_INVALID_ARG from fa_last_device_error).
  * The stored values are exact in the products; P times the V scale is rounded to fp16 with its
