@@ -1077,6 +1077,9 @@ int dec8_ctas(int rows) {
   return (sms > 0 ? sms : 148) * (rows <= 32 ? 2 : 1);
 }
 int dec8_tile(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// K/V heads of a unit, as a shift: one where the query rows fill more than a tile (the products,
+// not the loads, take the time then, and one head's queries are all that shared memory holds).
+int dec8_heads(int rows, int Hkv) { return rows > 16 ? 0 : Hkv % 4 == 0 ? 2 : Hkv % 2 == 0 ? 1 : 0; }
 
 template <int D, int MT, int RG>
 fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& prm, cudaStream_t st) {
@@ -1084,9 +1087,9 @@ fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& pr
   CUtensorMap maps[2];
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return FA_ERR_CUDA;
-  const cuuint64_t dims[3] = {D, (cuuint64_t)prm.Hkv, (cuuint64_t)prm.num_pages << prm.page_shift};
-  const cuuint64_t strides[2] = {D, (cuuint64_t)prm.Hkv * D};
-  const cuuint32_t box[3] = {D, 1, (cuuint32_t)prm.box}, estr[3] = {1, 1, 1};
+  const cuuint64_t dims[3] = {D, (cuuint64_t)prm.num_pages << prm.page_shift, (cuuint64_t)prm.Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)prm.Hkv * D, D};
+  const cuuint32_t box[3] = {D, (cuuint32_t)prm.box, 1u << prm.hs}, estr[3] = {1, 1, 1};
   for (int w = 0; w < 2; ++w)
     if (enc(&maps[w], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w ? vp : kp), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
@@ -1098,8 +1101,23 @@ fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& pr
   const int ctas = dec8_ctas(prm.rows);
   kern<<<ctas, C::kThreads, C::kSmem, st>>>(maps[0], maps[1], prm);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  fa_decode_fp8_combine_kernel<D, C::kRows><<<dim3(ctas, (std::min(prm.rows, C::kRows) + 3) / 4), 128, 0, st>>>(prm);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  // No unit can be cut where the longest sequence that the table holds is short.
+  if ((prm.cap - 1 >> (7 - prm.hs)) + 1 <= kDec8Whole) return FA_OK;
+  // The merge starts on the SMs that the last CTAs leave and waits there for their results.
+  const int items = std::min(prm.rows, C::kRows) << prm.hs, gx = prm.by_unit ? prm.B * prm.units : ctas;
+  const bool wide = (int64_t)gx * items <= 8ll * ctas;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(gx, wide ? items : (items + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t err = wide ? cudaLaunchKernelEx(&cfg, fa_decode_fp8_combine_kernel<D, C::kRows, true>, prm)
+                               : cudaLaunchKernelEx(&cfg, fa_decode_fp8_combine_kernel<D, C::kRows, false>, prm);
+  return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1143,7 +1161,8 @@ extern "C" size_t fa_decode_paged_fp8_workspace_size(int B, int Nq, int Hq, int 
   const int64_t rows = (int64_t)Nq * (Hq / Hkv);
   const int tile = rows > 32 ? 64 : dec8_tile((int)rows);
   const size_t ctas = (size_t)dec8_ctas(tile);
-  return align_up(2 * ctas * tile * d * 4, 256) + align_up(2 * ctas * tile * 8, 256) + align_up(ctas * 16, 256);
+  const size_t slots = (2 * ctas * tile) << dec8_heads(tile, Hkv);
+  return align_up(slots * d * 4, 256) + align_up(slots * 8, 256) + align_up(ctas * 16, 256);
 }
 
 extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
@@ -1185,13 +1204,21 @@ extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, con
   prm.rows = (int)rows;
   const int tile = dec8_tile(prm.rows);
   prm.tiles = (prm.rows + tile - 1) / tile;
-  prm.box = std::min(page_size, kDec8Keys);
+  prm.hs = dec8_heads(prm.rows, Hkv);
+  prm.box = std::min(page_size, kDec8Keys >> prm.hs);
   const size_t ctas = (size_t)dec8_ctas(prm.rows);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   prm.ws_acc = reinterpret_cast<float*>(ws);
-  ws += align_up(2 * ctas * tile * d * 4, 256);
+  const size_t slots = (2 * ctas * tile) << prm.hs;
+  ws += align_up(slots * d * 4, 256);
   prm.ws_ml = reinterpret_cast<float2*>(ws);
-  prm.ws_desc = reinterpret_cast<int4*>(ws + align_up(2 * ctas * tile * 8, 256));
+  prm.ws_desc = reinterpret_cast<int4*>(ws + align_up(slots * 8, 256));
+  prm.cap = (int)((int64_t)max_pages_per_seq * page_size);
+  const int64_t units = (int64_t)(Hkv >> prm.hs) * prm.tiles;
+  // positions among all chunks are 32-bit in the kernel
+  if (B * units * (((prm.cap - 1) >> (7 - prm.hs)) + 1) >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  prm.units = (int)units;
+  prm.by_unit = B * units <= (int64_t)ctas;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (d == 64)
     return tile == 16   ? launch_decode_fp8<64, 1, 1>(k_pages, v_pages, prm, st)

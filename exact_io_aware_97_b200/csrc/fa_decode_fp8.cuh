@@ -10,7 +10,10 @@
 // stream is kept up is the work per byte, twice that of a bf16 cache.
 //
 // Partition.  The Nq * G query rows of one K/V head form tiles of R rows; a unit is (sequence,
-// K/V head, tile) and is cut into chunks of 64 cache rows.  All units' chunks, one after the
+// group of K/V heads, tile) and is cut into chunks of cache rows.  A group is four heads (two, one)
+// where that divides Hkv and a tile has 16 rows: a chunk then reads 4 d bytes side by side from
+// each cache row instead of d (streaming alone, d = 128: KSTREAM1 us for one head at a time, KSTREAM4
+// for four).  All units' chunks, one after the
 // other, are dealt to the CTAs of one wave in equal contiguous shares, whatever the lengths, so
 // every CTA streams the same number of bytes.  A CTA writes the output of units that lie in its
 // share whole; of at most two others (its first and its last) it writes partial sums, which
@@ -40,15 +43,20 @@ struct Dec8Params {
   const int32_t* seqlens;
   __nv_bfloat16* o;
   float* lse;      // [B, Hq, Nq] or null
-  float* ws_acc;   // [2 * CTAs][R][D]
-  float2* ws_ml;   // [2 * CTAs][R]: m (base 2), l
-  int4* ws_desc;   // [CTAs]: the unit whose first part is this CTA's last segment (see combine)
+  float* ws_acc;   // [2 * CTAs][2^hs][R][D]
+  float2* ws_ml;   // [2 * CTAs][2^hs][R]: m (base 2), l
+  int4* ws_desc;   // [units or CTAs]: the units to merge (see combine)
+  int by_unit;     // ws_desc is by unit
   int B, Nq, Hq, Hkv, G, rows, tiles;  // rows = Nq * G, tiles = ceil(rows / R)
   int num_pages, page_shift, sb_shift, max_pages, box;
+  int cap;    // rows that the table holds of a sequence
+  int units;  // of a sequence: groups of K/V heads * tiles
+  int hs;     // a unit covers 2^hs K/V heads, a chunk 128 >> hs cache rows of them
   float tau;  // scale * log2(e)
 };
 
-constexpr int kDec8Keys = 128;  // cache rows of a chunk
+constexpr int kDec8Keys = 128;  // cache rows of a chunk, counted over its K/V heads
+constexpr int kDec8Whole = 4;   // units of at most this many chunks are not cut
 constexpr float kDec8Low = -3e38f;  // running maxima before anything was seen
 
 template <int D, int MT, int RG>
@@ -77,30 +85,31 @@ struct Dec8Cfg {
 // Position in the sequence of chunks: sequence b, offset u among its units' chunks.
 struct Dec8Seg {
   int b, len, chunks;  // sequence, its length and chunks per unit
-  int unit;            // K/V head * tiles + tile
+  int unit;            // group of K/V heads * tiles + tile
   int c0, c1;          // chunks [c0, c1)
 };
 
+__device__ __forceinline__ int dec8_len(const Dec8Params& p, int b) { return min(max(__ldg(p.seqlens + b), 0), p.cap); }
+
+// The number of all chunks is under 2^31 (the host sees to that), so positions are ints.
 struct Dec8Walk {
-  long long left, u;
-  int b;
+  int left, u, b;
   __device__ __forceinline__ bool next(const Dec8Params& p, Dec8Seg& s) {
     if (left <= 0) return false;
     int len;
     for (;; ++b) {  // left > 0: some sequence from b on holds rows
-      const long long cap = (long long)p.max_pages << p.page_shift;
-      len = (int)min((long long)max(__ldg(p.seqlens + b), 0), cap);
+      len = dec8_len(p, b);
       if (len > 0) break;
     }
     s.b = b;
     s.len = len;
-    s.chunks = (len + kDec8Keys - 1) / kDec8Keys;
-    s.unit = (int)(u / s.chunks);
-    s.c0 = (int)(u - (long long)s.unit * s.chunks);
-    s.c1 = (int)min((long long)s.chunks, s.c0 + left);
+    s.chunks = (len - 1 >> 7 - p.hs) + 1;
+    s.unit = (unsigned)u / (unsigned)s.chunks;
+    s.c0 = u - s.unit * s.chunks;
+    s.c1 = min(s.chunks, s.c0 + left);
     left -= s.c1 - s.c0;
     u += s.c1 - s.c0;
-    if (u == (long long)s.chunks * p.Hkv * p.tiles) {
+    if (u == s.chunks * p.units) {
       ++b;
       u = 0;
     }
@@ -137,12 +146,12 @@ __device__ __forceinline__ uint32_t dec8_offset(int row, int unit) {
   return row * D + ((D == 128 ? unit ^ (row & 7) : unit ^ ((row >> 1) & 3)) << 4);
 }
 
-// V codes of a warp's rows [j0, j0 + n) that some query does not see (`vs`: the first of them in
+// V codes of a tile's rows [j0, j0 + 16) that some query does not see (`vs`: the first of them in
 // shared memory).  Rows past the end may hold anything and become zeros.  Returns whether a row
 // before the end holds a NaN code.
 template <int D>
-__device__ __noinline__ bool dec8_clean_v(uint8_t* vs, int j0, int n, int len) {
-  constexpr int KS = D / 16;
+__device__ __noinline__ bool dec8_clean_v(uint8_t* vs, int j0, int len) {
+  constexpr int KS = D / 16, n = 16;
   uint32_t nan = 0;
   for (int u = threadIdx.x & 31; u < n * KS; u += 32) {
     uint4* at = reinterpret_cast<uint4*>(vs + u * 16);
@@ -161,8 +170,9 @@ __device__ __noinline__ bool dec8_clean_v(uint8_t* vs, int j0, int n, int len) {
 // A NaN code may be for some queries only, but 0 * NaN would reach the others: it goes straight
 // into the sums of those that see its row, and becomes a zero code.  Rare, so a call.
 template <int D, int MT>
-__device__ __noinline__ void dec8_nan_v(uint8_t* vs, int j0, int n, int len, const int (&limit)[MT][2],
+__device__ __noinline__ void dec8_nan_v(uint8_t* vs, int j0, int len, const int (&limit)[MT][2],
                                         float (&acc)[MT][D / 8][4]) {
+  constexpr int n = 16;
   const int lane = threadIdx.x & 31, tig = lane & 3;
   for (int r = 0; r < n && j0 + r < len; ++r)
 #pragma unroll
@@ -198,8 +208,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
   float* sm_scale = reinterpret_cast<float*>(sm_ml + RG * 4 * 16);                           // [NS][2][8]
   uint64_t* full = reinterpret_cast<uint64_t*>(sm_scale + NS * 16);
   uint64_t* empty = full + NS;
-  __shared__ long long sm_scan[C::kThreads / 32], sm_u;
-  __shared__ int sm_b;
+  __shared__ int2 sm_scan[C::kThreads / 32];
+  __shared__ int sm_b, sm_u, sm_skip[2];
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -212,71 +222,100 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
   }
 
   // This CTA's share of all chunks: prefix sums over the sequences.
-  const long long cap = (long long)p.max_pages << p.page_shift;
   const int per = (p.B + C::kThreads - 1) / C::kThreads;
-  const int b_lo = min(threadIdx.x * per, p.B), b_hi = min(b_lo + per, p.B);
-  auto chunks_of = [&](int b) {
-    return (int)((min((long long)max(__ldg(p.seqlens + b), 0), cap) + kDec8Keys - 1) / kDec8Keys);
-  };
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += chunks_of(b);
-  long long incl = mine;
+  const int b_lo = min((int)threadIdx.x * per, p.B), b_hi = min(b_lo + per, p.B);
+  auto chunks_of = [&](int b) { return dec8_len(p, b) + (kDec8Keys >> p.hs) - 1 >> (7 - p.hs); };
+  int mine = 0, most = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int n = chunks_of(b);
+    mine += n;
+    most = max(most, n);
+  }
+  int incl = mine;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+    const int y = __shfl_up_sync(0xffffffffu, incl, off);
     if (lane >= off) incl += y;
   }
-  if (lane == 31) sm_scan[warp] = incl;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) sm_scan[warp] = make_int2(incl, most);
   __syncthreads();
-  long long before = 0, all = 0;
+  int before = 0, all = 0;
+#pragma unroll
   for (int w = 0; w < C::kThreads / 32; ++w) {
-    before += w < warp ? sm_scan[w] : 0;
-    all += sm_scan[w];
+    before += w < warp ? sm_scan[w].x : 0;
+    all += sm_scan[w].x;
+    most = max(most, sm_scan[w].y);
   }
   before += incl - mine;
-  const long long HR = (long long)p.Hkv * p.tiles, T = all * HR;
-  const long long ctas = min((long long)gridDim.x, T);  // each of these has at least one chunk
-  const bool busy = blockIdx.x < ctas;
-  const long long begin = busy ? blockIdx.x * T / ctas : 0, end = busy ? (blockIdx.x + 1) * T / ctas : 0;
-  if (begin < end && before * HR <= begin && begin < (before + mine) * HR) {
-    long long at = before * HR;
-    int b = b_lo;
-    for (;; ++b) {
-      const long long n = chunks_of(b) * HR;
-      if (begin < at + n) break;
-      at += n;
-    }
-    sm_b = b;
-    sm_u = begin - at;
-  }
-  if (threadIdx.x == 0) p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  const int T = all * p.units, ctas = min((int)gridDim.x, T);  // each of these has at least one chunk
+  const bool busy = (int)blockIdx.x < ctas;
+  const int quot = busy ? T / ctas : 0, rest = T - quot * ctas;  // share x begins at x T / ctas, rounded down
+  int begin = busy ? blockIdx.x * quot + (int)blockIdx.x * rest / ctas : 0;
+  int end = busy ? (blockIdx.x + 1) * quot + ((int)blockIdx.x + 1) * rest / ctas : 0;
+  // Short sequences: shares begin and end at units (rounded up), nothing is left to merge.
+  const bool snap = most <= kDec8Whole;
+  if (threadIdx.x == 0) sm_skip[1] = 0;  // end == T: no thread finds it
   __syncthreads();
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const int x = which ? end : begin;
+    if (busy && before * p.units <= x && x < (before + mine) * p.units && (which == 0 || snap)) {
+      int at = before * p.units, b = b_lo, n;
+      for (;; ++b) {
+        n = chunks_of(b) * p.units;
+        if (x < at + n) break;
+        at += n;
+      }
+      int skip = 0;
+      if (snap) {
+        const int c = n / p.units, in = (x - at) % c;
+        skip = in ? c - in : 0;
+      }
+      sm_skip[which] = skip;
+      if (which == 0) {
+        const bool over = x - at + skip == n;  // on to the next sequence that has rows
+        sm_b = b + over;
+        sm_u = over ? 0 : x - at + skip;
+      }
+    }
+  }
+  __syncthreads();
+  if (busy) {
+    begin += sm_skip[0];
+    end += sm_skip[1];
+  }
+  if (threadIdx.x == 0 && !p.by_unit) p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   Dec8Walk walk{end - begin, begin < end ? sm_u : 0, begin < end ? sm_b : 0};
   Dec8Seg seg;
 
   if (warp >= C::kWarps) {
     // ------------------------------------------------------------ producer
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    // Lanes 0..15: (K or V, 16-row slice of the chunk).  Each fetches the scale of its slice, and
-    // the lanes at the head of a page's rows its box of them; slices past the end are left out.
+    // Lanes 0..15: (K or V, K/V head, 16-row tile of the chunk), in the order of the warps that take
+    // them.  Each fetches the scale of its tile, and the first head's lanes at the head of a page's
+    // rows the box of them, all heads at once; tiles past the end are left out.
     // The table entry of the next chunk is loaded while this one is issued.
     if (warp == C::kWarps && lane < 16) {
       const int which = lane >> 3, sub = lane & 7;
       const uint64_t pol = policy_evict_first();
       const int psm = (1 << p.page_shift) - 1, nb_shift = p.page_shift - p.sb_shift;
-      const bool leads = (16 * sub) % p.box == 0;
+      const int chunk = kDec8Keys >> p.hs;
+      const int headi = (sub >> 1) >> (2 - p.hs);
+      const int ro = 16 * (2 * ((sub >> 1) & ((4 >> p.hs) - 1)) + (sub & 1));  // first row in the chunk
+      const bool leads = headi == 0 && ro % p.box == 0;
       int slot = 0;
       uint32_t phase = 1;  // of the slot's release: the first round finds it free
       bool ok = true;
       while (ok && walk.next(p, seg)) {
-        const int kvh = seg.unit / p.tiles;
+        const int kvh0 = (seg.unit / p.tiles) << p.hs;
         const int32_t* bt = p.block_table + (long long)seg.b * p.max_pages;
-        int tok = seg.c0 * kDec8Keys + 16 * sub;
+        int tok = seg.c0 * chunk + ro;
         int page_next = tok < seg.len ? __ldg(bt + (tok >> p.page_shift)) : 0;
-        for (int c = seg.c0; c < seg.c1; ++c, tok += kDec8Keys) {
+        for (int c = seg.c0; c < seg.c1; ++c, tok += chunk) {
           int page = page_next;
           const bool here = tok < seg.len;
-          if (c + 1 < seg.c1 && tok + kDec8Keys < seg.len) page_next = __ldg(bt + ((tok + kDec8Keys) >> p.page_shift));
+          if (c + 1 < seg.c1 && tok + chunk < seg.len) page_next = __ldg(bt + ((tok + chunk) >> p.page_shift));
           if (page < 0 || page >= p.num_pages) {
             atomicOr(&g_error_word, kErrBadPage);
             page = 0;
@@ -285,16 +324,17 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
           if (!ok) break;
           uint8_t* st = ring + slot * C::kStage;
           if (lane == 0) {
-            const int rows = min(kDec8Keys, (seg.len - c * kDec8Keys + p.box - 1) / p.box * p.box);
-            mbar_arrive_expect_tx(full + slot, 2 * rows * D);
+            const int rows = min(chunk, (seg.len - c * chunk + p.box - 1) / p.box * p.box);
+            mbar_arrive_expect_tx(full + slot, 2 * (rows << p.hs) * D);
           }
           __syncwarp(0xffffu);
           const int r = tok & psm;
           if (here) {
             if (leads)
-              tma_load_3d_hint(st + which * C::kHalf + 16 * sub * D, which ? &tmV : &tmK, 0, kvh,
-                               (page << p.page_shift) + r, full + slot, pol);
-            const float* src = p.scales[which] + (((long long)page * p.Hkv + kvh) << nb_shift) + (r >> p.sb_shift);
+              tma_load_3d_hint(st + which * C::kHalf + (ro << p.hs) * D, which ? &tmV : &tmK, 0,
+                               (page << p.page_shift) + r, kvh0, full + slot, pol);
+            const float* src =
+                p.scales[which] + (((long long)page * p.Hkv + kvh0 + headi) << nb_shift) + (r >> p.sb_shift);
             asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sm_scale + slot * 16 + lane)),
                          "l"(src)
                          : "memory");
@@ -307,6 +347,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
           if (++slot == NS) slot = 0, phase ^= 1u;
         }
       }
+      // the merge may be launched once every CTA has its last loads under way
+      if (lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
     return;
   }
@@ -314,7 +356,15 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
   // -------------------------------------------------------------- compute warps
   if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kComputeRegs));
   constexpr int KT = C::kTiles;
-  const int slice = warp & 3, rg = warp >> 2;  // 32-row slice of the chunk, row group of the tile
+  const int w4 = warp & 3, rg = warp >> 2;  // (K/V head, 32-row slice of the chunk), row group of the tile
+  const int headi = w4 >> (2 - p.hs), slice = w4 & ((4 >> p.hs) - 1), chunk = kDec8Keys >> p.hs;
+  // where this warp's two tiles are in a chunk: boxes of p.box rows, each [heads][rows][D]
+  int toff[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int ro = 32 * slice + 16 * t, in = ro % p.box;
+    toff[t] = ((ro - in) << p.hs) * D + (headi * p.box + in) * D;
+  }
   const int g = lane >> 2, tig = lane & 3;
   // ldmatrix addresses of this lane within a tile: row (lane & 7) + 8 * ((lane >> 3) & 1), unit
   // lane >> 4 of a pair of units; the swizzle makes the pair 2 k an exclusive or with 2 k.
@@ -325,16 +375,19 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
 
   // sequences without rows: o = 0, lse = -inf
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (min((long long)__ldg(p.seqlens + b), cap) > 0) continue;
+    if (dec8_len(p, b) > 0) continue;
     const long long n = (long long)p.Nq * p.Hq;
     for (long long k = threadIdx.x; k < n * D / 8; k += C::kWarps * 32)
       reinterpret_cast<uint4*>(p.o)[(long long)b * (n * D / 8) + k] = make_uint4(0u, 0u, 0u, 0u);
     if (p.lse)
       for (long long k = threadIdx.x; k < n; k += C::kWarps * 32) p.lse[b * n + k] = -INFINITY;
+    if (p.by_unit)
+      for (int k = threadIdx.x; k < p.units; k += C::kWarps * 32) p.ws_desc[b * p.units + k] = make_int4(0, 0, 0, 0);
   }
 
   while (walk.next(p, seg)) {
-    const int kvh = seg.unit / p.tiles, tile = seg.unit - kvh * p.tiles;
+    const int group = seg.unit / p.tiles, tile = seg.unit - group * p.tiles;
+    const int kvh = (group << p.hs) + headi;
     const int row0 = tile * R + rg * 16 * MT;  // first query row of this warp
     // rows [16 mt + g + 8 hr]: query token and head, how many cache rows it sees, its factor
     int limit[MT][2];
@@ -373,7 +426,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
           if constexpr (MT == 1) {
             qa[k][hr] = lo;      // A fragment: row g + 8 hr, columns 16 k + 4 tig + 0, 1
             qa[k][2 + hr] = hi;  // and + 2, 3 (the order that ldmatrix gives the K bytes in)
-          } else if (slice == 0) {
+          } else if (w4 == 0) {  // MT > 1: one K/V head
             uint32_t* to = reinterpret_cast<uint32_t*>(sm_q + ((rg * MT + mt) * KS + k) * 32 + lane);
             to[hr] = lo;
             to[2 + hr] = hi;
@@ -400,34 +453,39 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
     for (int c = seg.c0; c < seg.c1; ++c) {
       if (ok && !mbar_wait(full + slot, phase)) ok = false;
       uint8_t* const st = ring + slot * C::kStage;
-      const int jw = c * kDec8Keys + 32 * slice;
+      const int jw = c * chunk + 32 * slice;
       if (ok && !idle && jw < seg.len) {
 #pragma unroll
         for (int t0 = 0; t0 < 2; t0 += KT) {
-          const int j0 = jw + 16 * t0, r0 = 32 * slice + 16 * t0;  // first row: in the sequence, in the chunk
+          const int j0 = jw + 16 * t0;
           if (KT == 1 && j0 >= seg.len) break;
           const bool partly = j0 + 16 * KT > first_limit;  // rows past the end, or that some query does not see
-          if (partly && dec8_clean_v<D>(st + C::kHalf + r0 * D, j0, 16 * KT, seg.len)) {
-            // copies, so that the sums themselves stay in registers
-            int lim[MT][2];
-            float sums[MT][D / 8][4];
+          if (partly) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              lim[mt][0] = limit[mt][0], lim[mt][1] = limit[mt][1];
+            for (int kt = 0; kt < KT; ++kt) {
+              uint8_t* const vs = st + C::kHalf + toff[t0 + kt];
+              if (!dec8_clean_v<D>(vs, j0 + 16 * kt, seg.len)) continue;
+              // copies, so that the sums themselves stay in registers
+              int lim[MT][2];
+              float sums[MT][D / 8][4];
 #pragma unroll
-              for (int n = 0; n < D / 8; ++n)
+              for (int mt = 0; mt < MT; ++mt) {
+                lim[mt][0] = limit[mt][0], lim[mt][1] = limit[mt][1];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sums[mt][n][e] = acc[mt][n][e];
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) sums[mt][n][e] = acc[mt][n][e];
+              }
+              dec8_nan_v<D, MT>(vs, j0 + 16 * kt, seg.len, lim, sums);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) acc[mt][n][e] = sums[mt][n][e];
             }
-            dec8_nan_v<D, MT>(st + C::kHalf + r0 * D, j0, 16 * KT, seg.len, lim, sums);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[mt][n][e] = sums[mt][n][e];
           }
-          const uint32_t kb = smem_u32(st + r0 * D) + ld_off, vb = kb + C::kHalf;
+          const uint32_t base = smem_u32(st) + ld_off;
           float sc[MT][2 * KT][4];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
@@ -439,7 +497,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
             for (int kt = 0; kt < KT; ++kt) {
               // matrices: rows 0..7 and 8..15 of the tile, units k and k + 1
               uint32_t w[4], b0, b1;
-              ldsm_x4((kb + kt * 16 * D) ^ (k << 4), w[0], w[1], w[2], w[3]);
+              ldsm_x4((base + toff[t0 + kt]) ^ (k << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
                 e4m3x4_to_f16(w[x], b0, b1);
@@ -458,8 +516,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
           float sk[KT], lsv[KT];
 #pragma unroll
           for (int kt = 0; kt < KT; ++kt) {
-            sk[kt] = sm_scale[slot * 16 + 2 * slice + t0 + kt];
-            lsv[kt] = __log2f(sm_scale[slot * 16 + 8 + 2 * slice + t0 + kt]);
+            sk[kt] = sm_scale[slot * 16 + 2 * w4 + t0 + kt];
+            lsv[kt] = __log2f(sm_scale[slot * 16 + 8 + 2 * w4 + t0 + kt]);
           }
           // Scores to fp16 weights.  sc is scaled to t = sc * f inside the exponent (f >= 0).
           uint32_t pa[MT][KT][4];
@@ -548,7 +606,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
             for (int kt = 0; kt < KT; ++kt) {
               // transposed: a register holds bytes (2 g, 2 g + 1) of the unit for rows 2 tig and 2 tig + 1
               uint32_t w[4], e0, o0, e1, o1;
-              ldsm_x4_t((vb + kt * 16 * D) ^ (k << 4), w[0], w[1], w[2], w[3]);
+              ldsm_x4_t((base + C::kHalf + toff[t0 + kt]) ^ (k << 4), w[0], w[1], w[2], w[3]);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 e4m3x4_to_f16(__byte_perm(w[2 * x], 0u, 0x3120), e0, o0);
@@ -571,10 +629,43 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
       if (++slot == NS) slot = 0, phase ^= 1u;
     }
 
-    // Merge the four slices of each row group through the last slot, 16 rows at a time, and write
-    // them out.
+    // Merge the slices of each K/V head and row group through the last slot, 16 rows at a time, and
+    // write them out.
     const bool whole = seg.c0 == 0 && seg.c1 == seg.chunks;
     const int part = 2 * blockIdx.x + (seg.c0 == 0 ? 1 : 0);
+    // final (o, lse) or partial (sums, m, l) results of four columns of a row
+    auto put = [&](int kv, int row, int col, float4 A, float M, float L) {
+      if (whole) {
+        const int i = row / p.G, h = kv * p.G + row - i * p.G;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        *reinterpret_cast<uint2*>(p.o + (((long long)seg.b * p.Nq + i) * p.Hq + h) * D + col) =
+            make_uint2(pack_bf16x2(A.x * inv, A.y * inv), pack_bf16x2(A.z * inv, A.w * inv));
+        if (col == 0 && p.lse)
+          p.lse[((long long)seg.b * p.Hq + h) * p.Nq + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+      } else {
+        const long long at = (((long long)part << p.hs) + kv - (group << p.hs)) * R + row - tile * R;
+        *reinterpret_cast<float4*>(p.ws_acc + at * D + col) = A;
+        if (col == 0) p.ws_ml[at] = make_float2(M, L);
+      }
+    };
+    if (MT == 1 && RG == 1 && p.hs == 2) {
+      // a warp has its K/V head to itself: straight from its registers
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        float l = l_r[0][hr];
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        const int row = row0 + g + 8 * hr;
+        if (row >= p.rows) continue;
+        const float e = ex2_approx(w_r[0][hr] - m_r[0][hr]);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          put(kvh, row, 16 * k + 4 * tig,
+              make_float4(acc[0][2 * k][2 * hr] * e, acc[0][2 * k + 1][2 * hr] * e, acc[0][2 * k][2 * hr + 1] * e,
+                          acc[0][2 * k + 1][2 * hr + 1] * e),
+              m_r[0][hr], l);
+      }
+    } else {
     float* const mg = reinterpret_cast<float*>(ring + slot * C::kStage);
     float2* const ml = sm_ml + rg * 64;
 #pragma unroll
@@ -590,8 +681,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
             l += __shfl_xor_sync(0xffffffffu, l, 2);
             // weights so far are relative to 2^w_r: relative to 2^m from here on
             const float e = ex2_approx(w_r[mt][hr] - m_r[mt][hr]);
-            if (tig == 0) ml[slice * 16 + g + 8 * hr] = make_float2(m_r[mt][hr], l);
-            float* to = mg + (slice * 16 + g + 8 * hr) * D + 4 * tig;
+            if (tig == 0) ml[w4 * 16 + g + 8 * hr] = make_float2(m_r[mt][hr], l);
+            float* to = mg + (w4 * 16 + g + 8 * hr) * D + 4 * tig;
 #pragma unroll
             for (int k = 0; k < KS; ++k)
               *reinterpret_cast<float4*>(to + 16 * k) =
@@ -601,16 +692,15 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
         }
         asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
         const int row_at = tile * R + (turn * MT + mt) * 16;  // of the rows now in the slot
-        for (int idx = threadIdx.x; idx < 16 * (D / 4); idx += C::kWarps * 32) {
-          const int r = idx / (D / 4), col = 4 * (idx - r * (D / 4));
-          const int row = row_at + r;
-          if (row >= p.rows) break;
+        for (int idx = threadIdx.x; idx < (16 << p.hs) * (D / 4); idx += C::kWarps * 32) {
+          const int hd = idx / (16 * (D / 4)), r = idx / (D / 4) & 15, col = 4 * (idx % (D / 4));
+          const int row = row_at + r, w0 = hd << (2 - p.hs), w1 = (hd + 1) << (2 - p.hs);
+          if (row >= p.rows) continue;
           const float2* from = sm_ml + turn * 64 + r;
-          const float M = fmaxf(fmaxf(from[0].x, from[16].x), fmaxf(from[32].x, from[48].x));
-          float L = 0.f;
+          float M = kDec8Low, L = 0.f;
+          for (int w = w0; w < w1; ++w) M = fmaxf(M, from[w * 16].x);
           float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int w = w0; w < w1; ++w) {
             const float e = ex2_approx(from[w * 16].x - M);
             L += e * from[w * 16].y;
             const float4 x = *reinterpret_cast<const float4*>(mg + (w * 16 + r) * D + col);
@@ -619,103 +709,92 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
             A.z += e * x.z;
             A.w += e * x.w;
           }
-          if (whole) {
-            const int i = row / p.G, h = kvh * p.G + row - i * p.G;
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            *reinterpret_cast<uint2*>(p.o + (((long long)seg.b * p.Nq + i) * p.Hq + h) * D + col) =
-                make_uint2(pack_bf16x2(A.x * inv, A.y * inv), pack_bf16x2(A.z * inv, A.w * inv));
-            if (col == 0 && p.lse)
-              p.lse[((long long)seg.b * p.Hq + h) * p.Nq + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-          } else {
-            const long long at = (long long)part * R + row - tile * R;
-            *reinterpret_cast<float4*>(p.ws_acc + at * D + col) = A;
-            if (col == 0) p.ws_ml[at] = make_float2(M, L);
-          }
+          put((group << p.hs) + hd, row, col, A, M, L);
         }
       }
+    }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + slot);
     if (++slot == NS) slot = 0, phase ^= 1u;
     if constexpr (MT > 1) asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");  // sm_q is free
-    if (!whole && seg.c0 == 0 && threadIdx.x == 0) {
+    if (seg.c0 == 0 && threadIdx.x == 0 && (!whole || p.by_unit)) {
       // the parts after this one: the CTAs whose shares begin before the unit ends
-      const long long stop = end + (seg.chunks - seg.c1);
-      int parts = 1;
-      while (blockIdx.x + parts < ctas && (blockIdx.x + parts) * T / ctas < stop) ++parts;
-      p.ws_desc[blockIdx.x] = make_int4(parts, seg.b, kvh, tile);
+      int parts = whole ? 0 : 1;
+      if (!whole) {
+        // x T / ctas < stop, rounded down or not, is x < stop ctas / T, rounded up
+        const long long stop = end + (seg.chunks - seg.c1);
+        parts = (int)((stop * ctas + T - 1) / T) - (int)blockIdx.x;
+      }
+      p.ws_desc[p.by_unit ? seg.b * p.units + seg.unit : blockIdx.x] =
+          make_int4(parts | (int)blockIdx.x << 16, seg.b, group, tile);
     }
   }
 }
 
-// Merges the parts of the unit that begins in CTA x's last segment: its part 2 x + 1, then the
-// first parts 2 (x + 1), 2 (x + 2), ...  A warp per query row, or four when there are many parts.
-template <int D, int R>
-__global__ void __launch_bounds__(128) fa_decode_fp8_combine_kernel(const Dec8Params p) {
-  constexpr int V = D / 32;
-  __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
-  const int x = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 d = p.ws_desc[x];
-  const int parts = d.x;
+// Merges the parts of a unit: part 2 x + 1 of the CTA x it begins in, then the first parts
+// 2 (x + 1), 2 (x + 2), ...  blockIdx.x counts units where there are at most as many as CTAs, else
+// the CTAs that a unit begins in last (p.by_unit).  WIDE: a block per query row, its warps share
+// the parts (few units have many parts each); else a warp per row.
+template <int D, int R, bool WIDE>
+__global__ void __launch_bounds__(256) fa_decode_fp8_combine_kernel(const Dec8Params p) {
+  constexpr int V = D / 32, W = 8;
+  __shared__ float sm_l[W], sm_o[W][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 d = p.ws_desc[blockIdx.x];
+  const int parts = d.x & 0xFFFF, x = d.x >> 16;
   if (parts == 0) return;
-  const bool wide = parts > 8;
-  for (int k = 0; k < (wide ? 4 : 1); ++k) {
-    const int r = blockIdx.y * 4 + (wide ? k : warp), row = d.w * R + r;
-    const bool in = row < p.rows;
-    float M = kDec8Low, L = 0.f, a[V];
+  const int item = WIDE ? blockIdx.y : blockIdx.y * W + warp;  // row of a tile, over the K/V heads
+  const int per = min(p.rows, R), hd = item / per, r = item - hd * per, row = d.w * R + r;
+  const bool in = hd < (1 << p.hs) && row < p.rows;
+  if (WIDE && !in) return;
+  const long long pitch = (long long)R << (1 + p.hs);  // from a CTA's first part to the next one's
+  const long long first = ((((long long)2 * x) << p.hs) + hd) * R + r, odd = (long long)R << p.hs;
+  float M = kDec8Low, L = 0.f, a[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) a[v] = 0.f;
-    if (in) {
-      const int step = wide ? 4 : 1;
-#pragma unroll 4
-      for (int s = wide ? warp : 0; s < parts; s += step) {
-        const long long slot = (long long)(2 * (x + s) + (s == 0 ? 1 : 0)) * R + r;
-        const float2 ml = p.ws_ml[slot];
-        float y[V];
-        if constexpr (V == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(p.ws_acc + slot * D + lane * 4);
-          y[0] = f.x, y[1] = f.y, y[2] = f.z, y[3] = f.w;
-        } else {
-          const float2 f = *reinterpret_cast<const float2*>(p.ws_acc + slot * D + lane * 2);
-          y[0] = f.x, y[1] = f.y;
-        }
-        const float m_new = fmaxf(M, ml.x);
-        const float e0 = ex2_approx(M - m_new), e1 = ex2_approx(ml.x - m_new);
-        L = L * e0 + ml.y * e1;
+  for (int v = 0; v < V; ++v) a[v] = 0.f;
+  if (in) {
+    // every part's maximum first, so that the sums are independent loads
+    const int s0 = WIDE ? warp : 0, step = WIDE ? W : 1;
+    for (int s = lane; s < parts; s += 32) M = fmaxf(M, p.ws_ml[first + s * pitch + (s ? 0 : odd)].x);
 #pragma unroll
-        for (int v = 0; v < V; ++v) a[v] = a[v] * e0 + y[v] * e1;
-        M = m_new;
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+#pragma unroll 8
+    for (int s = s0; s < parts; s += step) {
+      const long long at = first + s * pitch + (s ? 0 : odd);
+      const float2 ml = p.ws_ml[at];
+      const float e = ex2_approx(ml.x - M);
+      L += e * ml.y;
+      if constexpr (V == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(p.ws_acc + at * D + lane * 4);
+        a[0] += e * f.x, a[1] += e * f.y, a[2] += e * f.z, a[3] += e * f.w;
+      } else {
+        const float2 f = *reinterpret_cast<const float2*>(p.ws_acc + at * D + lane * 2);
+        a[0] += e * f.x, a[1] += e * f.y;
       }
     }
-    if (wide) {
-      if (lane == 0) {
-        sm_m[warp] = M;
-        sm_l[warp] = L;
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) sm_o[warp][lane * V + v] = a[v];
-      __syncthreads();
-      M = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
-      L = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v) a[v] = 0.f;
-      for (int w = 0; w < 4; ++w) {
-        const float e = ex2_approx(sm_m[w] - M);
-        L += e * sm_l[w];
-#pragma unroll
-        for (int v = 0; v < V; ++v) a[v] += e * sm_o[w][lane * V + v];
-      }
-      __syncthreads();
-    }
-    if (!in || (wide && warp != 0)) continue;
-    const int i = row / p.G, h = d.z * p.G + row - i * p.G;
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    __nv_bfloat16* to = p.o + (((long long)d.y * p.Nq + i) * p.Hq + h) * D + lane * V;
-#pragma unroll
-    for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(to + v) = pack_bf16x2(a[v] * inv, a[v + 1] * inv);
-    if (lane == 0 && p.lse)
-      p.lse[((long long)d.y * p.Hq + h) * p.Nq + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   }
+  if constexpr (WIDE) {
+    if (lane == 0) sm_l[warp] = L;
+#pragma unroll
+    for (int v = 0; v < V; ++v) sm_o[warp][lane * V + v] = a[v];
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < W; ++w) {
+      L += sm_l[w];
+#pragma unroll
+      for (int v = 0; v < V; ++v) a[v] += sm_o[w][lane * V + v];
+    }
+  }
+  if (!in) return;
+  const int i = row / p.G, h = ((d.z << p.hs) + hd) * p.G + row - i * p.G;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  __nv_bfloat16* to = p.o + (((long long)d.y * p.Nq + i) * p.Hq + h) * D + lane * V;
+#pragma unroll
+  for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(to + v) = pack_bf16x2(a[v] * inv, a[v + 1] * inv);
+  if (lane == 0 && p.lse)
+    p.lse[((long long)d.y * p.Hq + h) * p.Nq + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 }  // namespace fa

@@ -324,7 +324,9 @@ FA_EXPORT fa_status fa_cache_append_fp8(const void* k, const void* v, const int3
  * read as page 0 and recorded (FA_ERR_INVALID_ARG from fa_last_device_error).
  * The stored values are exact in the products; P times the V scale is rounded to fp16 with its
  * own running maximum, sums are fp32, o is rounded to bf16.
- * Hq a multiple of Hkv; d 64 or 128; sizes as in fa_cache_append_fp8.  workspace: at least
+ * Hq a multiple of Hkv; d 64 or 128; sizes as in fa_cache_append_fp8, and B * Hkv *
+ * max_pages_per_seq * page_size * (Nq * (Hq / Hkv) / 64, rounded up) < 2^37 (FA_ERR_UNSUPPORTED
+ * beyond).  workspace: at least
  * fa_decode_paged_fp8_workspace_size(...) bytes, 16-byte aligned, not initialised; calls that
  * share one must not overlap on the GPU. */
 FA_EXPORT fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
