@@ -1063,11 +1063,10 @@ fa_status check_cache8(const void* k_pages, const void* v_pages, const float* k_
 
 template <int D>
 fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
-  const int wpu = (1 << prm.sb_shift) / 16;
-  const int warps = std::max(8, wpu), upc = warps / wpu;
+  const int upc = kAppendCta / append_warps<D>(prm.sb_shift);
   const dim3 grid((unsigned)(prm.cu ? (prm.total >> prm.sb_shift) + 2ll * prm.B : prm.B),
                   (unsigned)((prm.Hkv + upc - 1) / upc));
-  fa_cache_append_kernel<D><<<grid, warps * 32, 0, st>>>(prm);
+  fa_cache_append_kernel<D><<<grid, kAppendCta * 32, 0, st>>>(prm);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
