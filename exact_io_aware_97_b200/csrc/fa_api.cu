@@ -1240,6 +1240,8 @@ fa_status check_pages(const fa_pool* pools, int n_pools, const int32_t* block_ta
   if (B > 0 && (!block_table || !seqlens || !aligned4(block_table) || !aligned4(seqlens))) return FA_ERR_INVALID_ARG;
   for (int i = 0; i < n_pools; ++i)
     if (!pools[i].base || pools[i].page_bytes == 0) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < n_pools; ++i)
+    if (pools[i].page_bytes >= (size_t(1) << 31)) return FA_ERR_UNSUPPORTED;
   if ((page_size & (page_size - 1)) != 0) return FA_ERR_UNSUPPORTED;
   if (num_pages >= kFreeMark || (int64_t)max_pages * page_size >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
@@ -1254,10 +1256,19 @@ fa_status launch_copies(const fa_pool* pools, int n_pools, const int32_t* src, c
     list.n = std::min(kMaxPools, n_pools - at);
     for (int i = 0; i < list.n; ++i) {
       list.base[i] = static_cast<uint8_t*>(pools[at + i].base);
-      list.bytes[i] = pools[at + i].page_bytes;
+      list.bytes[i] = (unsigned)pools[at + i].page_bytes;
     }
-    pages_copy_kernel<<<sms * 8, 256, 0, st>>>(list, src, dst, count);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    // a wave of blocks over all pools, at least 8 for each
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sms * 8, list.n);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, pages_copy_kernel, list, src, dst, count) != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;
 }
@@ -1267,7 +1278,7 @@ fa_status launch_copies(const fa_pool* pools, int n_pools, const int32_t* src, c
 
 extern "C" size_t fa_pages_workspace_size(int num_pages, int B_out) {
   if (num_pages <= 0 || B_out < 0) return 0;
-  return align_up((size_t)num_pages * 4, 256) + align_up(16, 256) +
+  return align_up((size_t)num_pages * 4, 256) + 256 +
          4 * align_up((size_t)std::max(num_pages / 2 + 1, B_out) * 4, 256);
 }
 
@@ -1299,6 +1310,7 @@ extern "C" fa_status fa_pages_fork(const fa_pool* pools, int n_pools, const int3
   prm.mark = reinterpret_cast<int32_t*>(ws);
   ws += align_up((size_t)num_pages * 4, 256);
   prm.count = reinterpret_cast<int32_t*>(ws);
+  prm.counts = prm.count + 4;
   ws += 256;
   prm.rank = reinterpret_cast<int32_t*>(ws);
   prm.src = reinterpret_cast<int32_t*>(ws + list);
@@ -1308,10 +1320,7 @@ extern "C" fa_status fa_pages_fork(const fa_pool* pools, int n_pools, const int3
   prm.max_pages = max_pages_per_seq;
   prm.page_shift = __builtin_ctz((unsigned)page_size);
   prm.num_pages = num_pages;
-  if (cudaMemsetAsync(prm.mark, 0x7F, (size_t)num_pages * 4, st) != cudaSuccess) return FA_ERR_CUDA;
-  if (B_out > 0) fork_mark_kernel<<<B_out, 256, 0, st>>>(prm);
-  fork_plan_kernel<<<1, 1024, 0, st>>>(prm);
-  if (B_out > 0) fork_write_kernel<<<B_out, 256, 0, st>>>(prm);
+  fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   return launch_copies(pools, n_pools, prm.src, prm.dst, prm.count, st);
 }
@@ -1338,6 +1347,7 @@ extern "C" fa_status fa_pages_compact(const fa_pool* pools, int n_pools, const i
   prm.mark = reinterpret_cast<int32_t*>(ws);
   ws += align_up((size_t)num_pages * 4, 256);
   prm.count = reinterpret_cast<int32_t*>(ws);
+  prm.counts = prm.count + 4;
   ws += 256;
   prm.src = reinterpret_cast<int32_t*>(ws);
   prm.dst = reinterpret_cast<int32_t*>(ws + list);
@@ -1345,10 +1355,7 @@ extern "C" fa_status fa_pages_compact(const fa_pool* pools, int n_pools, const i
   prm.max_pages = max_pages_per_seq;
   prm.page_shift = __builtin_ctz((unsigned)page_size);
   prm.num_pages = num_pages;
-  if (cudaMemsetAsync(prm.mark, 0x7F, (size_t)num_pages * 4, st) != cudaSuccess) return FA_ERR_CUDA;
-  if (B > 0) compact_mark_kernel<<<B, 256, 0, st>>>(prm);
-  compact_plan_kernel<<<1, 1024, 0, st>>>(prm);
-  if (B > 0) compact_write_kernel<<<B, 256, 0, st>>>(prm);
+  compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   return launch_copies(pools, n_pools, prm.src, prm.dst, prm.count, st);
 }

@@ -12,8 +12,9 @@
 // Free pages are handed out in ascending order and copies in the order of the new sequences, so
 // results do not depend on the order of the atomics (a minimum per page).
 //
-// Bound by HBM where pages are copied (2 bytes moved a byte) and by launches and one pass over
-// the pool's marks where only tables change.
+// Bound by HBM where pages are copied (2 bytes moved a byte), and by latency where only tables
+// change: one kernel plans (five of them, one with a single CTA, took FORK1 us on 16 prompts forked
+// into 64 sequences, this one and the copies FORK2 us), one copies.
 #pragma once
 
 #include "fa_device.cuh"
@@ -21,11 +22,11 @@
 namespace fa {
 
 constexpr int kMaxPools = 128;
-constexpr int kFreeMark = 0x7F7F7F7F;  // what a memset of 0x7F leaves
+constexpr int kFreeMark = 0x7FFFFFFF;
 
 struct PoolList {
   uint8_t* base[kMaxPools];
-  unsigned long long bytes[kMaxPools];  // of one page
+  unsigned bytes[kMaxPools];  // of one page
   int n;
 };
 
@@ -36,6 +37,7 @@ struct ForkParams {
   int32_t *rank;          // [R]: number of the copy that row i needs, or -1
   int32_t *src, *dst;     // [R]: the copies
   int32_t *count;         // number of copies
+  int32_t *counts;        // per CTA of the planning cluster
   int B, R, max_pages, page_shift, num_pages;
 };
 
@@ -44,7 +46,7 @@ struct CompactParams {
   int32_t *table_out, *n_live;
   int32_t *mark;       // [num_pages]
   int32_t *src, *dst;  // [num_pages / 2 + 1]
-  int32_t *count;
+  int32_t *count, *counts;
   int B, max_pages, page_shift, num_pages;
 };
 
@@ -74,167 +76,244 @@ __device__ __forceinline__ bool pages_ok(int page, int num_pages) {
   return false;
 }
 
-// mark[page]: -1 where some new row holds it full, else the first new row that ends in it.
-__global__ void __launch_bounds__(256) fork_mark_kernel(const ForkParams p) {
-  const int i = blockIdx.x;
-  int b;
-  const int n = fork_len(p, i, &b);
-  const int full = n >> p.page_shift, np = full + ((n & ((1 << p.page_shift) - 1)) != 0);
-  for (int t = threadIdx.x; t < np; t += blockDim.x) {
-    const int page = __ldg(p.table + (long long)b * p.max_pages + t);
-    if (pages_ok(page, p.num_pages)) atomicMin(p.mark + page, t < full ? -1 : i);
-  }
+// The planning kernels run as one cluster of 8 CTAs, whose barriers (hardware ones) separate their
+// steps; pages and rows are cut into 8 contiguous segments, so that ranks are sums over segments.
+constexpr int kPlanCtas = 8, kPlanThreads = 1024;
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Exclusive sum over the 1024 threads of a block of one flag each; total in *total.
+__device__ __forceinline__ int plan_begin(int n, int cta) { return (int)((long long)n * cta / kPlanCtas); }
+
+// Exclusive rank of one flag per thread over the CTA; the CTA's total in *total.
 __device__ __forceinline__ int block_rank(bool flag, int* sm, int* total) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned ballot = __ballot_sync(0xffffffffu, flag);
   __syncthreads();
   if (lane == 0) sm[warp] = __popc(ballot);
   __syncthreads();
+  const int c = sm[lane];
+  *total = __reduce_add_sync(0xffffffffu, c);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? c : 0) + __popc(ballot & ((1u << lane) - 1u));
+}
+
+// Per-CTA counts in the workspace: what comes before this CTA, and the total.
+__device__ __forceinline__ int plan_before(const int32_t* counts, int cta, int* total) {
   int before = 0, all = 0;
-  for (int w = 0; w < 32; ++w) {
-    const int c = sm[w];
-    before += w < warp ? c : 0;
-    all += c;
+  for (int c = 0; c < kPlanCtas; ++c) {
+    const int x = __ldcg(counts + c);
+    before += c < cta ? x : 0;
+    all += x;
   }
   *total = all;
-  return before + __popc(ballot & ((1u << lane) - 1u));
+  return before;
 }
 
-__global__ void __launch_bounds__(1024) fork_plan_kernel(const ForkParams p) {
-  __shared__ int sm[32];
-  int need = 0;
-  for (int i0 = 0; i0 < p.R; i0 += 1024) {
-    const int i = i0 + threadIdx.x;
-    bool copy = false;
-    int page = -1;
-    if (i < p.R) {
-      int b;
-      const int n = fork_len(p, i, &b);
-      if (n & ((1 << p.page_shift) - 1)) {
-        page = __ldg(p.table + (long long)b * p.max_pages + (n >> p.page_shift));
-        copy = page >= 0 && page < p.num_pages && p.mark[page] != i;
-      }
-    }
-    int total;
-    const int r = need + block_rank(copy, sm, &total);
-    if (i < p.R) p.rank[i] = copy ? r : -1;
-    if (copy) p.src[r] = page;
-    need += total;
-  }
-  int free_pages = 0;
-  for (int g0 = 0; g0 < p.num_pages; g0 += 1024) {
-    const int g = g0 + threadIdx.x;
-    const bool is_free = g < p.num_pages && p.mark[g] == kFreeMark;
-    int total;
-    const int r = free_pages + block_rank(is_free, sm, &total);
-    if (is_free) {
-      if (r < need) p.dst[r] = g;
-      else p.free_pages[r - need] = g;
-    }
-    free_pages += total;
-  }
-  const int left = max(free_pages - need, 0);
-  for (int k = left + threadIdx.x; k < p.num_pages; k += 1024) p.free_pages[k] = -1;
-  if (threadIdx.x == 0) {
-    *p.n_free = left;
-    *p.count = min(need, free_pages);
-    if (need > free_pages) atomicOr(&g_error_word, kErrNoPages);
-  }
-}
-
-__global__ void __launch_bounds__(256) fork_write_kernel(const ForkParams p) {
-  const int i = blockIdx.x, r = p.rank[i];
+// The page of row i's last tokens if that page is not full, else -1.
+__device__ __forceinline__ int fork_tail(const ForkParams& p, int i) {
   int b;
-  int n = fork_len(p, i, &b);
-  if (r >= 0 && r >= *p.count) n = 0;  // no page was left for it
-  const int full = n >> p.page_shift, np = full + ((n & ((1 << p.page_shift) - 1)) != 0);
-  for (int t = threadIdx.x; t < p.max_pages; t += blockDim.x) {
-    int page = -1;
-    if (t < np) page = (t == full && r >= 0) ? p.dst[r] : __ldg(p.table + (long long)b * p.max_pages + t);
-    p.table_out[(long long)i * p.max_pages + t] = page;
-  }
-  if (threadIdx.x == 0) p.lens_out[i] = n;
+  const int n = fork_len(p, i, &b);
+  if ((n & ((1 << p.page_shift) - 1)) == 0) return -1;
+  return __ldg(p.table + (long long)b * p.max_pages + (n >> p.page_shift));
 }
 
-__global__ void __launch_bounds__(256) compact_mark_kernel(const CompactParams p) {
-  const int b = blockIdx.x;
-  const int n = pages_len(p.lens, b, p.max_pages, p.page_shift);
-  const int np = (n + (1 << p.page_shift) - 1) >> p.page_shift;
-  for (int t = threadIdx.x; t < np; t += blockDim.x) {
-    const int page = __ldg(p.table + (long long)b * p.max_pages + t);
-    if (pages_ok(page, p.num_pages)) p.mark[page] = page;
-  }
-}
-
-__global__ void __launch_bounds__(1024) compact_plan_kernel(const CompactParams p) {
+__global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParams p) {
   __shared__ int sm[32];
-  int live = 0;
-  for (int g0 = 0; g0 < p.num_pages; g0 += 1024) {
-    const int g = g0 + threadIdx.x;
-    int total;
-    block_rank(g < p.num_pages && p.mark[g] != kFreeMark, sm, &total);
-    live += total;
+  const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = cta * kPlanThreads + threadIdx.x, threads = kPlanCtas * kPlanThreads;
+  const int psm = (1 << p.page_shift) - 1;
+  for (int g = tid; g < p.num_pages; g += threads) p.mark[g] = kFreeMark;
+  cluster_sync();
+  // mark[page]: -1 where some new row holds it full, else the first new row that ends in it
+  for (int i = cta * 32 + warp; i < p.R; i += kPlanCtas * 32) {
+    int b;
+    const int n = fork_len(p, i, &b), full = n >> p.page_shift, np = full + ((n & psm) != 0);
+    for (int t = lane; t < np; t += 32) {
+      const int page = __ldg(p.table + (long long)b * p.max_pages + t);
+      if (pages_ok(page, p.num_pages)) atomicMin(p.mark + page, t < full ? -1 : i);
+    }
   }
+  cluster_sync();
+  // count the copies that this CTA's rows need and the free pages in its part of the pool
+  auto needs_copy = [&](int i, int page) { return page >= 0 && page < p.num_pages && __ldcg(p.mark + page) != i; };
+  const int i0 = plan_begin(p.R, cta), i1 = plan_begin(p.R, cta + 1);
+  const int g0 = plan_begin(p.num_pages, cta), g1 = plan_begin(p.num_pages, cta + 1);
+  int copies = 0, frees = 0, total;
+  for (int at = i0; at < i1; at += kPlanThreads) {
+    const int i = at + threadIdx.x;
+    block_rank(i < i1 && needs_copy(i, fork_tail(p, i)), sm, &total);
+    copies += total;
+  }
+  for (int at = g0; at < g1; at += kPlanThreads) {
+    const int g = at + threadIdx.x;
+    block_rank(g < g1 && __ldcg(p.mark + g) == kFreeMark, sm, &total);
+    frees += total;
+  }
+  if (threadIdx.x == 0) {
+    p.counts[cta] = copies;
+    p.counts[kPlanCtas + cta] = frees;
+  }
+  cluster_sync();
+  int need, have;
+  int r = plan_before(p.counts, cta, &need), f = plan_before(p.counts + kPlanCtas, cta, &have);
+  for (int at = i0; at < i1; at += kPlanThreads) {
+    const int i = at + threadIdx.x, page = i < i1 ? fork_tail(p, i) : -1;
+    const bool copy = i < i1 && needs_copy(i, page);
+    const int mine = r + block_rank(copy, sm, &total);
+    if (i < i1) p.rank[i] = copy ? mine : -1;
+    if (copy) p.src[mine] = page;
+    r += total;
+  }
+  for (int at = g0; at < g1; at += kPlanThreads) {
+    const int g = at + threadIdx.x;
+    const bool is_free = g < g1 && __ldcg(p.mark + g) == kFreeMark;
+    const int mine = f + block_rank(is_free, sm, &total);
+    if (is_free) {
+      if (mine < need) p.dst[mine] = g;
+      else p.free_pages[mine - need] = g;
+    }
+    f += total;
+  }
+  const int left = max(have - need, 0);
+  for (int k = left + tid; k < p.num_pages; k += threads) p.free_pages[k] = -1;
+  if (tid == 0) {
+    *p.n_free = left;
+    *p.count = min(need, have);
+    if (need > have) atomicOr(&g_error_word, kErrNoPages);
+  }
+  cluster_sync();
+  for (int i = cta * 32 + warp; i < p.R; i += kPlanCtas * 32) {
+    const int k = __ldcg(p.rank + i);
+    int b;
+    int n = fork_len(p, i, &b);
+    if (k >= have) n = 0;  // no page was left for it
+    const int full = n >> p.page_shift, np = full + ((n & psm) != 0);
+    const int32_t* from = p.table + (long long)max(b, 0) * p.max_pages;
+    int32_t* to = p.table_out + (long long)i * p.max_pages;
+    for (int t = lane; t < p.max_pages; t += 32)
+      to[t] = t >= np ? -1 : t == full && k >= 0 ? __ldcg(p.dst + k) : __ldg(from + t);
+    if (lane == 0) p.lens_out[i] = n;
+  }
+}
+
+__global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) compact_plan_kernel(const CompactParams p) {
+  __shared__ int sm[32];
+  const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = cta * kPlanThreads + threadIdx.x, threads = kPlanCtas * kPlanThreads;
+  const int psm = (1 << p.page_shift) - 1;
+  for (int g = tid; g < p.num_pages; g += threads) p.mark[g] = kFreeMark;
+  cluster_sync();
+  for (int b = cta * 32 + warp; b < p.B; b += kPlanCtas * 32) {
+    const int n = pages_len(p.lens, b, p.max_pages, p.page_shift), np = (n >> p.page_shift) + ((n & psm) != 0);
+    for (int t = lane; t < np; t += 32) {
+      const int page = __ldg(p.table + (long long)b * p.max_pages + t);
+      if (pages_ok(page, p.num_pages)) p.mark[page] = page;
+    }
+  }
+  cluster_sync();
+  const int g0 = plan_begin(p.num_pages, cta), g1 = plan_begin(p.num_pages, cta + 1);
+  auto used = [&](int g) { return g < g1 && __ldcg(p.mark + g) != kFreeMark; };
+  int n = 0, total;
+  for (int at = g0; at < g1; at += kPlanThreads) {
+    block_rank(used(at + threadIdx.x), sm, &total);
+    n += total;
+  }
+  if (threadIdx.x == 0) p.counts[cta] = n;
+  cluster_sync();
+  int live;
+  plan_before(p.counts, cta, &live);
   int holes = 0, moves = 0;
-  for (int g0 = 0; g0 < p.num_pages; g0 += 1024) {
-    const int g = g0 + threadIdx.x;
-    const bool used = g < p.num_pages && p.mark[g] != kFreeMark;
-    const bool hole = g < live && !used, move = g >= live && used;
-    int total;
-    int r = holes + block_rank(hole, sm, &total);
-    if (hole) p.dst[r] = g;
+  for (int at = g0; at < g1; at += kPlanThreads) {
+    const int g = at + threadIdx.x;
+    const bool u = used(g);
+    block_rank(g < g1 && g < live && !u, sm, &total);
     holes += total;
-    r = moves + block_rank(move, sm, &total);
-    if (move) p.src[r] = g;
+    block_rank(g >= live && u, sm, &total);
     moves += total;
   }
-  __syncthreads();  // moves == holes: both count the pages in use past `live`
-  for (int k = threadIdx.x; k < moves; k += 1024) p.mark[p.src[k]] = p.dst[k];
   if (threadIdx.x == 0) {
+    p.counts[kPlanCtas + cta] = holes;
+    p.counts[2 * kPlanCtas + cta] = moves;
+  }
+  cluster_sync();
+  int all_moves;
+  int h = plan_before(p.counts + kPlanCtas, cta, &total), m = plan_before(p.counts + 2 * kPlanCtas, cta, &all_moves);
+  for (int at = g0; at < g1; at += kPlanThreads) {
+    const int g = at + threadIdx.x;
+    const bool u = used(g);
+    const bool hole = g < g1 && g < live && !u, move = g >= live && u;
+    int k = h + block_rank(hole, sm, &total);
+    if (hole) p.dst[k] = g;
+    h += total;
+    k = m + block_rank(move, sm, &total);
+    if (move) p.src[k] = g;
+    m += total;
+  }
+  if (tid == 0) {
     *p.n_live = live;
-    *p.count = moves;
+    *p.count = all_moves;
   }
-}
-
-__global__ void __launch_bounds__(256) compact_write_kernel(const CompactParams p) {
-  const int b = blockIdx.x;
-  const int n = pages_len(p.lens, b, p.max_pages, p.page_shift);
-  const int np = (n + (1 << p.page_shift) - 1) >> p.page_shift;
-  for (int t = threadIdx.x; t < p.max_pages; t += blockDim.x) {
-    int page = -1;
-    if (t < np) {
-      page = __ldg(p.table + (long long)b * p.max_pages + t);
-      if (page >= 0 && page < p.num_pages) page = p.mark[page];
+  cluster_sync();
+  for (int k = tid; k < all_moves; k += threads) p.mark[__ldcg(p.src + k)] = __ldcg(p.dst + k);
+  cluster_sync();
+  for (int b = cta * 32 + warp; b < p.B; b += kPlanCtas * 32) {
+    const int len = pages_len(p.lens, b, p.max_pages, p.page_shift), np = (len >> p.page_shift) + ((len & psm) != 0);
+    const int32_t* from = p.table + (long long)b * p.max_pages;
+    int32_t* to = p.table_out + (long long)b * p.max_pages;
+    for (int t = lane; t < p.max_pages; t += 32) {
+      int page = t < np ? __ldg(from + t) : -1;
+      if (page >= 0 && page < p.num_pages) page = __ldcg(p.mark + page);
+      to[t] = page;
     }
-    p.table_out[(long long)b * p.max_pages + t] = page;
   }
 }
 
-// Copies pages src[k] -> dst[k], k < *count, of every pool.  No dst is a src.
+// Copies pages src[k] -> dst[k], k < *count, of every pool (blockIdx.y); no dst is a src.  A block
+// moves 16 KB at a time, four vectors a thread, loaded before the first is stored: a part of a
+// large page, or several small ones.
+constexpr int kCopyBytes = 16384, kCopyThreads = 256;
+
 template <typename T>
-__device__ __forceinline__ void copy_piece(const uint8_t* s, uint8_t* d, unsigned long long from,
-                                           unsigned long long to) {
-  for (unsigned long long at = from + threadIdx.x * sizeof(T); at < to; at += blockDim.x * sizeof(T))
-    *reinterpret_cast<T*>(d + at) = *reinterpret_cast<const T*>(s + at);
+__device__ __forceinline__ void copy_pool(uint8_t* base, unsigned bytes, int n, const int32_t* src, const int32_t* dst) {
+  constexpr unsigned kVec = kCopyBytes / 16;  // vectors of a piece
+  const unsigned vpp = bytes / sizeof(T);     // vectors of a page
+  const unsigned pieces = (vpp + kVec - 1) / kVec, pages = vpp < kVec ? kVec / vpp : 1;
+  const long long items = pages > 1 ? (n + (long long)pages - 1) / pages : (long long)n * pieces;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const unsigned k0 = pages > 1 ? (unsigned)(it * pages) : (unsigned)(it / pieces);
+    const unsigned v0 = pages > 1 ? 0u : (unsigned)(it - (long long)k0 * pieces) * kVec;
+    const unsigned vn = pages > 1 ? min(pages, (unsigned)n - k0) * vpp : min(kVec, vpp - v0);
+    T x[4];
+    T* to[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned v = j * kCopyThreads + threadIdx.x;
+      to[j] = nullptr;
+      if (v < vn) {
+        const unsigned k = pages > 1 ? v / vpp : 0u, in = pages > 1 ? v - k * vpp : v0 + v;
+        const long long from = __ldg(src + k0 + k), at = __ldg(dst + k0 + k);
+        x[j] = __ldcs(reinterpret_cast<const T*>(base) + from * vpp + in);
+        to[j] = reinterpret_cast<T*>(base) + at * vpp + in;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (to[j]) __stcs(to[j], x[j]);
+  }
 }
 
-__global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__ PoolList pools, const int32_t* src,
-                                                         const int32_t* dst, const int32_t* count) {
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ PoolList pools,
+                                                                  const int32_t* src, const int32_t* dst,
+                                                                  const int32_t* count) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = *count;
-  const long long items = (long long)n * pools.n;
-  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int pool = (int)(it / n), k = (int)(it - (long long)pool * n);
-    const unsigned long long bytes = pools.bytes[pool];
-    const uint8_t* s = pools.base[pool] + (unsigned long long)src[k] * bytes;
-    uint8_t* d = pools.base[pool] + (unsigned long long)dst[k] * bytes;
-    const unsigned long long mis = reinterpret_cast<uintptr_t>(pools.base[pool]) | bytes;
-    if ((mis & 15) == 0) copy_piece<uint4>(s, d, 0, bytes);
-    else if ((mis & 3) == 0) copy_piece<uint32_t>(s, d, 0, bytes);
-    else copy_piece<uint8_t>(s, d, 0, bytes);
-  }
+  uint8_t* base = pools.base[blockIdx.y];
+  const unsigned bytes = pools.bytes[blockIdx.y];
+  const unsigned long long mis = reinterpret_cast<uintptr_t>(base) | bytes;
+  if ((mis & 15) == 0) copy_pool<uint4>(base, bytes, n, src, dst);
+  else if ((mis & 3) == 0) copy_pool<uint32_t>(base, bytes, n, src, dst);
+  else copy_pool<uint8_t>(base, bytes, n, src, dst);
 }
 
 }  // namespace fa
