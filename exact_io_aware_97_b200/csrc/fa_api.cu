@@ -1251,20 +1251,36 @@ fa_status launch_copies(const fa_pool* pools, int n_pools, const int32_t* src, c
                         const int32_t* count, cudaStream_t st) {
   const int sms = sm_count_cached();
   if (sms <= 0) return FA_ERR_CUDA;
+  static std::atomic<uint64_t> smem_set{0};  // a bit for each device
+  if (!set_smem_once(pages_copy_kernel, kCopySmem, smem_set)) return FA_ERR_CUDA;
   for (int at = 0; at < n_pools; at += kMaxPools) {
     PoolList list{};
-    list.n = std::min(kMaxPools, n_pools - at);
-    for (int i = 0; i < list.n; ++i) {
-      list.base[i] = static_cast<uint8_t*>(pools[at + i].base);
-      list.bytes[i] = (unsigned)pools[at + i].page_bytes;
+    const int m = std::min(kMaxPools, n_pools - at);
+    // pools whose pages are worth bulk copies first
+    for (int turn = 0; turn < 2; ++turn) {
+      for (int i = 0; i < m; ++i) {
+        const fa_pool& pool = pools[at + i];
+        const uintptr_t mis = reinterpret_cast<uintptr_t>(pool.base) | pool.page_bytes;
+        const unsigned vec = (mis & 15) == 0 ? 16 : (mis & 3) == 0 ? 4 : 1, vpp = (unsigned)pool.page_bytes / vec;
+        const bool bulk = vec == 16 && pool.page_bytes >= 4096;
+        if (bulk != (turn == 0)) continue;
+        const unsigned per = bulk ? kBulkBytes / 16 : kCopyVecs;  // vectors of an item
+        const int k = list.n++;
+        list.base[k] = static_cast<uint8_t*>(pool.base);
+        list.vec[k] = (uint8_t)vec;
+        list.vpp[k] = vpp;
+        list.pages[k] = !bulk && vpp <= per / 2 ? per / vpp : 0;
+        list.pieces[k] = (vpp + per - 1) / per;
+      }
+      if (turn == 0) list.bulk = list.n;
     }
-    // a wave of blocks over all pools, at least 8 for each
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sms * 8, list.n);
-    cfg.blockDim = dim3(kCopyThreads);
+    cfg.gridDim = dim3(sms * 2);
+    cfg.blockDim = dim3(kCopyThreads + 32);
+    cfg.dynamicSmemBytes = kCopySmem;
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;

@@ -26,8 +26,11 @@ constexpr int kFreeMark = 0x7FFFFFFF;
 
 struct PoolList {
   uint8_t* base[kMaxPools];
-  unsigned bytes[kMaxPools];  // of one page
-  int n;
+  unsigned vpp[kMaxPools];     // vectors of a page
+  unsigned pages[kMaxPools];   // whole pages of an item, or 0
+  unsigned pieces[kMaxPools];  // else items of a page
+  uint8_t vec[kMaxPools];      // bytes of a vector: 16, 4 or 1, what the pages' alignment allows
+  int n, bulk;                 // pools; the first `bulk` of them have pages for bulk copies
 };
 
 struct ForkParams {
@@ -123,26 +126,38 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork
   const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tid = cta * kPlanThreads + threadIdx.x, threads = kPlanCtas * kPlanThreads;
   const int psm = (1 << p.page_shift) - 1;
+  // the copies' blocks may come to the idle SMs now; they wait for this kernel's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int g = tid; g < p.num_pages; g += threads) p.mark[g] = kFreeMark;
   cluster_sync();
-  // mark[page]: -1 where some new row holds it full, else the first new row that ends in it
-  for (int i = cta * 32 + warp; i < p.R; i += kPlanCtas * 32) {
+  // mark[page]: -1 where some new row holds it full, else the first new row that ends in it; a
+  // warp takes 128 entries of a row, all loaded before the first is marked
+  const int strips = (p.max_pages + 127) / 128;
+  for (long long it = cta * 32 + warp; it < (long long)p.R * strips; it += kPlanCtas * 32) {
+    const int i = (int)(it / strips), t0 = (int)(it - (long long)i * strips) * 128 + lane;
     int b;
     const int n = fork_len(p, i, &b), full = n >> p.page_shift, np = full + ((n & psm) != 0);
-    for (int t = lane; t < np; t += 32) {
-      const int page = __ldg(p.table + (long long)b * p.max_pages + t);
-      if (pages_ok(page, p.num_pages)) atomicMin(p.mark + page, t < full ? -1 : i);
-    }
+    int page[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      page[j] = t0 + 32 * j < np ? __ldg(p.table + (long long)b * p.max_pages + t0 + 32 * j) : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t0 + 32 * j < np && pages_ok(page[j], p.num_pages))
+        atomicMin(p.mark + page[j], t0 + 32 * j < full ? -1 : i);
   }
+  // this thread's first row of the next steps, looked up behind the marks
+  const int i0 = plan_begin(p.R, cta), i1 = plan_begin(p.R, cta + 1);
+  const int mine_i = i0 + threadIdx.x, mine_tail = mine_i < i1 ? fork_tail(p, mine_i) : -1;
+  auto tail = [&](int i) { return i == mine_i ? mine_tail : i < i1 ? fork_tail(p, i) : -1; };
   cluster_sync();
   // count the copies that this CTA's rows need and the free pages in its part of the pool
   auto needs_copy = [&](int i, int page) { return page >= 0 && page < p.num_pages && __ldcg(p.mark + page) != i; };
-  const int i0 = plan_begin(p.R, cta), i1 = plan_begin(p.R, cta + 1);
   const int g0 = plan_begin(p.num_pages, cta), g1 = plan_begin(p.num_pages, cta + 1);
   int copies = 0, frees = 0, total;
   for (int at = i0; at < i1; at += kPlanThreads) {
     const int i = at + threadIdx.x;
-    block_rank(i < i1 && needs_copy(i, fork_tail(p, i)), sm, &total);
+    block_rank(i < i1 && needs_copy(i, tail(i)), sm, &total);
     copies += total;
   }
   for (int at = g0; at < g1; at += kPlanThreads) {
@@ -158,7 +173,7 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork
   int need, have;
   int r = plan_before(p.counts, cta, &need), f = plan_before(p.counts + kPlanCtas, cta, &have);
   for (int at = i0; at < i1; at += kPlanThreads) {
-    const int i = at + threadIdx.x, page = i < i1 ? fork_tail(p, i) : -1;
+    const int i = at + threadIdx.x, page = tail(i);
     const bool copy = i < i1 && needs_copy(i, page);
     const int mine = r + block_rank(copy, sm, &total);
     if (i < i1) p.rank[i] = copy ? mine : -1;
@@ -183,17 +198,24 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork
     if (need > have) atomicOr(&g_error_word, kErrNoPages);
   }
   cluster_sync();
-  for (int i = cta * 32 + warp; i < p.R; i += kPlanCtas * 32) {
+  for (long long it = cta * 32 + warp; it < (long long)p.R * strips; it += kPlanCtas * 32) {
+    const int i = (int)(it / strips), t0 = (int)(it - (long long)i * strips) * 128 + lane;
     const int k = __ldcg(p.rank + i);
     int b;
     int n = fork_len(p, i, &b);
     if (k >= have) n = 0;  // no page was left for it
     const int full = n >> p.page_shift, np = full + ((n & psm) != 0);
     const int32_t* from = p.table + (long long)max(b, 0) * p.max_pages;
-    int32_t* to = p.table_out + (long long)i * p.max_pages;
-    for (int t = lane; t < p.max_pages; t += 32)
-      to[t] = t >= np ? -1 : t == full && k >= 0 ? __ldcg(p.dst + k) : __ldg(from + t);
-    if (lane == 0) p.lens_out[i] = n;
+    int page[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = t0 + 32 * j;
+      page[j] = t >= np ? -1 : t == full && k >= 0 ? __ldcg(p.dst + k) : __ldg(from + t);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t0 + 32 * j < p.max_pages) p.table_out[(long long)i * p.max_pages + t0 + 32 * j] = page[j];
+    if (t0 == 0) p.lens_out[i] = n;
   }
 }
 
@@ -202,14 +224,21 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) comp
   const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tid = cta * kPlanThreads + threadIdx.x, threads = kPlanCtas * kPlanThreads;
   const int psm = (1 << p.page_shift) - 1;
+  // the copies' blocks may come to the idle SMs now; they wait for this kernel's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int g = tid; g < p.num_pages; g += threads) p.mark[g] = kFreeMark;
   cluster_sync();
-  for (int b = cta * 32 + warp; b < p.B; b += kPlanCtas * 32) {
+  const int strips = (p.max_pages + 127) / 128;  // a warp takes 128 entries of a row
+  for (long long it = cta * 32 + warp; it < (long long)p.B * strips; it += kPlanCtas * 32) {
+    const int b = (int)(it / strips), t0 = (int)(it - (long long)b * strips) * 128 + lane;
     const int n = pages_len(p.lens, b, p.max_pages, p.page_shift), np = (n >> p.page_shift) + ((n & psm) != 0);
-    for (int t = lane; t < np; t += 32) {
-      const int page = __ldg(p.table + (long long)b * p.max_pages + t);
-      if (pages_ok(page, p.num_pages)) p.mark[page] = page;
-    }
+    int page[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      page[j] = t0 + 32 * j < np ? __ldg(p.table + (long long)b * p.max_pages + t0 + 32 * j) : 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t0 + 32 * j < np && pages_ok(page[j], p.num_pages)) p.mark[page[j]] = page[j];
   }
   cluster_sync();
   const int g0 = plan_begin(p.num_pages, cta), g1 = plan_begin(p.num_pages, cta + 1);
@@ -257,63 +286,124 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) comp
   cluster_sync();
   for (int k = tid; k < all_moves; k += threads) p.mark[__ldcg(p.src + k)] = __ldcg(p.dst + k);
   cluster_sync();
-  for (int b = cta * 32 + warp; b < p.B; b += kPlanCtas * 32) {
+  for (long long it = cta * 32 + warp; it < (long long)p.B * strips; it += kPlanCtas * 32) {
+    const int b = (int)(it / strips), t0 = (int)(it - (long long)b * strips) * 128 + lane;
     const int len = pages_len(p.lens, b, p.max_pages, p.page_shift), np = (len >> p.page_shift) + ((len & psm) != 0);
-    const int32_t* from = p.table + (long long)b * p.max_pages;
-    int32_t* to = p.table_out + (long long)b * p.max_pages;
-    for (int t = lane; t < p.max_pages; t += 32) {
-      int page = t < np ? __ldg(from + t) : -1;
-      if (page >= 0 && page < p.num_pages) page = __ldcg(p.mark + page);
-      to[t] = page;
-    }
-  }
-}
-
-// Copies pages src[k] -> dst[k], k < *count, of every pool (blockIdx.y); no dst is a src.  A block
-// moves 16 KB at a time, four vectors a thread, loaded before the first is stored: a part of a
-// large page, or several small ones.
-constexpr int kCopyBytes = 16384, kCopyThreads = 256;
-
-template <typename T>
-__device__ __forceinline__ void copy_pool(uint8_t* base, unsigned bytes, int n, const int32_t* src, const int32_t* dst) {
-  constexpr unsigned kVec = kCopyBytes / 16;  // vectors of a piece
-  const unsigned vpp = bytes / sizeof(T);     // vectors of a page
-  const unsigned pieces = (vpp + kVec - 1) / kVec, pages = vpp < kVec ? kVec / vpp : 1;
-  const long long items = pages > 1 ? (n + (long long)pages - 1) / pages : (long long)n * pieces;
-  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const unsigned k0 = pages > 1 ? (unsigned)(it * pages) : (unsigned)(it / pieces);
-    const unsigned v0 = pages > 1 ? 0u : (unsigned)(it - (long long)k0 * pieces) * kVec;
-    const unsigned vn = pages > 1 ? min(pages, (unsigned)n - k0) * vpp : min(kVec, vpp - v0);
-    T x[4];
-    T* to[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const unsigned v = j * kCopyThreads + threadIdx.x;
-      to[j] = nullptr;
-      if (v < vn) {
-        const unsigned k = pages > 1 ? v / vpp : 0u, in = pages > 1 ? v - k * vpp : v0 + v;
-        const long long from = __ldg(src + k0 + k), at = __ldg(dst + k0 + k);
-        x[j] = __ldcs(reinterpret_cast<const T*>(base) + from * vpp + in);
-        to[j] = reinterpret_cast<T*>(base) + at * vpp + in;
-      }
-    }
+    int page[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (to[j]) __stcs(to[j], x[j]);
+      page[j] = t0 + 32 * j < np ? __ldg(p.table + (long long)b * p.max_pages + t0 + 32 * j) : -1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (page[j] >= 0 && page[j] < p.num_pages) page[j] = __ldcg(p.mark + page[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t0 + 32 * j < p.max_pages) p.table_out[(long long)b * p.max_pages + t0 + 32 * j] = page[j];
   }
 }
 
-__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ PoolList pools,
-                                                                  const int32_t* src, const int32_t* dst,
-                                                                  const int32_t* count) {
+// Copies pages src[k] -> dst[k], k < *count, of every pool; no dst is a src.
+//
+// Large pages (the pools before `bulk`) go through shared memory in pieces of up to 16 KB by bulk
+// copies, which one thread issues: a ring of six pieces in flight each way per CTA, two CTAs per SM
+// (four vectors a thread in registers instead: COPYREG us for the COPYBULK us of the compaction of half a
+// pool).  Small pages go in vectors, four a thread, loaded before the first is stored.
+constexpr int kCopyVecs = 1024, kCopyThreads = 256;
+constexpr int kBulkBytes = 16384, kBulkStages = 6, kCopySmem = kBulkStages * kBulkBytes + 128;
+
+template <typename T>
+__device__ __forceinline__ void copy_item(uint8_t* base, unsigned vpp, unsigned pages, unsigned pieces, long long it,
+                                          int n, const int32_t* src, const int32_t* dst) {
+  const unsigned k0 = pages ? (unsigned)it * pages : (unsigned)(it / pieces);
+  const unsigned v0 = pages ? 0u : (unsigned)(it - (long long)k0 * pieces) * kCopyVecs;
+  const unsigned vn = pages ? min(pages, (unsigned)n - k0) * vpp : min((unsigned)kCopyVecs, vpp - v0);
+  T x[4];
+  T* to[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const unsigned v = j * kCopyThreads + threadIdx.x;
+    to[j] = nullptr;
+    if (v < vn) {
+      const unsigned k = pages ? v / vpp : 0u, in = pages ? v - k * vpp : v0 + v;
+      const long long from = __ldg(src + k0 + k), at = __ldg(dst + k0 + k);
+      x[j] = __ldcs(reinterpret_cast<const T*>(base) + from * vpp + in);
+      to[j] = reinterpret_cast<T*>(base) + at * vpp + in;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (to[j]) __stcs(to[j], x[j]);
+}
+
+// Walks the items of pools [pool, stop) that fall to this block.
+struct CopyWalk {
+  int pool, stop;
+  long long it, first;  // item; first item of the pool
+  __device__ __forceinline__ bool next(const PoolList& pools, int n) {
+    for (;; ++pool) {
+      if (pool >= stop) return false;
+      const unsigned pages = pools.pages[pool];
+      const long long items = pages ? ((long long)n + pages - 1) / pages : (long long)n * pools.pieces[pool];
+      if (it < first + items) return true;
+      first += items;
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kCopyThreads + 32, 2)
+    pages_copy_kernel(const __grid_constant__ PoolList pools, const int32_t* src, const int32_t* dst,
+                      const int32_t* count) {
+  extern __shared__ uint8_t smem_raw[];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = *count;
-  uint8_t* base = pools.base[blockIdx.y];
-  const unsigned bytes = pools.bytes[blockIdx.y];
-  const unsigned long long mis = reinterpret_cast<uintptr_t>(base) | bytes;
-  if ((mis & 15) == 0) copy_pool<uint4>(base, bytes, n, src, dst);
-  else if ((mis & 3) == 0) copy_pool<uint32_t>(base, bytes, n, src, dst);
-  else copy_pool<uint8_t>(base, bytes, n, src, dst);
+  if (threadIdx.x < kCopyThreads) {
+    CopyWalk w{pools.bulk, pools.n, blockIdx.x, 0};
+    for (; w.next(pools, n); w.it += gridDim.x) {
+      const unsigned vpp = pools.vpp[w.pool], pages = pools.pages[w.pool], pieces = pools.pieces[w.pool];
+      uint8_t* const base = pools.base[w.pool];
+      const long long it = w.it - w.first;
+      if (pools.vec[w.pool] == 16) copy_item<uint4>(base, vpp, pages, pieces, it, n, src, dst);
+      else if (pools.vec[w.pool] == 4) copy_item<uint32_t>(base, vpp, pages, pieces, it, n, src, dst);
+      else copy_item<uint8_t>(base, vpp, pages, pieces, it, n, src, dst);
+    }
+    return;
+  }
+  if (threadIdx.x != kCopyThreads) return;
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem_raw + kBulkStages * kBulkBytes);
+  for (int s = 0; s < kBulkStages; ++s) mbar_init(full + s, 1);
+  fence_barrier_init();
+  // `ahead` loads, `w` stores: the store of piece i follows its load, and the load of piece
+  // i + kBulkStages - 1 the store of piece i - 1, once that has read its slot
+  CopyWalk ahead{0, pools.bulk, blockIdx.x, 0}, w = ahead;
+  auto where = [&](const CopyWalk& c, const int32_t* pages_of, unsigned& bytes) {
+    const unsigned pieces = pools.pieces[c.pool];
+    const long long it = c.it - c.first, k = it / pieces, piece = it - k * pieces;
+    const unsigned long long page = (unsigned long long)pools.vpp[c.pool] * 16;
+    bytes = (unsigned)min(page - piece * kBulkBytes, (unsigned long long)kBulkBytes);
+    return pools.base[c.pool] + (unsigned long long)__ldg(pages_of + k) * page + piece * kBulkBytes;
+  };
+  auto load = [&](int slot) {
+    if (!ahead.next(pools, n)) return;
+    unsigned bytes;
+    const uint8_t* from = where(ahead, src, bytes);
+    mbar_arrive_expect_tx(full + slot, bytes);
+    bulk_load(smem_raw + slot * kBulkBytes, from, bytes, full + slot);
+    ahead.it += gridDim.x;
+  };
+  for (int s = 0; s < kBulkStages - 1; ++s) load(s);
+  int slot = 0;
+  uint32_t phase = 0;
+  for (; w.next(pools, n); w.it += gridDim.x) {
+    bulk_wait_group_read0();  // the slot before this one is free: all stores so far have read theirs
+    load(slot == 0 ? kBulkStages - 1 : slot - 1);
+    unsigned bytes;
+    uint8_t* to = where(w, dst, bytes);
+    if (!mbar_wait(full + slot, phase)) break;
+    bulk_store(to, smem_raw + slot * kBulkBytes, bytes);
+    bulk_commit_group();
+    if (++slot == kBulkStages) slot = 0, phase ^= 1u;
+  }
+  bulk_wait_group0();
 }
 
 }  // namespace fa
