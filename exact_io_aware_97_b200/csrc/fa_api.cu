@@ -1242,13 +1242,13 @@ fa_status check_pages(const fa_pool* pools, int n_pools, const int32_t* block_ta
     if (!pools[i].base || pools[i].page_bytes == 0) return FA_ERR_INVALID_ARG;
   for (int i = 0; i < n_pools; ++i)
     if (pools[i].page_bytes >= (size_t(1) << 31)) return FA_ERR_UNSUPPORTED;
-  if ((page_size & (page_size - 1)) != 0) return FA_ERR_UNSUPPORTED;
+  if ((page_size & (page_size - 1)) != 0 || n_pools > kMaxPools * kMaxLaunches) return FA_ERR_UNSUPPORTED;
   if (num_pages >= kFreeMark || (int64_t)max_pages * page_size >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
 fa_status launch_copies(const fa_pool* pools, int n_pools, const int32_t* src, const int32_t* dst,
-                        const int32_t* count, cudaStream_t st) {
+                        const int32_t* count, int32_t* tickets, cudaStream_t st) {
   const int sms = sm_count_cached();
   if (sms <= 0) return FA_ERR_CUDA;
   static std::atomic<uint64_t> smem_set{0};  // a bit for each device
@@ -1284,7 +1284,7 @@ fa_status launch_copies(const fa_pool* pools, int n_pools, const int32_t* src, c
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, pages_copy_kernel, list, src, dst, count) != cudaSuccess) return FA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, pages_copy_kernel, list, src, dst, count, tickets++) != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;
 }
@@ -1326,7 +1326,8 @@ extern "C" fa_status fa_pages_fork(const fa_pool* pools, int n_pools, const int3
   prm.mark = reinterpret_cast<int32_t*>(ws);
   ws += align_up((size_t)num_pages * 4, 256);
   prm.count = reinterpret_cast<int32_t*>(ws);
-  prm.counts = prm.count + 4;
+  prm.tickets = prm.count + 4;
+  prm.counts = prm.tickets + kMaxLaunches;
   ws += 256;
   prm.rank = reinterpret_cast<int32_t*>(ws);
   prm.src = reinterpret_cast<int32_t*>(ws + list);
@@ -1338,7 +1339,7 @@ extern "C" fa_status fa_pages_fork(const fa_pool* pools, int n_pools, const int3
   prm.num_pages = num_pages;
   fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  return launch_copies(pools, n_pools, prm.src, prm.dst, prm.count, st);
+  return launch_copies(pools, n_pools, prm.src, prm.dst, prm.count, prm.tickets, st);
 }
 
 extern "C" fa_status fa_pages_compact(const fa_pool* pools, int n_pools, const int32_t* block_table,
@@ -1363,7 +1364,8 @@ extern "C" fa_status fa_pages_compact(const fa_pool* pools, int n_pools, const i
   prm.mark = reinterpret_cast<int32_t*>(ws);
   ws += align_up((size_t)num_pages * 4, 256);
   prm.count = reinterpret_cast<int32_t*>(ws);
-  prm.counts = prm.count + 4;
+  prm.tickets = prm.count + 4;
+  prm.counts = prm.tickets + kMaxLaunches;
   ws += 256;
   prm.src = reinterpret_cast<int32_t*>(ws);
   prm.dst = reinterpret_cast<int32_t*>(ws + list);
@@ -1373,5 +1375,5 @@ extern "C" fa_status fa_pages_compact(const fa_pool* pools, int n_pools, const i
   prm.num_pages = num_pages;
   compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(prm);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  return launch_copies(pools, n_pools, prm.src, prm.dst, prm.count, st);
+  return launch_copies(pools, n_pools, prm.src, prm.dst, prm.count, prm.tickets, st);
 }

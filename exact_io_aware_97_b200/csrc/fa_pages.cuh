@@ -21,7 +21,7 @@
 
 namespace fa {
 
-constexpr int kMaxPools = 128;
+constexpr int kMaxPools = 128, kMaxLaunches = 32;  // pools of a launch, launches
 constexpr int kFreeMark = 0x7FFFFFFF;
 
 struct PoolList {
@@ -40,6 +40,7 @@ struct ForkParams {
   int32_t *rank;          // [R]: number of the copy that row i needs, or -1
   int32_t *src, *dst;     // [R]: the copies
   int32_t *count;         // number of copies
+  int32_t *tickets;       // [kMaxLaunches]: next piece to copy, for each launch of the copies
   int32_t *counts;        // per CTA of the planning cluster
   int B, R, max_pages, page_shift, num_pages;
 };
@@ -49,7 +50,7 @@ struct CompactParams {
   int32_t *table_out, *n_live;
   int32_t *mark;       // [num_pages]
   int32_t *src, *dst;  // [num_pages / 2 + 1]
-  int32_t *count, *counts;
+  int32_t *count, *counts, *tickets;
   int B, max_pages, page_shift, num_pages;
 };
 
@@ -128,7 +129,16 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork
   const int psm = (1 << p.page_shift) - 1;
   // the copies' blocks may come to the idle SMs now; they wait for this kernel's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid < kMaxLaunches) p.tickets[tid] = 0;
   for (int g = tid; g < p.num_pages; g += threads) p.mark[g] = kFreeMark;
+  // this thread's first row of the steps after the marks; lookups that fill the cache meanwhile
+  const int i0 = plan_begin(p.R, cta), i1 = plan_begin(p.R, cta + 1);
+  const int mine_i = i0 + threadIdx.x, mine_tail = mine_i < i1 ? fork_tail(p, mine_i) : -1;
+  auto tail = [&](int i) { return i == mine_i ? mine_tail : i < i1 ? fork_tail(p, i) : -1; };
+  if (p.R > 0) {
+    int b;
+    (void)fork_len(p, (cta * 32 + warp) / ((p.max_pages + 127) / 128) % p.R, &b);
+  }
   cluster_sync();
   // mark[page]: -1 where some new row holds it full, else the first new row that ends in it; a
   // warp takes 128 entries of a row, all loaded before the first is marked
@@ -146,21 +156,23 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork
       if (t0 + 32 * j < np && pages_ok(page[j], p.num_pages))
         atomicMin(p.mark + page[j], t0 + 32 * j < full ? -1 : i);
   }
-  // this thread's first row of the next steps, looked up behind the marks
-  const int i0 = plan_begin(p.R, cta), i1 = plan_begin(p.R, cta + 1);
-  const int mine_i = i0 + threadIdx.x, mine_tail = mine_i < i1 ? fork_tail(p, mine_i) : -1;
-  auto tail = [&](int i) { return i == mine_i ? mine_tail : i < i1 ? fork_tail(p, i) : -1; };
   cluster_sync();
   // count the copies that this CTA's rows need and the free pages in its part of the pool
   auto needs_copy = [&](int i, int page) { return page >= 0 && page < p.num_pages && __ldcg(p.mark + page) != i; };
   const int g0 = plan_begin(p.num_pages, cta), g1 = plan_begin(p.num_pages, cta + 1);
-  int copies = 0, frees = 0, total;
-  for (int at = i0; at < i1; at += kPlanThreads) {
+  // (what the first round of each count finds is kept for the ranks below)
+  const int mine_g = g0 + threadIdx.x;
+  const bool mine_free = mine_g < g1 && __ldcg(p.mark + mine_g) == kFreeMark;
+  const bool mine_copy = mine_i < i1 && needs_copy(mine_i, mine_tail);
+  int copies, frees, total;
+  const int mine_copy_rank = block_rank(mine_copy, sm, &copies), mine_free_rank = block_rank(mine_free, sm, &frees);
+  const int first_copies = copies, first_frees = frees;
+  for (int at = i0 + kPlanThreads; at < i1; at += kPlanThreads) {
     const int i = at + threadIdx.x;
     block_rank(i < i1 && needs_copy(i, tail(i)), sm, &total);
     copies += total;
   }
-  for (int at = g0; at < g1; at += kPlanThreads) {
+  for (int at = g0 + kPlanThreads; at < g1; at += kPlanThreads) {
     const int g = at + threadIdx.x;
     block_rank(g < g1 && __ldcg(p.mark + g) == kFreeMark, sm, &total);
     frees += total;
@@ -172,22 +184,29 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork
   cluster_sync();
   int need, have;
   int r = plan_before(p.counts, cta, &need), f = plan_before(p.counts + kPlanCtas, cta, &have);
-  for (int at = i0; at < i1; at += kPlanThreads) {
+  auto take_copy = [&](int i, int page, bool copy, int k) {
+    if (i < i1) p.rank[i] = copy ? k : -1;
+    if (copy) p.src[k] = page;
+  };
+  auto take_free = [&](int g, bool is_free, int k) {
+    if (!is_free) return;
+    if (k < need) p.dst[k] = g;
+    else p.free_pages[k - need] = g;
+  };
+  take_copy(mine_i, mine_tail, mine_copy, r + mine_copy_rank);
+  take_free(mine_g, mine_free, f + mine_free_rank);
+  r += first_copies;
+  f += first_frees;
+  for (int at = i0 + kPlanThreads; at < i1; at += kPlanThreads) {
     const int i = at + threadIdx.x, page = tail(i);
     const bool copy = i < i1 && needs_copy(i, page);
-    const int mine = r + block_rank(copy, sm, &total);
-    if (i < i1) p.rank[i] = copy ? mine : -1;
-    if (copy) p.src[mine] = page;
+    take_copy(i, page, copy, r + block_rank(copy, sm, &total));
     r += total;
   }
-  for (int at = g0; at < g1; at += kPlanThreads) {
+  for (int at = g0 + kPlanThreads; at < g1; at += kPlanThreads) {
     const int g = at + threadIdx.x;
     const bool is_free = g < g1 && __ldcg(p.mark + g) == kFreeMark;
-    const int mine = f + block_rank(is_free, sm, &total);
-    if (is_free) {
-      if (mine < need) p.dst[mine] = g;
-      else p.free_pages[mine - need] = g;
-    }
+    take_free(g, is_free, f + block_rank(is_free, sm, &total));
     f += total;
   }
   const int left = max(have - need, 0);
@@ -226,6 +245,7 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) comp
   const int psm = (1 << p.page_shift) - 1;
   // the copies' blocks may come to the idle SMs now; they wait for this kernel's end
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid < kMaxLaunches) p.tickets[tid] = 0;
   for (int g = tid; g < p.num_pages; g += threads) p.mark[g] = kFreeMark;
   cluster_sync();
   const int strips = (p.max_pages + 127) / 128;  // a warp takes 128 entries of a row
@@ -352,7 +372,7 @@ struct CopyWalk {
 
 __global__ void __launch_bounds__(kCopyThreads + 32, 2)
     pages_copy_kernel(const __grid_constant__ PoolList pools, const int32_t* src, const int32_t* dst,
-                      const int32_t* count) {
+                      const int32_t* count, int32_t* next) {
   extern __shared__ uint8_t smem_raw[];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = *count;
@@ -372,36 +392,45 @@ __global__ void __launch_bounds__(kCopyThreads + 32, 2)
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem_raw + kBulkStages * kBulkBytes);
   for (int s = 0; s < kBulkStages; ++s) mbar_init(full + s, 1);
   fence_barrier_init();
-  // `ahead` loads, `w` stores: the store of piece i follows its load, and the load of piece
-  // i + kBulkStages - 1 the store of piece i - 1, once that has read its slot
-  CopyWalk ahead{0, pools.bulk, blockIdx.x, 0}, w = ahead;
-  auto where = [&](const CopyWalk& c, const int32_t* pages_of, unsigned& bytes) {
-    const unsigned pieces = pools.pieces[c.pool];
-    const long long it = c.it - c.first, k = it / pieces, piece = it - k * pieces;
-    const unsigned long long page = (unsigned long long)pools.vpp[c.pool] * 16;
-    bytes = (unsigned)min(page - piece * kBulkBytes, (unsigned long long)kBulkBytes);
-    return pools.base[c.pool] + (unsigned long long)__ldg(pages_of + k) * page + piece * kBulkBytes;
-  };
+  // Pieces are handed out by a counter (dealt in equal shares, the first CTA was done at 136 us of
+  // 185); which CTA copies a piece changes nothing in the result.  The next ticket is drawn while
+  // the last one's piece is loaded.
+  CopyWalk walk{0, pools.bulk, 0, 0};
+  uint8_t* to[kBulkStages];
+  unsigned bytes[kBulkStages];
+  long long ticket = atomicAdd(next, 1);
   auto load = [&](int slot) {
-    if (!ahead.next(pools, n)) return;
-    unsigned bytes;
-    const uint8_t* from = where(ahead, src, bytes);
-    mbar_arrive_expect_tx(full + slot, bytes);
-    bulk_load(smem_raw + slot * kBulkBytes, from, bytes, full + slot);
-    ahead.it += gridDim.x;
+    bytes[slot] = 0;
+    walk.it = ticket;
+    if (!walk.next(pools, n)) return;
+    ticket = atomicAdd(next, 1);
+    const unsigned pieces = pools.pieces[walk.pool];
+    const long long it = walk.it - walk.first, k = it / pieces, piece = it - k * pieces;
+    const unsigned long long page = (unsigned long long)pools.vpp[walk.pool] * 16;
+    uint8_t* const base = pools.base[walk.pool] + piece * kBulkBytes;
+    bytes[slot] = (unsigned)min(page - piece * kBulkBytes, (unsigned long long)kBulkBytes);
+    to[slot] = base + (unsigned long long)__ldg(dst + k) * page;
+    mbar_arrive_expect_tx(full + slot, bytes[slot]);
+    bulk_load(smem_raw + slot * kBulkBytes, base + (unsigned long long)__ldg(src + k) * page, bytes[slot], full + slot);
   };
+  // the store of a piece follows its load; the load of the piece five further on follows the store
+  // of the one before, once that has read its slot
+#pragma unroll
   for (int s = 0; s < kBulkStages - 1; ++s) load(s);
-  int slot = 0;
-  uint32_t phase = 0;
-  for (; w.next(pools, n); w.it += gridDim.x) {
-    bulk_wait_group_read0();  // the slot before this one is free: all stores so far have read theirs
-    load(slot == 0 ? kBulkStages - 1 : slot - 1);
-    unsigned bytes;
-    uint8_t* to = where(w, dst, bytes);
-    if (!mbar_wait(full + slot, phase)) break;
-    bulk_store(to, smem_raw + slot * kBulkBytes, bytes);
-    bulk_commit_group();
-    if (++slot == kBulkStages) slot = 0, phase ^= 1u;
+  bool ok = true;
+  for (uint32_t phase = 0; ok; phase ^= 1u) {
+#pragma unroll
+    for (int s = 0; s < kBulkStages; ++s) {
+      if (ok) {
+        bulk_wait_group_read0();
+        load((s + kBulkStages - 1) % kBulkStages);
+        ok = bytes[s] != 0 && mbar_wait(full + s, phase);
+      }
+      if (ok) {
+        bulk_store(to[s], smem_raw + s * kBulkBytes, bytes[s]);
+        bulk_commit_group();
+      }
+    }
   }
   bulk_wait_group0();
 }

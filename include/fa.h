@@ -356,7 +356,7 @@ typedef struct {
  * that the copies took (the lowest ones, in the order of the new sequences), then -1;
  * n_free [1] their number.  Entries of a row past the sequence's pages become -1.
  * Pages are copied in every pool of `pools` (a HOST array of n_pools; any element types; 0 pools:
- * tables only; pages under 2^31 bytes).  block_table [B, max_pages_per_seq], block_table_out [B_out, max_pages_per_seq],
+ * tables only; at most 4096; pages under 2^31 bytes).  block_table [B, max_pages_per_seq], block_table_out [B_out, max_pages_per_seq],
  * all device int32; outputs must not overlap inputs.  page_size is a power of two.
  * Recorded for fa_last_device_error (FA_ERR_INVALID_ARG): a parent outside [-1, B) (taken as
  * -1), a length that is negative or past the table (taken as 0), an entry outside [0, num_pages)

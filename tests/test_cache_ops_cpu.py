@@ -126,7 +126,7 @@ def test_pages_reject_before_launch(lib):
                    dict(sl=None), dict(bt=514), dict(sl=513), dict(bto=None), dict(bto=1026), dict(bto=512),
                    dict(B=-1), dict(P=0), dict(ps=0), dict(maxp=0)):
             assert st(**kw) == BAD, kw
-        for kw in (dict(ps=24), dict(maxp=1 << 28), dict(P=0x7FFFFFFF), dict(p=pools((256, 1 << 31)))):
+        for kw in (dict(ps=24), dict(maxp=1 << 28), dict(P=0x7FFFFFFF), dict(p=pools((256, 1 << 31))), dict(n=4097, p=pools(*[(256, 16)] * 4097))):
             assert st(**kw) == UNS, kw
         for kw in (dict(ws=None), dict(wsb=100), dict(ws=260)):
             assert st(**kw) == WS, kw

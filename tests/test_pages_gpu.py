@@ -82,6 +82,7 @@ FORKS = [
     ([100, 200, 300], [], 32, 3, [(16,)]),
     ([1, 64, 65, 127], [3, 1, 3, 0, 2, 3, 0], 64, 9, [(64, 33), (4,)]),
     ([1000] * 7 + [17], list(range(8)) * 9, 16, 70, [(2048,)]),
+    ([300, 77, 128], [0, 0, 1, 1, 2, 2], 128, 4, [(128, 321), (40016,), (5000,)]),
     ([31] * 300, [i // 4 for i in range(1200)], 8, 1500, [(48,), (20,)]),
 ]
 
@@ -150,6 +151,7 @@ COMPACTS = [
     ([0, 0], 16, 5, [(16,)]),
     ([100, 0, 33, 1], 16, 30, [(640,), (7,), (12,)]),
     ([64] * 40, 64, 40, [(4096,)]),
+    ([700, 130, 1], 128, 9, [(128, 321), (40016,), (16384,)]),
     ([3000, 17, 900], 16, 2000, [(48,), (20,)]),
     ([5] * 2000, 8, 2100, [(4,)]),
 ]
@@ -180,8 +182,11 @@ def test_many_pools_and_unaligned_ones():
     lens, ps = [40, 3, 25], 16
     table, P = layout(rng, lens, ps, 8)
     parent = [0, 0, 1, 1, 2, 2]
-    raw = [torch.from_numpy(rng.integers(0, 256, 1 + P * 33, dtype=np.uint8)).cuda() for _ in range(300)]
-    pools = [r[(1 if j % 3 == 0 else 0):][:P * (32 if j % 3 else 33)].view(P, -1) for j, r in enumerate(raw)]
+    pools = []
+    for j in range(300):
+        size = (33, 32, 4096, 20000)[j % 4]  # two of them large enough for bulk copies
+        raw = torch.from_numpy(rng.integers(0, 256, 1 + P * size, dtype=np.uint8)).cuda()
+        pools.append(raw[j % 5 == 0:][:P * size].view(P, size))
     before = [p.clone() for p in pools]
     t, n, free, moves = fork_model(table, np.array(lens), parent, ps, P)
     gt, *_ = fa.pages_fork(pools, dev(table), dev(lens), dev(parent), ps)
