@@ -328,21 +328,22 @@ def fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d) -> int:
 
 def _pool_array(pools, num_pages):
     """fa_pool array of tensors [num_pages, ...]; raw (address, page_bytes) pairs pass through."""
-    arr = (FaPool * max(1, len(pools)))()
+    flat = []
     for n, t in enumerate(pools):
         if isinstance(t, tuple):
-            arr[n].base, arr[n].page_bytes = t
+            flat += t
             continue
         if t.dim() < 1 or t.shape[0] != num_pages:
             raise ValueError(f"pool {n}: expected [{num_pages}, ...], got shape {tuple(t.shape)}")
-        arr[n].base, arr[n].page_bytes = _ptr(t), t.numel() // num_pages * t.element_size()
-    return ctypes.cast(arr, ctypes.c_void_p) if len(pools) else None, arr
+        if not t.is_cuda or not t.is_contiguous():
+            _ptr(t)  # says what is wrong
+        flat += (t.data_ptr(), t.nbytes // num_pages)
+    return (ctypes.c_uint64 * len(flat))(*flat) if flat else None
 
 
 def fa_pages_fork(pools, block_table, seqlens, parent, block_table_out, seqlens_out, free_pages, n_free, B, B_out,
                   num_pages, page_size, max_pages_per_seq, workspace, workspace_bytes, stream=None) -> None:
-    ptr, _keep = _pool_array(pools, int(num_pages))
-    st = load().fa_pages_fork(ptr, len(pools), _ptr_i32(block_table, "block_table"), _ptr_i32(seqlens, "seqlens"),
+    st = load().fa_pages_fork(_pool_array(pools, int(num_pages)), len(pools), _ptr_i32(block_table, "block_table"), _ptr_i32(seqlens, "seqlens"),
                               _ptr_i32(parent, "parent"), _ptr_i32(block_table_out, "block_table_out"),
                               _ptr_i32(seqlens_out, "seqlens_out"), _ptr_i32(free_pages, "free_pages"),
                               _ptr_i32(n_free, "n_free"), int(B), int(B_out), int(num_pages), int(page_size),
@@ -352,8 +353,7 @@ def fa_pages_fork(pools, block_table, seqlens, parent, block_table_out, seqlens_
 
 def fa_pages_compact(pools, block_table, seqlens, block_table_out, n_live, B, num_pages, page_size,
                      max_pages_per_seq, workspace, workspace_bytes, stream=None) -> None:
-    ptr, _keep = _pool_array(pools, int(num_pages))
-    st = load().fa_pages_compact(ptr, len(pools), _ptr_i32(block_table, "block_table"),
+    st = load().fa_pages_compact(_pool_array(pools, int(num_pages)), len(pools), _ptr_i32(block_table, "block_table"),
                                  _ptr_i32(seqlens, "seqlens"), _ptr_i32(block_table_out, "block_table_out"),
                                  _ptr_i32(n_live, "n_live"), int(B), int(num_pages), int(page_size),
                                  int(max_pages_per_seq), _ptr(workspace), int(workspace_bytes), _stream(stream))
@@ -648,49 +648,51 @@ def _row_stride(t, what: str) -> int:
 
 def _rope(q, k, freqs, positions, interleaved, amplitude, q_out, k_out, stream, backward):
     import torch
-    if q.dim() not in (3, 4) or q.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"q: expected bf16 or fp32 [B, N, Hq, d] or [total, Hq, d], got {q.dtype} {tuple(q.shape)}")
-    shape = q.shape
-    Hq, d = shape[-2:]
-    rows = q.numel() // max(1, Hq * d)
+    dt, qs = q.dtype, q.shape
+    if len(qs) not in (3, 4) or (dt != torch.bfloat16 and dt != torch.float32):
+        raise ValueError(f"q: expected bf16 or fp32 [B, N, Hq, d] or [total, Hq, d], got {dt} {tuple(qs)}")
+    period, Hq, d = qs[-3:]
+    rows = period if len(qs) == 3 else period * qs[0]
+    Hk = 0
     if k is not None:
-        if k.dtype != q.dtype or k.dim() != q.dim() or k.shape[:-2] != shape[:-2] or k.shape[-1] != d:
-            raise ValueError(f"k: expected {q.dtype} {tuple(shape[:-2])} + (Hkv, {d}) like q, got {k.dtype} "
-                             f"{tuple(k.shape)}")
+        ks = k.shape
+        Hk = ks[-2] if len(ks) > 1 else 0
+        if k.dtype != dt or ks != (*qs[:-2], Hk, d):
+            raise ValueError(f"k: expected {dt} {tuple(qs[:-2])} + (Hkv, {d}) like q, got {k.dtype} {tuple(ks)}")
     elif k_out is not None:
         raise ValueError("k_out given without k")
     rot = 2 * freqs.numel()
-    if freqs.dim() != 1 or freqs.dtype != torch.float64 or not 0 < rot <= d:
-        raise ValueError(f"freqs: expected float64 [rot_dim / 2] with rot_dim <= {d}, got {freqs.dtype} "
+    if freqs.dtype != torch.float64 or not 0 < rot <= d or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError(f"freqs: expected dense float64 [rot_dim / 2] with rot_dim <= {d}, got {freqs.dtype} "
                          f"{tuple(freqs.shape)}")
-    if positions is not None and (positions.numel() != rows or
-                                  (positions.dim() != 1 and positions.shape != shape[:-2])):
-        raise ValueError(f"positions: expected {tuple(shape[:-2])} or [{rows}], got shape {tuple(positions.shape)}")
-    for t, like, what in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if t is not None and (t.shape != like.shape or t.dtype != like.dtype):
-            raise ValueError(f"{what}: expected {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
+    if positions is not None:
+        if positions.numel() != rows or (positions.dim() != 1 and positions.shape != qs[:-2]):
+            raise ValueError(f"positions: expected {tuple(qs[:-2])} or [{rows}], got shape {tuple(positions.shape)}")
+        if positions.dtype != torch.int32 or not positions.is_contiguous():
+            raise ValueError(f"positions: expected a dense int32 tensor, got {positions.dtype}, strides "
+                             f"{tuple(positions.stride())}")
+    if q_out is not None and (q_out.shape != qs or q_out.dtype != dt):
+        raise ValueError(f"q_out: expected {dt} {tuple(qs)}, got {q_out.dtype} {tuple(q_out.shape)}")
+    if k_out is not None and (k_out.shape != ks or k_out.dtype != dt):
+        raise ValueError(f"k_out: expected {dt} {tuple(ks)}, got {k_out.dtype} {tuple(k_out.shape)}")
     idx = _home(q, k, freqs, positions, q_out, k_out)
-    _dense(freqs=freqs, positions=positions)
-    _is_i32(positions=positions)
+    # like the input where that is dense; empty_like would keep the strides of a slice's dimensions
+    if q_out is None:
+        q_out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(qs)
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k) if k.is_contiguous() else k.new_empty(ks)
+    if rows == 0:
+        return q_out, k_out
 
     def call():
-        yq = q_out if q_out is not None else torch.empty(shape, dtype=q.dtype, device=q.device)
-        yk = k_out
-        if yk is None and k is not None:
-            yk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        if rows > 0:
-            sq, syq, sk, syk = _row_stride(q, "q"), _row_stride(yq, "q_out"), 0, 0
-            if k is not None:
-                sk, syk = _row_stride(k, "k"), _row_stride(yk, "k_out")
-            st = load().fa_rope(q.data_ptr(), None if k is None else k.data_ptr(), yq.data_ptr(),
-                                None if k is None else yk.data_ptr(),
-                                None if positions is None else positions.data_ptr(), freqs.data_ptr(), rows, shape[-3],
-                                Hq, 0 if k is None else k.shape[-2], d, rot, 1 if interleaved else 0, amplitude,
-                                1 if backward else 0, FA_BF16 if q.dtype == torch.bfloat16 else FA_F32, sq, sk, syq,
-                                syk, _stream(stream))
-            _check(st, "fa_rope")
-        return yq, yk
-    return _at(idx, call)
+        _check(load().fa_rope(q.data_ptr(), k.data_ptr() if Hk else None, q_out.data_ptr(),
+                              k_out.data_ptr() if Hk else None, None if positions is None else positions.data_ptr(),
+                              freqs.data_ptr(), rows, period, Hq, Hk, d, rot, 1 if interleaved else 0, amplitude,
+                              1 if backward else 0, FA_BF16 if dt == torch.bfloat16 else FA_F32, _row_stride(q, "q"),
+                              _row_stride(k, "k") if Hk else 0, _row_stride(q_out, "q_out"),
+                              _row_stride(k_out, "k_out") if Hk else 0, _stream(stream)), "fa_rope")
+    _at(idx, call)
+    return q_out, k_out
 
 
 def rope(q, k, freqs, positions=None, interleaved=False, amplitude=1.0, q_out=None, k_out=None, stream=None):
@@ -710,12 +712,12 @@ def rope_backward(dq, dk, freqs, positions=None, interleaved=False, amplitude=1.
 def _cache8(k_pages, v_pages, k_scale, v_scale, block_table, seqlens):
     """Checks an e4m3 paged cache; returns (B, num_pages, page_size, max_pages, Hkv, d, scale_block)."""
     import torch
-    if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.dim() != 4 or \
-            k_pages.dtype not in (torch.float8_e4m3fn, torch.uint8):
+    shape, dt, ks = k_pages.shape, k_pages.dtype, k_scale.shape
+    if shape != v_pages.shape or dt != v_pages.dtype or len(shape) != 4 or \
+            (dt != torch.float8_e4m3fn and dt != torch.uint8):
         raise ValueError(f"k_pages, v_pages: expected two e4m3 (or byte) [num_pages, page_size, Hkv, d], got "
-                         f"{k_pages.dtype} {tuple(k_pages.shape)} and {v_pages.dtype} {tuple(v_pages.shape)}")
-    num_pages, page_size, Hkv, d = k_pages.shape
-    ks = k_scale.shape
+                         f"{dt} {tuple(shape)} and {v_pages.dtype} {tuple(v_pages.shape)}")
+    num_pages, page_size, Hkv, d = shape
     if ks != v_scale.shape or len(ks) != 3 or ks[0] != num_pages or ks[1] != Hkv or ks[2] <= 0 or \
             page_size % ks[2] != 0 or k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
         raise ValueError(f"k_scale, v_scale: expected two float32 [{num_pages}, {Hkv}, page_size / scale_block], got "
@@ -725,9 +727,11 @@ def _cache8(k_pages, v_pages, k_scale, v_scale, block_table, seqlens):
     B, maxp = block_table.shape
     if seqlens.dim() != 1 or seqlens.shape[0] != B:
         raise ValueError(f"seqlens: expected {B} entries, got shape {tuple(seqlens.shape)}")
-    _is_i32(block_table=block_table, seqlens=seqlens)
-    _dense(k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
-           seqlens=seqlens)
+    if block_table.dtype != torch.int32 or seqlens.dtype != torch.int32:
+        raise ValueError(f"block_table, seqlens: expected int32 tensors, got {block_table.dtype} and {seqlens.dtype}")
+    if not (k_pages.is_contiguous() and v_pages.is_contiguous() and k_scale.is_contiguous() and
+            v_scale.is_contiguous() and block_table.is_contiguous() and seqlens.is_contiguous()):
+        raise ValueError("expected contiguous tensors: pages, scales, block_table, seqlens")
     return B, num_pages, page_size, maxp, Hkv, d, page_size // ks[2]
 
 
@@ -749,8 +753,11 @@ def cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seql
     elif cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != B + 1:
         raise ValueError(f"cu_seqlens: expected [B + 1 = {B + 1}] offsets, got shape {tuple(cu_seqlens.shape)}")
     idx = _home(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, cu_seqlens)
-    _is_i32(cu_seqlens=cu_seqlens)
-    _dense(k=k, v=v, cu_seqlens=cu_seqlens)
+    if not (k.is_contiguous() and v.is_contiguous()):
+        raise ValueError(f"k, v: expected contiguous tensors, got strides {tuple(k.stride())} and {tuple(v.stride())}")
+    if cu_seqlens is not None:
+        _is_i32(cu_seqlens=cu_seqlens)
+        _dense(cu_seqlens=cu_seqlens)
 
     def call():
         _check(load().fa_cache_append_fp8(k.data_ptr(), v.data_ptr(),
@@ -779,18 +786,23 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens
     lse_shape = (B, Hq) if q.dim() == 3 else (B, Hq, Nq)
     if scale is None:
         scale = d ** -0.5
-    _expect(out, shape, "torch.bfloat16", "out")
-    _expect(lse, lse_shape, "torch.float32", "lse")
+    if out is not None:
+        _expect(out, shape, "torch.bfloat16", "out")
+    if lse is not None:
+        _expect(lse, lse_shape, "torch.float32", "lse")
     idx = _home(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace)
-    _dense(q=q, out=out, lse=lse, workspace=workspace)
+    if not q.is_contiguous():
+        raise ValueError(f"q: expected a contiguous tensor, got strides {tuple(q.stride())} for shape {tuple(shape)}")
+    if out is not None or lse is not None or workspace is not None:
+        _dense(out=out, lse=lse, workspace=workspace)
 
     def call():
         lib = load()
         o = out if out is not None else torch.empty_like(q)
-        ml = lse if lse is not None else torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+        ml = lse if lse is not None else q.new_empty(lse_shape, dtype=torch.float32)
         if workspace is None:
             nbytes = lib.fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d)
-            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+            ws = q.new_empty(max(nbytes, 1), dtype=torch.uint8)
         else:
             ws, nbytes = workspace, workspace.numel() * workspace.element_size()
         if B > 0 and Nq > 0 and Hq > 0:
@@ -832,16 +844,20 @@ def pages_fork(pools, block_table, seqlens, parent, page_size, num_pages=None, w
     _dense(parent=parent, workspace=workspace)
 
     def call():
+        lib = load()
+        arr = _pool_array(pools, num_pages)
         # one allocation for the four results
-        buf = torch.empty(R * (maxp + 1) + num_pages + 1, dtype=torch.int32, device=block_table.device)
-        table, lens, free, n_free = buf.split([R * maxp, R, num_pages, 1])
-        table = table.view(R, maxp)
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(fa_pages_workspace_size(num_pages, R), dtype=torch.uint8, device=block_table.device)
-        fa_pages_fork(pools, block_table, seqlens, parent, table, lens, free, n_free, B, R, num_pages, page_size, maxp,
-                      ws, ws.numel() * ws.element_size(), stream)
-        return table, lens, free, n_free
+        buf = block_table.new_empty(R * (maxp + 1) + num_pages + 1)
+        table, lens, free, n_free = buf.split((R * maxp, R, num_pages, 1))
+        if workspace is None:
+            nbytes = lib.fa_pages_workspace_size(num_pages, R)
+            ws = block_table.new_empty(max(nbytes, 1), dtype=torch.uint8)
+        else:
+            ws, nbytes = workspace, workspace.numel() * workspace.element_size()
+        _check(lib.fa_pages_fork(arr, len(pools), block_table.data_ptr(), seqlens.data_ptr(), parent.data_ptr(),
+                                 table.data_ptr(), lens.data_ptr(), free.data_ptr(), n_free.data_ptr(), B, R,
+                                 num_pages, page_size, maxp, ws.data_ptr(), nbytes, _stream(stream)), "fa_pages_fork")
+        return table.view(R, maxp), lens, free, n_free
     return _at(_home(block_table, seqlens, parent, workspace, *pools), call)
 
 
@@ -852,12 +868,16 @@ def pages_compact(pools, block_table, seqlens, page_size, num_pages=None, worksp
     _dense(workspace=workspace)
 
     def call():
-        table = torch.empty((B, maxp), dtype=torch.int32, device=block_table.device)
-        n_live = torch.empty(1, dtype=torch.int32, device=block_table.device)
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(fa_pages_workspace_size(num_pages), dtype=torch.uint8, device=block_table.device)
-        fa_pages_compact(pools, block_table, seqlens, table, n_live, B, num_pages, page_size, maxp, ws,
-                         ws.numel() * ws.element_size(), stream)
+        lib = load()
+        arr = _pool_array(pools, num_pages)
+        table, n_live = torch.empty_like(block_table), block_table.new_empty(1)
+        if workspace is None:
+            nbytes = lib.fa_pages_workspace_size(num_pages, 0)
+            ws = block_table.new_empty(max(nbytes, 1), dtype=torch.uint8)
+        else:
+            ws, nbytes = workspace, workspace.numel() * workspace.element_size()
+        _check(lib.fa_pages_compact(arr, len(pools), block_table.data_ptr(), seqlens.data_ptr(), table.data_ptr(),
+                                    n_live.data_ptr(), B, num_pages, page_size, maxp, ws.data_ptr(), nbytes,
+                                    _stream(stream)), "fa_pages_compact")
         return table, n_live
     return _at(_home(block_table, seqlens, workspace, *pools), call)
