@@ -13,6 +13,7 @@
 #include "fa_bwd_sm100.cuh"
 #include "fa_cache.cuh"
 #include "fa_decode_fp8.cuh"
+#include "fa_decode_fp8_tc.cuh"
 #include "fa_decode_sm100.cuh"
 #include "fa_fwd_sm100.cuh"
 #include "fa_pages.cuh"
@@ -1070,40 +1071,39 @@ fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// One wave of CTAs: what a device without a known SM count would be given is the B200's.
-int dec8_ctas(int rows) {
-  const int sms = sm_count_cached();
-  return (sms > 0 ? sms : 148) * (rows <= 32 ? 2 : 1);
-}
-int dec8_tile(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Query rows of a unit: one tensor-core tile of 16 where that holds them; else the kernel on tcgen05
+// products with 64 (d = 128: 40 rows in TCNEW us instead of 205 with 64 rows in registers), or
+// registers for 32 or 64 (d = 64, where a cache row is too short for those products' 128 rows).
+int dec8_tile(int64_t rows, int d) { return rows <= 16 ? 16 : rows <= 32 && d == 64 ? 32 : 64; }
 // K/V heads of a unit, as a shift: one where the query rows fill more than a tile (the products,
 // not the loads, take the time then, and one head's queries are all that shared memory holds).
-int dec8_heads(int rows, int Hkv) { return rows > 16 ? 0 : Hkv % 4 == 0 ? 2 : Hkv % 2 == 0 ? 1 : 0; }
+int dec8_heads(int tile, int Hkv) { return tile > 16 ? 0 : Hkv % 4 == 0 ? 2 : Hkv % 2 == 0 ? 1 : 0; }
+// One wave of CTAs (where no device is present, the number of the B200's).
+int dec8_ctas(int tile) {
+  const int sms = sm_count_cached();
+  return (sms > 0 ? sms : 148) * (tile <= 32 ? 2 : 1);
+}
 
-template <int D, int MT, int RG>
-fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& prm, cudaStream_t st) {
-  using C = Dec8Cfg<D, MT, RG>;
-  CUtensorMap maps[2];
+bool dec8_maps(CUtensorMap (&maps)[2], const void* kp, const void* vp, int d, const Dec8Params& prm) {
   EncodeTiledFn enc = get_encode_fn();
-  if (!enc) return FA_ERR_CUDA;
-  const cuuint64_t dims[3] = {D, (cuuint64_t)prm.num_pages << prm.page_shift, (cuuint64_t)prm.Hkv};
-  const cuuint64_t strides[2] = {(cuuint64_t)prm.Hkv * D, D};
-  const cuuint32_t box[3] = {D, (cuuint32_t)prm.box, 1u << prm.hs}, estr[3] = {1, 1, 1};
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)prm.num_pages << prm.page_shift, (cuuint64_t)prm.Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)prm.Hkv * d, (cuuint64_t)d};
+  const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)prm.box, 1u << prm.hs}, estr[3] = {1, 1, 1};
   for (int w = 0; w < 2; ++w)
     if (enc(&maps[w], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(w ? vp : kp), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return FA_ERR_CUDA;
-  auto kern = fa_decode_fp8_kernel<D, MT, RG>;
-  static std::atomic<uint64_t> smem_set{0};  // a bit for each device
-  if (!set_smem_once(kern, C::kSmem, smem_set)) return FA_ERR_CUDA;
-  const int ctas = dec8_ctas(prm.rows);
-  kern<<<ctas, C::kThreads, C::kSmem, st>>>(maps[0], maps[1], prm);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+      return false;
+  return true;
+}
+
+template <int D, int R>
+fa_status launch_decode_fp8_merge(const Dec8Params& prm, int ctas, cudaStream_t st) {
   // No unit can be cut where the longest sequence that the table holds is short.
   if ((prm.cap - 1 >> (7 - prm.hs)) + 1 <= kDec8Whole) return FA_OK;
   // The merge starts on the SMs that the last CTAs leave and waits there for their results.
-  const int items = std::min(prm.rows, C::kRows) << prm.hs, gx = prm.by_unit ? prm.B * prm.units : ctas;
+  const int items = std::min(prm.rows, R) << prm.hs, gx = prm.by_unit ? prm.B * prm.units : ctas;
   const bool wide = (int64_t)gx * items <= 8ll * ctas;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1114,9 +1114,35 @@ fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& pr
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t err = wide ? cudaLaunchKernelEx(&cfg, fa_decode_fp8_combine_kernel<D, C::kRows, true>, prm)
-                               : cudaLaunchKernelEx(&cfg, fa_decode_fp8_combine_kernel<D, C::kRows, false>, prm);
+  const cudaError_t err = wide ? cudaLaunchKernelEx(&cfg, fa_decode_fp8_combine_kernel<D, R, true>, prm)
+                               : cudaLaunchKernelEx(&cfg, fa_decode_fp8_combine_kernel<D, R, false>, prm);
   return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D, int MT, int RG>
+fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& prm, cudaStream_t st) {
+  using C = Dec8Cfg<D, MT, RG>;
+  CUtensorMap maps[2];
+  if (!dec8_maps(maps, kp, vp, D, prm)) return FA_ERR_CUDA;
+  auto kern = fa_decode_fp8_kernel<D, MT, RG>;
+  static std::atomic<uint64_t> smem_set{0};  // a bit for each device
+  if (!set_smem_once(kern, C::kSmem, smem_set)) return FA_ERR_CUDA;
+  const int ctas = dec8_ctas(C::kRows);
+  kern<<<ctas, C::kThreads, C::kSmem, st>>>(maps[0], maps[1], prm);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return launch_decode_fp8_merge<D, C::kRows>(prm, ctas, st);
+}
+
+fa_status launch_decode_fp8_tc(const void* kp, const void* vp, const Dec8Params& prm, cudaStream_t st) {
+  using C = Dec8TcCfg;
+  CUtensorMap maps[2];
+  if (!dec8_maps(maps, kp, vp, C::D, prm)) return FA_ERR_CUDA;
+  static std::atomic<uint64_t> smem_set{0};
+  if (!set_smem_once(fa_decode_fp8_tc_kernel, C::kSmem, smem_set)) return FA_ERR_CUDA;
+  const int ctas = dec8_ctas(C::kRows);
+  fa_decode_fp8_tc_kernel<<<ctas, C::kThreads, C::kSmem, st>>>(maps[0], maps[1], prm);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  return launch_decode_fp8_merge<C::D, C::kRows>(prm, ctas, st);
 }
 
 }  // namespace
@@ -1157,8 +1183,7 @@ extern "C" fa_status fa_cache_append_fp8(const void* k, const void* v, const int
 extern "C" size_t fa_decode_paged_fp8_workspace_size(int B, int Nq, int Hq, int Hkv, int d) {
   if (B <= 0 || Nq <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0) return 0;
   // two parts per CTA (sums, then m and l) and a descriptor per CTA
-  const int64_t rows = (int64_t)Nq * (Hq / Hkv);
-  const int tile = rows > 32 ? 64 : dec8_tile((int)rows);
+  const int tile = dec8_tile((int64_t)Nq * (Hq / Hkv), d);
   const size_t ctas = (size_t)dec8_ctas(tile);
   const size_t slots = (2 * ctas * tile) << dec8_heads(tile, Hkv);
   return align_up(slots * d * 4, 256) + align_up(slots * 8, 256) + align_up(ctas * 16, 256);
@@ -1201,11 +1226,11 @@ extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, con
   prm.max_pages = max_pages_per_seq;
   prm.tau = (float)((double)scale * 1.4426950408889634074);
   prm.rows = (int)rows;
-  const int tile = dec8_tile(prm.rows);
+  const int tile = dec8_tile(rows, d);
   prm.tiles = (prm.rows + tile - 1) / tile;
-  prm.hs = dec8_heads(prm.rows, Hkv);
+  prm.hs = dec8_heads(tile, Hkv);
   prm.box = std::min(page_size, kDec8Keys >> prm.hs);
-  const size_t ctas = (size_t)dec8_ctas(prm.rows);
+  const size_t ctas = (size_t)dec8_ctas(tile);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   prm.ws_acc = reinterpret_cast<float*>(ws);
   const size_t slots = (2 * ctas * tile) << prm.hs;
@@ -1223,9 +1248,8 @@ extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, con
     return tile == 16   ? launch_decode_fp8<64, 1, 1>(k_pages, v_pages, prm, st)
            : tile == 32 ? launch_decode_fp8<64, 2, 1>(k_pages, v_pages, prm, st)
                         : launch_decode_fp8<64, 2, 2>(k_pages, v_pages, prm, st);
-  return tile == 16   ? launch_decode_fp8<128, 1, 1>(k_pages, v_pages, prm, st)
-         : tile == 32 ? launch_decode_fp8<128, 2, 1>(k_pages, v_pages, prm, st)
-                      : launch_decode_fp8<128, 2, 2>(k_pages, v_pages, prm, st);
+  return tile == 16 ? launch_decode_fp8<128, 1, 1>(k_pages, v_pages, prm, st)
+                    : launch_decode_fp8_tc(k_pages, v_pages, prm, st);
 }
 
 // ---------------------------------------------------------------------------------------

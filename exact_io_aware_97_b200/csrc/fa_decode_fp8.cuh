@@ -117,6 +117,104 @@ struct Dec8Walk {
   }
 };
 
+// What the CTAs share out among themselves, in shared memory.
+struct Dec8Share {
+  int2 scan[32];  // per warp: chunks, most chunks of a sequence
+  int b, u, skip[2];
+  int end, T, ctas;  // end of this CTA's share (without skip); all chunks; CTAs with a share
+};
+
+// This CTA's share of all chunks, by prefix sums over the sequences; synchronises the CTA.
+template <int THREADS>
+__device__ __forceinline__ Dec8Walk dec8_share(const Dec8Params& p, Dec8Share& sh) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (p.B + THREADS - 1) / THREADS;
+  const int b_lo = min((int)threadIdx.x * per, p.B), b_hi = min(b_lo + per, p.B);
+  auto chunks_of = [&](int b) { return dec8_len(p, b) + (kDec8Keys >> p.hs) - 1 >> (7 - p.hs); };
+  int mine = 0, most = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int n = chunks_of(b);
+    mine += n;
+    most = max(most, n);
+  }
+  int incl = mine;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) sh.scan[warp] = make_int2(incl, most);
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    before += w < warp ? sh.scan[w].x : 0;
+    all += sh.scan[w].x;
+    most = max(most, sh.scan[w].y);
+  }
+  before += incl - mine;
+  const int T = all * p.units, ctas = min((int)gridDim.x, T);  // each of these has at least one chunk
+  const bool busy = (int)blockIdx.x < ctas;
+  const int quot = busy ? T / ctas : 0, rest = T - quot * ctas;  // share x begins at x T / ctas, rounded down
+  int begin = busy ? blockIdx.x * quot + (int)blockIdx.x * rest / ctas : 0;
+  int end = busy ? (blockIdx.x + 1) * quot + ((int)blockIdx.x + 1) * rest / ctas : 0;
+  // Short sequences: shares begin and end at units (rounded up), nothing is left to merge.
+  const bool snap = most <= kDec8Whole;
+  if (threadIdx.x == 0) {
+    sh.skip[0] = sh.skip[1] = 0;  // end == T: no thread finds it
+    sh.end = end;
+    sh.T = T;
+    sh.ctas = ctas;
+    if (!p.by_unit) p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const int x = which ? end : begin;
+    if (busy && before * p.units <= x && x < (before + mine) * p.units && (which == 0 || snap)) {
+      int at = before * p.units, b = b_lo, n;
+      for (;; ++b) {
+        n = chunks_of(b) * p.units;
+        if (x < at + n) break;
+        at += n;
+      }
+      int skip = 0;
+      if (snap) {
+        const int c = n / p.units, in = (x - at) % c;
+        skip = in ? c - in : 0;
+      }
+      sh.skip[which] = skip;
+      if (which == 0) {
+        const bool over = x - at + skip == n;  // on to the next sequence that has rows
+        sh.b = b + over;
+        sh.u = over ? 0 : x - at + skip;
+      }
+    }
+  }
+  __syncthreads();
+  if (busy) {
+    begin += sh.skip[0];
+    end += sh.skip[1];
+  }
+  return Dec8Walk{end - begin, begin < end ? sh.u : 0, begin < end ? sh.b : 0};
+}
+
+// One thread, after a segment: a unit that begins here is described for the merge, if it has to be.
+__device__ __forceinline__ void dec8_describe(const Dec8Params& p, const Dec8Seg& seg, const Dec8Share& sh, int group,
+                                              int tile, bool whole) {
+  if (seg.c0 != 0 || (whole && !p.by_unit)) return;
+  // the parts after this one: the CTAs whose shares begin before the unit ends
+  int parts = 0;
+  if (!whole) {
+    // x T / ctas < stop, rounded down or not, is x < stop ctas / T, rounded up
+    const long long stop = sh.end + sh.skip[1] + (seg.chunks - seg.c1);
+    parts = (int)((stop * sh.ctas + sh.T - 1) / sh.T) - (int)blockIdx.x;
+  }
+  p.ws_desc[p.by_unit ? seg.b * p.units + seg.unit : blockIdx.x] =
+      make_int4(parts | (int)blockIdx.x << 16, seg.b, group, tile);
+}
+
 __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -208,8 +306,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
   float* sm_scale = reinterpret_cast<float*>(sm_ml + RG * 4 * 16);                           // [NS][2][8]
   uint64_t* full = reinterpret_cast<uint64_t*>(sm_scale + NS * 16);
   uint64_t* empty = full + NS;
-  __shared__ int2 sm_scan[C::kThreads / 32];
-  __shared__ int sm_b, sm_u, sm_skip[2];
+  __shared__ Dec8Share share;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
@@ -221,72 +318,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
     prefetch_tensormap(&tmV);
   }
 
-  // This CTA's share of all chunks: prefix sums over the sequences.
-  const int per = (p.B + C::kThreads - 1) / C::kThreads;
-  const int b_lo = min((int)threadIdx.x * per, p.B), b_hi = min(b_lo + per, p.B);
-  auto chunks_of = [&](int b) { return dec8_len(p, b) + (kDec8Keys >> p.hs) - 1 >> (7 - p.hs); };
-  int mine = 0, most = 0;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const int n = chunks_of(b);
-    mine += n;
-    most = max(most, n);
-  }
-  int incl = mine;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += y;
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 31) sm_scan[warp] = make_int2(incl, most);
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < C::kThreads / 32; ++w) {
-    before += w < warp ? sm_scan[w].x : 0;
-    all += sm_scan[w].x;
-    most = max(most, sm_scan[w].y);
-  }
-  before += incl - mine;
-  const int T = all * p.units, ctas = min((int)gridDim.x, T);  // each of these has at least one chunk
-  const bool busy = (int)blockIdx.x < ctas;
-  const int quot = busy ? T / ctas : 0, rest = T - quot * ctas;  // share x begins at x T / ctas, rounded down
-  int begin = busy ? blockIdx.x * quot + (int)blockIdx.x * rest / ctas : 0;
-  int end = busy ? (blockIdx.x + 1) * quot + ((int)blockIdx.x + 1) * rest / ctas : 0;
-  // Short sequences: shares begin and end at units (rounded up), nothing is left to merge.
-  const bool snap = most <= kDec8Whole;
-  if (threadIdx.x == 0) sm_skip[1] = 0;  // end == T: no thread finds it
-  __syncthreads();
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const int x = which ? end : begin;
-    if (busy && before * p.units <= x && x < (before + mine) * p.units && (which == 0 || snap)) {
-      int at = before * p.units, b = b_lo, n;
-      for (;; ++b) {
-        n = chunks_of(b) * p.units;
-        if (x < at + n) break;
-        at += n;
-      }
-      int skip = 0;
-      if (snap) {
-        const int c = n / p.units, in = (x - at) % c;
-        skip = in ? c - in : 0;
-      }
-      sm_skip[which] = skip;
-      if (which == 0) {
-        const bool over = x - at + skip == n;  // on to the next sequence that has rows
-        sm_b = b + over;
-        sm_u = over ? 0 : x - at + skip;
-      }
-    }
-  }
-  __syncthreads();
-  if (busy) {
-    begin += sm_skip[0];
-    end += sm_skip[1];
-  }
-  if (threadIdx.x == 0 && !p.by_unit) p.ws_desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-  Dec8Walk walk{end - begin, begin < end ? sm_u : 0, begin < end ? sm_b : 0};
+  Dec8Walk walk = dec8_share<C::kThreads>(p, share);
   Dec8Seg seg;
 
   if (warp >= C::kWarps) {
@@ -718,17 +750,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
     if (lane == 0) mbar_arrive(empty + slot);
     if (++slot == NS) slot = 0, phase ^= 1u;
     if constexpr (MT > 1) asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");  // sm_q is free
-    if (seg.c0 == 0 && threadIdx.x == 0 && (!whole || p.by_unit)) {
-      // the parts after this one: the CTAs whose shares begin before the unit ends
-      int parts = whole ? 0 : 1;
-      if (!whole) {
-        // x T / ctas < stop, rounded down or not, is x < stop ctas / T, rounded up
-        const long long stop = end + (seg.chunks - seg.c1);
-        parts = (int)((stop * ctas + T - 1) / T) - (int)blockIdx.x;
-      }
-      p.ws_desc[p.by_unit ? seg.b * p.units + seg.unit : blockIdx.x] =
-          make_int4(parts | (int)blockIdx.x << 16, seg.b, group, tile);
-    }
+    if (threadIdx.x == 0) dec8_describe(p, seg, share, group, tile, whole);
+    __syncwarp();
   }
 }
 

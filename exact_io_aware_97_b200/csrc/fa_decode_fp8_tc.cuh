@@ -1,0 +1,553 @@
+// Decode attention over an e4m3 paged cache for many query rows: more than 16 of a K/V head (several
+// new tokens, large head groups), d = 128 (sm_100a).
+//
+// The sums of fa_decode_fp8.cuh, with the cache side as M of tcgen05 products on the bytes as they
+// are in the cache: nothing of K or V is widened, and a product costs the same for 17 query rows
+// as for 64.  For a chunk of 128 cache rows and a tile of 64 query rows:
+//   S^T [128 rows of K x 64] = K q^T               (A = K, K-major; q from shared memory)
+//   P^T: thread = cache row, its 64 scores to weights
+//   O^T [128 columns of V x 64] += V^T P^T         (A = V, read column-major; P from shared memory)
+// q and the weights go to e4m3 as the sum of two terms.  q: a row is scaled by a power of two to a
+// largest element in [128, 256); hi = e4m3(q), lo = e4m3(q - hi), so hi + lo holds the 8 bits of a
+// bf16 down to 2^-9 of that scale, 2^-17 of the row's largest element (both terms into one sum).
+// Weights w = p sv: hi = e4m3(w), lo = e4m3(16 (w - hi)), 8 bits down to 2^-14, in two sums (columns
+// 0..63 and 64..127 of one product).  The largest w of a row is 1 when its reference is set and may
+// grow to 2^8.5; only a score that goes beyond raises the reference and rescales the sums (with room
+// for 2^4.5 only, some row of 40 did so in half of the chunks).  l sums p in fp32.  Both p and w are
+// relative to the one reference, which follows t + log2(sv).
+//
+// Warps stay together: whatever lanes do alone ends in a __syncwarp before the next barrier or TMEM
+// access, which are for whole warps.
+//
+// One CTA per SM: TMA producer, MMA issuer, two warpgroups that share the query rows of every chunk
+// (taking the chunks in turn with all 64 rows each meant 64 scores and 64 sums in registers, a merge
+// at each unit's end, and 385 us for 40 rows instead of TCNEW).  Scores and weights have two
+// buffers, so the products of one chunk run under the weights of the next.  K and V are slots of
+// their own in the ring, since a K slot is free as soon as its product is done.
+//
+// What bounds it: RATE.
+#pragma once
+
+#include "fa_decode_fp8.cuh"
+
+namespace fa {
+
+struct Dec8TcCfg {
+  static constexpr int D = 128, kRows = 64, kThreads = 384;
+  static constexpr int kControlRegs = 56, kWorkRegs = 216;  // 128 x 56 + 256 x 216 <= 384 x 168
+  static constexpr int kSlot = kDec8Keys * D;               // bytes of K (or V) of a chunk
+  static constexpr int kSlots = 10, kPairs = kSlots / 2;
+  static constexpr int kScales = 8;                         // chunks whose scales are kept (> kPairs)
+  static constexpr int kP = kDec8Keys * 128;                // weights of a chunk: hi | lo of 64 rows
+  static constexpr int kQ = kRows * D;                      // hi (and lo) of the query tile
+  static constexpr int kColS = 0, kColO = 128, kTmemCols = 256;  // S: 2 x 64 columns; O: hi and lo of 64
+  static constexpr int kCols = 32;                               // query rows of a warpgroup
+  static constexpr int kOffP = kSlots * kSlot, kOffQ = kOffP + 2 * kP, kOffMisc = kOffQ + 2 * kQ;
+  static constexpr int kSmem = 1024 + kOffMisc + kScales * 64 + kRows * 8 + kRows * 4 + kRows * 16 + 4 * kRows * 4 +
+                               64 * 8;
+};
+
+constexpr float kTcTop = 8.5f;  // largest exponent of a weight (0 at a new reference)
+
+// Instruction descriptor with both operands MN-major.
+constexpr uint32_t kMnMajorBoth = (1u << 15) | (1u << 16);
+
+// True for every thread of the warpgroup if it is for one (named barrier `id`, 128 threads).
+__device__ __forceinline__ bool group_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred.aligned q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// Float order as int order (for a maximum over a warp).
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i >= 0 ? i : i ^ 0x7FFFFFFF;
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
+
+__global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
+    fa_decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                            const Dec8Params p) {
+  using C = Dec8TcCfg;
+  constexpr int D = C::D, R = C::kRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const sm_p = ring + C::kOffP;
+  uint8_t* const sm_q = ring + C::kOffQ;
+  float* const sm_scale = reinterpret_cast<float*>(ring + C::kOffMisc);        // [kScales][2][8]
+  float2* const sm_fw = reinterpret_cast<float2*>(sm_scale + C::kScales * 16);  // [R]: factor, reference
+  int* const sm_limit = reinterpret_cast<int*>(sm_fw + R);                      // [R]
+  uint32_t* const sm_nan = reinterpret_cast<uint32_t*>(sm_limit + R);           // [R][4]
+  float* const sm_red = reinterpret_cast<float*>(sm_nan + R * 4);               // [2][4][kCols]
+  uint64_t* const full = reinterpret_cast<uint64_t*>(sm_red + 4 * R);
+  uint64_t* const empty = full + C::kSlots;
+  uint64_t* const q_full = empty + C::kSlots;
+  uint64_t* const s_full = q_full + 1;    // [2]
+  uint64_t* const s_empty = s_full + 2;   // [2]
+  uint64_t* const p_full = s_empty + 2;   // [2]
+  uint64_t* const p_done = p_full + 2;    // [2]
+  uint64_t* const all_done = p_done + 2;
+  __shared__ uint32_t tmem_slot;
+  __shared__ Dec8Share share;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(full + s, 1 + 8);  // the producer's expect_tx, and eight lanes' scales
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(q_full, 256);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(s_full + w, 1);
+      mbar_init(s_empty + w, 256);
+      mbar_init(p_full + w, 256);
+      mbar_init(p_done + w, 1);
+    }
+    mbar_init(all_done, 1);
+    fence_barrier_init();
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_slot, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  Dec8Walk walk = dec8_share<C::kThreads>(p, share);  // synchronises the CTA
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  Dec8Seg seg;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kControlRegs));
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      // Lanes 0..15: (K or V, 16-row tile of the chunk), as in fa_decode_fp8_kernel.
+      if (lane < 16) {
+        const int which = lane >> 3, sub = lane & 7, ro = 16 * sub;
+        const uint64_t pol = policy_evict_first();
+        const int psm = (1 << p.page_shift) - 1, nb_shift = p.page_shift - p.sb_shift;
+        const bool leads = ro % p.box == 0;
+        int pair = 0, entry = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        while (ok && walk.next(p, seg)) {
+          const int kvh = seg.unit / p.tiles;
+          const int32_t* bt = p.block_table + (long long)seg.b * p.max_pages;
+          int tok = seg.c0 * kDec8Keys + ro;
+          int page_next = tok < seg.len ? __ldg(bt + (tok >> p.page_shift)) : 0;
+          for (int c = seg.c0; c < seg.c1; ++c, tok += kDec8Keys) {
+            int page = page_next;
+            const bool here = tok < seg.len;
+            if (c + 1 < seg.c1 && tok + kDec8Keys < seg.len)
+              page_next = __ldg(bt + ((tok + kDec8Keys) >> p.page_shift));
+            if (page < 0 || page >= p.num_pages) {
+              atomicOr(&g_error_word, kErrBadPage);
+              page = 0;
+            }
+            const int slot = 2 * pair + which;
+            ok = __all_sync(0xffffu, mbar_wait(empty + slot, phase));
+            if (!ok) break;
+            if (sub == 0) {
+              const int rows = min(kDec8Keys, (seg.len - c * kDec8Keys + p.box - 1) / p.box * p.box);
+              mbar_arrive_expect_tx(full + slot, rows * D);
+            }
+            __syncwarp(0xffffu);
+            const int r = tok & psm;
+            float* const to = sm_scale + entry * 16 + lane;
+            if (here) {
+              if (leads)
+                tma_load_3d_hint(ring + slot * C::kSlot + ro * D, which ? &tmV : &tmK, 0, (page << p.page_shift) + r,
+                                 kvh, full + slot, pol);
+              const float* src = p.scales[which] + (((long long)page * p.Hkv + kvh) << nb_shift) + (r >> p.sb_shift);
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(src) : "memory");
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + slot))
+                           : "memory");
+            } else {
+              *to = 0.f;
+              mbar_arrive(full + slot);
+            }
+            if (++pair == C::kPairs) pair = 0, phase ^= 1u;
+            entry = (entry + 1) % C::kScales;
+          }
+        }
+        if (lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idS = idesc_e4m3_f32(128, R), idO = idesc_e4m3_f32(128, 128) | kMnMajorBoth;
+      const uint64_t dRing = smem_desc_sw128(smem_u32(ring), 16, 1024);
+      const uint64_t dP = smem_desc_sw128(smem_u32(sm_p), 16, 1024);
+      const uint64_t dQ = smem_desc_sw128(smem_u32(sm_q), 16, 1024);
+      int pair = 0, vpair = 0;
+      uint32_t kphase = 0, vphase = 0, qphase = 0;
+      uint32_t n_s = 0, n_p = 0;  // products issued; buffer = the last bit, use of it = the rest
+      bool ok = true;
+      auto product_s = [&] {
+        const uint32_t w = n_s & 1u;
+        ok = ok && warp_wait(full + 2 * pair, kphase) && (n_s < 2 || warp_wait(s_empty + w, ((n_s >> 1) - 1) & 1u));
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one_lane()) {
+          const uint64_t a = dRing + (uint64_t)((2 * pair * C::kSlot) >> 4);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)  // hi, lo
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              mma_ss<1>(tmem + C::kColS + w * R, a + (uint64_t)(k * 2), dQ + (uint64_t)((t * C::kQ + k * 32) >> 4), idS,
+                        t + k > 0 ? 1u : 0u);
+          umma_commit(s_full + w);
+          umma_commit(empty + 2 * pair);
+        }
+        __syncwarp();
+        ++n_s;
+        if (++pair == C::kPairs) pair = 0, kphase ^= 1u;
+      };
+      auto product_o = [&](bool first) {
+        const uint32_t w = n_p & 1u;
+        ok = ok && warp_wait(full + 2 * vpair + 1, vphase) && warp_wait(p_full + w, (n_p >> 1) & 1u);
+        if (!ok) return;
+        tc_fence_after();
+        if (elect_one_lane()) {
+          const uint64_t a = dRing + (uint64_t)(((2 * vpair + 1) * C::kSlot) >> 4);
+          const uint64_t b = dP + (uint64_t)((w * C::kP) >> 4);
+#pragma unroll
+          for (int k = 0; k < kDec8Keys / 32; ++k)  // 32 cache rows = 4 KB of either operand
+            mma_ss<1>(tmem + C::kColO, a + (uint64_t)(k * 256), b + (uint64_t)(k * 256), idO,
+                      first && k == 0 ? 0u : 1u);
+          umma_commit(p_done + w);
+          umma_commit(empty + 2 * vpair + 1);
+        }
+        __syncwarp();
+        ++n_p;
+        if (++vpair == C::kPairs) vpair = 0, vphase ^= 1u;
+      };
+      while (ok && walk.next(p, seg)) {
+        const int n = seg.c1 - seg.c0;
+        ok = warp_wait(q_full, qphase);
+        qphase ^= 1u;
+        if (ok) product_s();
+        for (int k = 0; k < n && ok; ++k) {
+          if (k + 1 < n) product_s();
+          product_o(k == 0);
+        }
+      }
+      umma_commit_elect(all_done);  // nothing is in flight when the columns are given back
+      (void)warp_wait(all_done, 0);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kWorkRegs));
+    // -------------------------------------------------------------- weights (two warpgroups)
+    const int w = (warp >> 2) - 1, tid = threadIdx.x - 128;  // group 0 or 1; 0..255
+    const int row = tid & 127, quarter = row >> 5;           // cache row of a chunk = TMEM lane
+    const uint32_t lanes = (uint32_t)quarter << 21;
+    float* const red = sm_red + w * 4 * C::kCols;
+    int pair = 0, entry = 0;
+    uint32_t kphase = 0, n = 0;  // chunks so far: buffer and use as for the MMA issuer
+    bool ok = true;
+
+    // sequences without rows: o = 0, lse = -inf
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+      if (dec8_len(p, b) > 0) continue;
+      const long long n = (long long)p.Nq * p.Hq;
+      for (long long k = tid; k < n * D / 8; k += 256)
+        reinterpret_cast<uint4*>(p.o)[(long long)b * (n * D / 8) + k] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (long long k = tid; k < n; k += 256) p.lse[b * n + k] = -INFINITY;
+      if (p.by_unit)
+        for (int k = tid; k < p.units; k += 256) p.ws_desc[b * p.units + k] = make_int4(0, 0, 0, 0);
+    }
+
+    while (walk.next(p, seg)) {
+      const int kvh = seg.unit / p.tiles, tile = seg.unit - kvh * p.tiles;
+      // this group's query rows: columns [col0, col0 + 8 blocks) of the tile, half of them rounded up
+      const int rows = min(R, p.rows - tile * R), share8 = (rows + 15) >> 4;
+      const int col0 = w * share8 * 8, blocks = w ? ((rows + 7) >> 3) - share8 : share8;
+      float2* const fw = sm_fw + col0;
+      const int* const limit = sm_limit + col0;
+      {
+        // the query tile: four threads a row, 32 elements each
+        const int r = tid >> 2, part = tid & 3, qr = tile * R + r;
+        const bool in = qr < p.rows;
+        const int i = in ? qr / p.G : 0, h = kvh * p.G + (in ? qr - i * p.G : 0);
+        const uint4* src =
+            reinterpret_cast<const uint4*>(p.q + (((long long)seg.b * p.Nq + i) * p.Hq + h) * D) + part * 4;
+        uint4 x[4];
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[k] = in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t v = (&x[k].x)[j];
+            top = max(top, max((v << 16) & 0x7FFF0000u, v & 0x7FFF0000u));
+          }
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const bool finite = top < 0x7F800000u;
+        const int be = (top == 0u || !finite) ? 127 : max((int)(top >> 23), 1);
+        // 2^(7 - e) in two factors, each a normal number
+        const float d0 = __uint_as_float((uint32_t)(127 + (127 - be) / 2) << 23);
+        const float d1 = __uint_as_float((uint32_t)(127 + 7 + (127 - be) - (127 - be) / 2) << 23);
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t v0 = (&x[k >> 1].x)[2 * (k & 1)], v1 = (&x[k >> 1].x)[2 * (k & 1) + 1];
+          const float a[4] = {__uint_as_float(v0 << 16) * d0 * d1, __uint_as_float(v0 & 0xFFFF0000u) * d0 * d1,
+                              __uint_as_float(v1 << 16) * d0 * d1, __uint_as_float(v1 & 0xFFFF0000u) * d0 * d1};
+          hi[k] = e4m3x4(a[0], a[1], a[2], a[3]);
+          uint32_t b0, b1;
+          e4m3x4_to_f16(hi[k], b0, b1);
+          const float2 f0 = __half22float2(*reinterpret_cast<__half2*>(&b0));
+          const float2 f1 = __half22float2(*reinterpret_cast<__half2*>(&b1));
+          lo[k] = e4m3x4(a[0] - f0.x, a[1] - f0.y, a[2] - f1.x, a[3] - f1.y);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int at = r * D + (((part * 2 + u) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(sm_q + at) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
+          *reinterpret_cast<uint4*>(sm_q + C::kQ + at) =
+              make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+        }
+        if (part == 0) {
+          // scores are q . k times 2^(e - 7); a row that is not finite makes everything of its own NaN
+          const float f = finite ? p.tau * 0.0078125f * __uint_as_float((uint32_t)be << 23) : __uint_as_float(0x7FC00000u);
+          sm_fw[r] = make_float2(f, 0.f);
+          sm_limit[r] = in ? seg.len - p.Nq + 1 + i : seg.len;
+        }
+        sm_nan[tid] = 0u;  // R * 4 words
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      mbar_arrive(q_full);
+
+      constexpr int N = C::kCols;
+      float l[N];
+#pragma unroll
+      for (int r = 0; r < N; ++r) l[r] = 0.f;
+      const int first_limit = seg.len - p.Nq + 1 + (tile * R) / p.G;
+
+      for (int c = seg.c0; c < seg.c1; ++c, ++n) {
+        const uint32_t buf = n & 1u, use = n >> 1;
+        // the chunk's scales, its V rows (which may be cleaned here), its scores
+        if (ok) ok = mbar_wait(full + 2 * pair, kphase) && mbar_wait(full + 2 * pair + 1, kphase) &&
+                     mbar_wait(s_full + buf, use & 1u);
+        __syncwarp();
+        tc_fence_after();
+        const int j = c * kDec8Keys + row;
+        const float sk = sm_scale[entry * 16 + (row >> 4)], sv = sm_scale[entry * 16 + 8 + (row >> 4)];
+        const float lsv = __log2f(sv), lse_v = lsv < -60.f ? -60.f : lsv;  // (a zero scale weighs nothing)
+        const bool partly = (c + 1) * kDec8Keys > first_limit, fresh = c == seg.c0;
+        float s[N];
+#pragma unroll
+        for (int b = 0; b < N / 8; ++b)
+          if (b < blocks) tmem_ld8(tmem + C::kColS + buf * R + col0 + b * 8 + lanes, reinterpret_cast<uint32_t(&)[8]>(s[b * 8]));
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(s_empty + buf);
+        // exponents t - reference, and whether one is past the top
+        float most = kDec8Low;
+#pragma unroll
+        for (int b = 0; b < N / 8; ++b)
+          if (b < blocks) {
+#pragma unroll
+            for (int x = b * 8; x < b * 8 + 8; x += 2) {
+              const float4 f = *reinterpret_cast<const float4*>(fw + x);
+              s[x] = fmaf(s[x] * sk, f.x, -f.y);
+              s[x + 1] = fmaf(s[x + 1] * sk, f.z, -f.w);
+              if (partly) {
+                if (j >= limit[x]) s[x] = -INFINITY;
+                if (j >= limit[x + 1]) s[x + 1] = -INFINITY;
+              }
+              most = fmax3(most, s[x], s[x + 1]);
+            }
+          }
+        if (group_any(2 + w, fresh || most + lse_v > kTcTop)) {
+          // new references: the largest exponent of each row over the group's threads
+#pragma unroll
+          for (int b = 0; b < N / 8; ++b)
+            if (b < blocks)
+#pragma unroll
+              for (int x = b * 8; x < b * 8 + 8; ++x) {
+                const float v = s[x] + lse_v;
+                const int m = __reduce_max_sync(0xffffffffu, v == v ? ordered(v) : ordered(-INFINITY));
+                if (lane == 0) red[quarter * N + x] = unordered(m);
+              }
+          __syncwarp();
+          asm volatile("bar.sync %0, 128;" ::"r"(2 + w) : "memory");
+          // the sums so far move to the new references (after the last product into them)
+          if (!fresh && ok) ok = mbar_wait(p_done + (buf ^ 1u), ((n - 1) >> 1) & 1u);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll
+          for (int b = 0; b < N / 8; ++b)
+            if (b < blocks) {
+              float up[8];
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const int r = b * 8 + x;
+                const float m = fmaxf(fmaxf(red[r], red[N + r]), fmaxf(red[2 * N + r], red[3 * N + r]));
+                // rows that stay under the top keep theirs, but all get their first one here
+                up[x] = m > (fresh ? -INFINITY : kTcTop) ? m : 0.f;
+                s[r] -= up[x];
+                up[x] = ex2_approx(-up[x]);
+                l[r] *= up[x];
+              }
+              if (!fresh) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                  float o[8];
+                  const uint32_t at = tmem + C::kColO + t * R + col0 + b * 8 + lanes;
+                  tmem_ld8(at, reinterpret_cast<uint32_t(&)[8]>(o));
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) o[x] *= up[x];
+                  tmem_st8(at, reinterpret_cast<uint32_t(&)[8]>(o));
+                }
+              }
+            }
+          tmem_wait_st();
+          if (row < blocks * 8) {  // (every thread has used the old references)
+            const float m = fmaxf(fmaxf(red[row], red[N + row]), fmaxf(red[2 * N + row], red[3 * N + row]));
+            if (m > (fresh ? -INFINITY : kTcTop)) fw[row].y += m;
+          }
+          __syncwarp();
+          asm volatile("bar.sync %0, 128;" ::"r"(2 + w) : "memory");
+        }
+        // V rows that some query does not see (this group's half of the columns): past the end they
+        // may hold anything, and a NaN code would reach every query; it goes to the queries that see
+        // it by hand
+        if (partly) {
+          uint8_t* const v = ring + (2 * pair + 1) * C::kSlot + row * D;
+          uint32_t nan = 0;
+          const bool past = j >= seg.len;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint4* const at = reinterpret_cast<uint4*>(v) + ((4 * w + u) ^ (row & 7));
+            uint4 y = *at;
+            if (past) y = make_uint4(0u, 0u, 0u, 0u);
+            *at = y;
+            nan |= ((y.x & 0x7F7F7F7Fu) + 0x01010101u) | ((y.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                   ((y.z & 0x7F7F7F7Fu) + 0x01010101u) | ((y.w & 0x7F7F7F7Fu) + 0x01010101u);
+          }
+          // (rare, and taken by whole warps)
+          if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0u)) {
+#pragma unroll 1
+            for (int d = 64 * w; d < 64 * w + 64; ++d) {
+              uint8_t* const at = v + (((d >> 4) ^ (row & 7)) << 4) + (d & 15);
+              const bool bad = (*at & 0x7Fu) == 0x7Fu;
+              if (bad) *at = 0;
+              if (__any_sync(0xffffffffu, bad)) {
+#pragma unroll 1
+                for (int r = 0; r < rows; ++r)
+                  if (bad && j < sm_limit[r]) atomicOr(sm_nan + r * 4 + (d >> 5), 1u << (d & 31));
+              }
+              __syncwarp();
+            }
+          }
+        }
+        // the weights replace those of the chunk before the last once their product is done
+        if (n >= 2 && ok) ok = mbar_wait(p_done + buf, (use - 1) & 1u);
+        uint8_t* const prow = sm_p + buf * C::kP + row * 128;
+#pragma unroll
+        for (int b = 0; b < N / 8; ++b)
+          if (b < blocks) {
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float wj[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const int r = b * 8 + 4 * x + y;
+                const float pj = ex2_approx(s[r]);
+                l[r] += pj;
+                wj[y] = pj * sv;
+                if (partly && j >= limit[r]) wj[y] = 0.f;  // a NaN scale is not for this query
+              }
+              hi[x] = e4m3x4(wj[0], wj[1], wj[2], wj[3]);
+              uint32_t b0, b1;
+              e4m3x4_to_f16(hi[x], b0, b1);
+              const float2 f0 = __half22float2(*reinterpret_cast<__half2*>(&b0));
+              const float2 f1 = __half22float2(*reinterpret_cast<__half2*>(&b1));
+              lo[x] = e4m3x4(fmaf(-16.f, f0.x, wj[0] * 16.f), fmaf(-16.f, f0.y, wj[1] * 16.f),
+                             fmaf(-16.f, f1.x, wj[2] * 16.f), fmaf(-16.f, f1.y, wj[3] * 16.f));
+            }
+            const int at = col0 + b * 8;  // byte of the row; its 16-byte unit is swizzled
+            *reinterpret_cast<uint2*>(prow + (((at >> 4) ^ (row & 7)) << 4) + (at & 8)) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(prow + (((4 + (at >> 4)) ^ (row & 7)) << 4) + (at & 8)) = make_uint2(lo[0], lo[1]);
+          }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(p_full + buf);
+        if (++pair == C::kPairs) pair = 0, kphase ^= 1u;
+        entry = (entry + 1) % C::kScales;
+      }
+
+      // ------------------------------------------------------------ a unit's end
+      // l of a row over the 128 threads: half of the rows are exchanged between lanes 16 apart, half
+      // of the rest between lanes 8 apart, ..., so that lane x ends with the sum of row x
+#pragma unroll
+      for (int off = 16, m = N; off > 0; off >>= 1, m >>= 1) {
+        const bool upper = (lane & off) != 0;
+#pragma unroll
+        for (int r = 0; r < N / 2; ++r)
+          if (r < m / 2) {
+            const float give = upper ? l[r] : l[r + m / 2], keep = upper ? l[r + m / 2] : l[r];
+            l[r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+          }
+      }
+      red[quarter * N + lane] = l[0];
+      if (ok) ok = mbar_wait(p_done + ((n - 1) & 1u), ((n - 1) >> 1) & 1u);
+      __syncwarp();
+      tc_fence_after();
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const bool whole = seg.c0 == 0 && seg.c1 == seg.chunks;
+      const long long part = 2ll * blockIdx.x + (seg.c0 == 0 ? 1 : 0);
+#pragma unroll
+      for (int b = 0; b < N / 8; ++b)
+        if (b < blocks) {
+          float hi[8], lo[8];
+          tmem_ld8(tmem + C::kColO + col0 + b * 8 + lanes, reinterpret_cast<uint32_t(&)[8]>(hi));
+          tmem_ld8(tmem + C::kColO + R + col0 + b * 8 + lanes, reinterpret_cast<uint32_t(&)[8]>(lo));
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int r = b * 8 + x, tr = col0 + r, qr = tile * R + tr;
+            if (tr >= rows) continue;
+            const float L = red[r] + red[N + r] + red[2 * N + r] + red[3 * N + r];
+            const float M = L == 0.f ? kDec8Low : fw[r].y;  // nothing seen: no reference
+            float A = fmaf(lo[x], 0.0625f, hi[x]);
+            if ((sm_nan[tr * 4 + (row >> 5)] >> (row & 31)) & 1u) A = __uint_as_float(0x7FC00000u);
+            if (whole) {
+              const int i = qr / p.G, h = kvh * p.G + qr - i * p.G;
+              const float inv = L == 0.f ? 0.f : 1.f / L;
+              p.o[(((long long)seg.b * p.Nq + i) * p.Hq + h) * D + row] = __float2bfloat16_rn(A * inv);
+              if (row == 0 && p.lse)
+                p.lse[((long long)seg.b * p.Hq + h) * p.Nq + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            } else {
+              p.ws_acc[(part * R + tr) * D + row] = A;
+              if (row == 0) p.ws_ml[part * R + tr] = make_float2(M, L);
+            }
+          }
+        }
+      tc_fence_before();
+      if (tid == 0) dec8_describe(p, seg, share, kvh, tile, whole);
+      __syncwarp();
+      asm volatile("bar.sync 1, 256;" ::: "memory");  // the tables are free for the next unit
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+}
+
+}  // namespace fa

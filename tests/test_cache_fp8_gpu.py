@@ -5,7 +5,15 @@ and fa_decode_paged_fp8 against attention in 64 bits over the stored values.
 Tolerance of o: half a bf16 step of the value (2^-8); of the weights p * scale 2^-11 relative (fp16)
 or 2^-25 of the largest one below fp16's normal range, so 2^-11 sum p|v| + 2^-25 sum|v|; and 2^-17
 (1 + t) relative for the fp32 scores (d = 128 products of size t in all, 2^-24 each, and the fp32
-exponentials).  lse: 2^-17 (1 + t)."""
+exponentials).  lse: 2^-17 (1 + t).
+
+More than 16 query rows of a K/V head at d = 128 take the kernel that multiplies e4m3 bytes, with q and
+the weights as two e4m3 terms.  Weights: the first term is off by at most 2^-4 of the weight and the
+second by 2^-4 of that, 2^-8 together, where its 16-fold is normal; below, by half of 2^-9 / 16 = 2^-14
+while the largest weight of the row is at least 1, so by 2^-14 of it: 2^-14 sum|v| times the
+largest over the smallest scale.  q: exact down to the step of the second term, 2^-9 where the
+row's largest element is at least 2^7, so off by at most 2^-17 of that element: 2^-17 u for scores,
+with u = max|q| sum|k| scale in place of t = sum|q||k| scale."""
 import math
 
 import numpy as np
@@ -18,18 +26,40 @@ from exact_io_aware_97_b200 import binding as fa
 pytestmark = pytest.mark.gpu
 
 
-def check(o, lse, ref, q_shape):
+def check(o, lse, ref, q, kv):
+    """kv: the cache's (codes, scales) of K and V and table, lens, sb, scale of cache8.attend."""
     r_o, r_lse, o_abs, v_sum, t_abs = ref
     got = o.double().cpu().numpy().reshape(r_o.shape)
     gl = lse.double().cpu().numpy().reshape(r_lse.shape)
     assert not np.isnan(got).any()
-    t = t_abs.transpose(0, 2, 1)[..., None]
-    tol = 2.0 ** -8 * np.abs(r_o) + (2.0 ** -11 + 2.0 ** -17 * (1 + t)) * o_abs + 2.0 ** -25 * v_sum
+    weight, small, u = 2.0 ** -11, 2.0 ** -25, 0.0
+    q64 = q.double().cpu().numpy().reshape(r_o.shape)
+    _, Nq, Hq, d = q64.shape
+    if Nq * Hq // kv[0].shape[2] > 16 and d == 128:
+        used = kv[3][np.isfinite(kv[3]) & (kv[3] > 0)]
+        weight, small = 2.0 ** -8, 2.0 ** -14 * used.max() / used.min()
+        u = _score_bound(q64, kv)
+    t = t_abs + u
+    tt = t.transpose(0, 2, 1)[..., None]
+    tol = 2.0 ** -8 * np.abs(r_o) + (weight + 2.0 ** -17 * (1 + tt)) * o_abs + small * v_sum
     bad = np.abs(got - r_o) > tol
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:3], np.abs(got - r_o).max())
     none = np.isneginf(r_lse)
     assert np.array_equal(np.isneginf(gl), none)
-    assert np.all(np.abs(gl[~none] - r_lse[~none]) <= 2.0 ** -17 * (1 + t_abs[~none]))
+    assert np.all(np.abs(gl[~none] - r_lse[~none]) <= 2.0 ** -17 * (1 + t[~none]))
+
+
+def _score_bound(q, kv):
+    """max|q| times the largest sum|k| of the sequence, times the scale: [B, Hq, Nq]."""
+    kc, ks, _, _, table, lens, sb, scale = kv
+    B, Nq, Hq, _ = q.shape
+    out = np.zeros((B, Hq, Nq))
+    for b in range(B):
+        if lens[b] == 0:
+            continue
+        k = np.abs(cache8.gather(kc, ks, table[b], lens[b], sb)).sum(-1).max(0)  # [H]
+        out[b] = np.abs(q[b]).max(-1).T * np.repeat(k, Hq // kc.shape[2])[:, None] * scale
+    return out
 
 
 CASES = [
@@ -64,7 +94,7 @@ def test_decode_fp8_matches_64_bits(case):
     o, lse = fa.decode_paged_fp8(q, dkc, dvc, dks, dvs, dt, dl, workspace=ws)
     torch.cuda.synchronize()
     assert fa.fa_last_device_error() == fa.FA_OK
-    check(o, lse, ref, q.shape)
+    check(o, lse, ref, q, (kc, ks, vc, vs, table, lens, sb, 1 / math.sqrt(d)))
     # the workspace, used once, gives the same bits again; so does the 3-D form for one token
     o2, lse2 = fa.decode_paged_fp8(q if Nq > 1 else q[:, 0], dkc, dvc, dks, dvs, dt, dl, workspace=ws)
     assert torch.equal(o2.view_as(o), o) and torch.equal(lse2.view_as(lse), lse)
@@ -132,7 +162,7 @@ def test_decode_fp8_extreme_queries_and_zero_scales():
         scale = 0.125 * 2.0 ** -e
         ref = cache8.attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, lens, sb, scale)
         o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5], scale=scale)
-        check(o, lse, ref, q.shape)
+        check(o, lse, ref, q, (kc, ks, vc, vs, table, lens, sb, scale))
 
 
 def test_decode_fp8_nan_reaches_only_what_attends_to_it():
@@ -371,10 +401,10 @@ def test_prefill_then_decode_through_the_cache():
 
     def verify(a, o, lse):
         ln = seqlens.cpu().numpy()
-        ref = cache8.attend(a.double().cpu().numpy()[:, None], kp.view(torch.uint8).cpu().numpy(),
-                            ks.double().cpu().numpy(), vp.view(torch.uint8).cpu().numpy(), vs.double().cpu().numpy(),
-                            table, ln, sb, 1 / math.sqrt(d))
-        check(o[:, None], lse[..., None], ref, None)
+        cache = (kp.view(torch.uint8).cpu().numpy(), ks.double().cpu().numpy(), vp.view(torch.uint8).cpu().numpy(),
+                 vs.double().cpu().numpy(), table, ln, sb, 1 / math.sqrt(d))
+        ref = cache8.attend(a.double().cpu().numpy()[:, None], *cache)
+        check(o[:, None], lse[..., None], ref, a, cache)
 
     def feed():
         for t in (sq, sk, sv):
