@@ -1071,6 +1071,8 @@ fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// What a unit costs beside its chunks, in chunks (measured on ragged batches).
+constexpr int kDec8Lead = 1, kDec8TcLead = 3;
 // Query rows of a unit: one tensor-core tile of 16 where that holds them; else the kernel on tcgen05
 // products with 64 (d = 128: 40 rows in TCNEW us instead of 205 with 64 rows in registers), or
 // registers for 32 or 64 (d = 64, where a cache row is too short for those products' 128 rows).
@@ -1240,7 +1242,8 @@ extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, con
   prm.cap = (int)((int64_t)max_pages_per_seq * page_size);
   const int64_t units = (int64_t)(Hkv >> prm.hs) * prm.tiles;
   // positions among all chunks are 32-bit in the kernel
-  if (B * units * (((prm.cap - 1) >> (7 - prm.hs)) + 1) >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  prm.lead = tile == 64 && d == 128 ? kDec8TcLead : kDec8Lead;
+  if (B * units * (((prm.cap - 1) >> (7 - prm.hs)) + 1 + prm.lead) >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
   prm.units = (int)units;
   prm.by_unit = B * units <= (int64_t)ctas;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -51,6 +51,7 @@ struct Dec8Params {
   int num_pages, page_shift, sb_shift, max_pages, box;
   int cap;    // rows that the table holds of a sequence
   int units;  // of a sequence: groups of K/V heads * tiles
+  int lead;   // positions of a unit before its first chunk
   int hs;     // a unit covers 2^hs K/V heads, a chunk 128 >> hs cache rows of them
   float tau;  // scale * log2(e)
 };
@@ -91,49 +92,58 @@ struct Dec8Seg {
 
 __device__ __forceinline__ int dec8_len(const Dec8Params& p, int b) { return min(max(__ldg(p.seqlens + b), 0), p.cap); }
 
-// The number of all chunks is under 2^31 (the host sees to that), so positions are ints.
+// Positions count chunks and, before each unit's first, p.lead more that stand for what a unit costs
+// on its own (its queries, the start and the end of its pipeline), so that shares of many short units
+// take no longer.  Their number is under 2^31 (the host sees to that).
 struct Dec8Walk {
   int left, u, b;
   __device__ __forceinline__ bool next(const Dec8Params& p, Dec8Seg& s) {
-    if (left <= 0) return false;
-    int len;
-    for (;; ++b) {  // left > 0: some sequence from b on holds rows
-      len = dec8_len(p, b);
-      if (len > 0) break;
+    while (left > 0) {
+      int len;
+      for (;; ++b) {  // left > 0: some sequence from b on holds rows
+        len = dec8_len(p, b);
+        if (len > 0) break;
+      }
+      s.b = b;
+      s.len = len;
+      s.chunks = (len - 1 >> 7 - p.hs) + 1;
+      const int span = s.chunks + p.lead;
+      s.unit = (unsigned)u / (unsigned)span;
+      const int from = u - s.unit * span, to = min(span, from + left);
+      s.c0 = max(from - p.lead, 0);
+      s.c1 = max(to - p.lead, 0);
+      left -= to - from;
+      u += to - from;
+      if (u == span * p.units) {
+        ++b;
+        u = 0;
+      }
+      if (s.c0 < s.c1) return true;
     }
-    s.b = b;
-    s.len = len;
-    s.chunks = (len - 1 >> 7 - p.hs) + 1;
-    s.unit = (unsigned)u / (unsigned)s.chunks;
-    s.c0 = u - s.unit * s.chunks;
-    s.c1 = min(s.chunks, s.c0 + left);
-    left -= s.c1 - s.c0;
-    u += s.c1 - s.c0;
-    if (u == s.chunks * p.units) {
-      ++b;
-      u = 0;
-    }
-    return true;
+    return false;
   }
 };
 
 // What the CTAs share out among themselves, in shared memory.
 struct Dec8Share {
-  int2 scan[32];  // per warp: chunks, most chunks of a sequence
+  int2 scan[32];  // per warp: positions, most positions of a unit
   int b, u, skip[2];
-  int end, T, ctas;  // end of this CTA's share (without skip); all chunks; CTAs with a share
+  int end, T, ctas;  // end of this CTA's share (without skip); all positions; CTAs with a share
 };
 
-// This CTA's share of all chunks, by prefix sums over the sequences; synchronises the CTA.
+// This CTA's share of all positions, by prefix sums over the sequences; synchronises the CTA.
 template <int THREADS>
 __device__ __forceinline__ Dec8Walk dec8_share(const Dec8Params& p, Dec8Share& sh) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = (p.B + THREADS - 1) / THREADS;
   const int b_lo = min((int)threadIdx.x * per, p.B), b_hi = min(b_lo + per, p.B);
-  auto chunks_of = [&](int b) { return dec8_len(p, b) + (kDec8Keys >> p.hs) - 1 >> (7 - p.hs); };
+  auto span_of = [&](int b) {  // positions of one unit of sequence b
+    const int n = dec8_len(p, b) + (kDec8Keys >> p.hs) - 1 >> (7 - p.hs);
+    return n ? n + p.lead : 0;
+  };
   int mine = 0, most = 0;
   for (int b = b_lo; b < b_hi; ++b) {
-    const int n = chunks_of(b);
+    const int n = span_of(b);
     mine += n;
     most = max(most, n);
   }
@@ -154,13 +164,13 @@ __device__ __forceinline__ Dec8Walk dec8_share(const Dec8Params& p, Dec8Share& s
     most = max(most, sh.scan[w].y);
   }
   before += incl - mine;
-  const int T = all * p.units, ctas = min((int)gridDim.x, T);  // each of these has at least one chunk
+  const int T = all * p.units, ctas = min((int)gridDim.x, T);  // each of these has at least one position
   const bool busy = (int)blockIdx.x < ctas;
   const int quot = busy ? T / ctas : 0, rest = T - quot * ctas;  // share x begins at x T / ctas, rounded down
   int begin = busy ? blockIdx.x * quot + (int)blockIdx.x * rest / ctas : 0;
   int end = busy ? (blockIdx.x + 1) * quot + ((int)blockIdx.x + 1) * rest / ctas : 0;
   // Short sequences: shares begin and end at units (rounded up), nothing is left to merge.
-  const bool snap = most <= kDec8Whole;
+  const bool snap = most <= kDec8Whole + p.lead;
   if (threadIdx.x == 0) {
     sh.skip[0] = sh.skip[1] = 0;  // end == T: no thread finds it
     sh.end = end;
@@ -175,7 +185,7 @@ __device__ __forceinline__ Dec8Walk dec8_share(const Dec8Params& p, Dec8Share& s
     if (busy && before * p.units <= x && x < (before + mine) * p.units && (which == 0 || snap)) {
       int at = before * p.units, b = b_lo, n;
       for (;; ++b) {
-        n = chunks_of(b) * p.units;
+        n = span_of(b) * p.units;
         if (x < at + n) break;
         at += n;
       }

@@ -11,9 +11,9 @@
 // largest element in [128, 256); hi = e4m3(q), lo = e4m3(q - hi), so hi + lo holds the 8 bits of a
 // bf16 down to 2^-9 of that scale, 2^-17 of the row's largest element (both terms into one sum).
 // Weights w = p sv: hi = e4m3(w), lo = e4m3(16 (w - hi)), 8 bits down to 2^-14, in two sums (columns
-// 0..63 and 64..127 of one product).  The largest w of a row is 1 when its reference is set and may
-// grow to 2^8.5; only a score that goes beyond raises the reference and rescales the sums (with room
-// for 2^4.5 only, some row of 40 did so in half of the chunks).  l sums p in fp32.  Both p and w are
+// 0..63 and 64..127 of one product).  The largest w of a row is 2^-2 when its reference is set and may
+// grow to 2^8.5; only a score that goes beyond raises the reference and rescales the sums, of its
+// block of eight rows (from 2^0, and all rows: 144 us for 40 rows instead of TCNEW).  l sums p in fp32.  Both p and w are
 // relative to the one reference, which follows t + log2(sv).
 //
 // Warps stay together: whatever lanes do alone ends in a __syncwarp before the next barrier or TMEM
@@ -47,7 +47,7 @@ struct Dec8TcCfg {
                                64 * 8;
 };
 
-constexpr float kTcTop = 8.5f;  // largest exponent of a weight (0 at a new reference)
+constexpr float kTcTop = 8.5f, kTcStart = -2.f;  // largest exponent of a weight; the one at a new reference
 
 // Instruction descriptor with both operands MN-major.
 constexpr uint32_t kMnMajorBoth = (1u << 15) | (1u << 16);
@@ -83,8 +83,9 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
   uint8_t* const sm_p = ring + C::kOffP;
   uint8_t* const sm_q = ring + C::kOffQ;
   float* const sm_scale = reinterpret_cast<float*>(ring + C::kOffMisc);        // [kScales][2][8]
-  float2* const sm_fw = reinterpret_cast<float2*>(sm_scale + C::kScales * 16);  // [R]: factor, reference
-  int* const sm_limit = reinterpret_cast<int*>(sm_fw + R);                      // [R]
+  float* const sm_f = sm_scale + C::kScales * 16;             // [R]: factor of a row's scores
+  float* const sm_ref = sm_f + R;                             // [R]: minus its reference
+  int* const sm_limit = reinterpret_cast<int*>(sm_ref + R);   // [R]
   uint32_t* const sm_nan = reinterpret_cast<uint32_t*>(sm_limit + R);           // [R][4]
   float* const sm_red = reinterpret_cast<float*>(sm_nan + R * 4);               // [2][4][kCols]
   uint64_t* const full = reinterpret_cast<uint64_t*>(sm_red + 4 * R);
@@ -270,7 +271,8 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
       // this group's query rows: columns [col0, col0 + 8 blocks) of the tile, half of them rounded up
       const int rows = min(R, p.rows - tile * R), share8 = (rows + 15) >> 4;
       const int col0 = w * share8 * 8, blocks = w ? ((rows + 7) >> 3) - share8 : share8;
-      float2* const fw = sm_fw + col0;
+      const float* const fac = sm_f + col0;
+      float* const ref = sm_ref + col0;
       const int* const limit = sm_limit + col0;
       {
         // the query tile: four threads a row, 32 elements each
@@ -320,7 +322,8 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         if (part == 0) {
           // scores are q . k times 2^(e - 7); a row that is not finite makes everything of its own NaN
           const float f = finite ? p.tau * 0.0078125f * __uint_as_float((uint32_t)be << 23) : __uint_as_float(0x7FC00000u);
-          sm_fw[r] = make_float2(f, 0.f);
+          sm_f[r] = f;
+          sm_ref[r] = 0.f;
           sm_limit[r] = in ? seg.len - p.Nq + 1 + i : seg.len;
         }
         sm_nan[tid] = 0u;  // R * 4 words
@@ -331,22 +334,34 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
       mbar_arrive(q_full);
 
       constexpr int N = C::kCols;
-      float l[N];
+      uint64_t l2[N / 2];  // sums of p, two rows a register pair
 #pragma unroll
-      for (int r = 0; r < N; ++r) l[r] = 0.f;
+      for (int r = 0; r < N / 2; ++r) l2[r] = 0;
       const int first_limit = seg.len - p.Nq + 1 + (tile * R) / p.G;
 
       for (int c = seg.c0; c < seg.c1; ++c, ++n) {
         const uint32_t buf = n & 1u, use = n >> 1;
-        // the chunk's scales, its V rows (which may be cleaned here), its scores
-        if (ok) ok = mbar_wait(full + 2 * pair, kphase) && mbar_wait(full + 2 * pair + 1, kphase) &&
-                     mbar_wait(s_full + buf, use & 1u);
+        // the chunk's scores, scales, and V rows (which may be cleaned here)
+        if (ok) ok = mbar_wait(s_full + buf, use & 1u) && mbar_wait(full + 2 * pair, kphase) &&
+                     mbar_wait(full + 2 * pair + 1, kphase);
         __syncwarp();
         tc_fence_after();
         const int j = c * kDec8Keys + row;
-        const float sk = sm_scale[entry * 16 + (row >> 4)], sv = sm_scale[entry * 16 + 8 + (row >> 4)];
-        const float lsv = __log2f(sv), lse_v = lsv < -60.f ? -60.f : lsv;  // (a zero scale weighs nothing)
+        const float sk = sm_scale[entry * 16 + (row >> 4)];
+        float sv = sm_scale[entry * 16 + 8 + (row >> 4)];
         const bool partly = (c + 1) * kDec8Keys > first_limit, fresh = c == seg.c0;
+        if (__any_sync(0xffffffffu, !(sv < INFINITY))) {
+          // (rare) a scale that is not finite makes NaN of what sees its rows, and of nothing else
+          const bool bad = !(sv < INFINITY);
+          if (w == 0)
+#pragma unroll 1
+            for (int r = 0; r < rows; ++r)
+              if (bad && j < sm_limit[r])
+                for (int k = 0; k < 4; ++k) atomicOr(sm_nan + r * 4 + k, 0xFFFFFFFFu);
+          if (bad) sv = 0.f;
+          __syncwarp();
+        }
+        const float lsv = fmaxf(__log2f(sv), -60.f);  // (a zero scale weighs nothing)
         float s[N];
 #pragma unroll
         for (int b = 0; b < N / 8; ++b)
@@ -355,53 +370,73 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         tc_fence_before();
         mbar_arrive(s_empty + buf);
         // exponents t - reference, and whether one is past the top
-        float most = kDec8Low;
+        float most[N / 8];
+        const uint64_t sk2 = f2(sk, sk);
 #pragma unroll
         for (int b = 0; b < N / 8; ++b)
           if (b < blocks) {
 #pragma unroll
-            for (int x = b * 8; x < b * 8 + 8; x += 2) {
-              const float4 f = *reinterpret_cast<const float4*>(fw + x);
-              s[x] = fmaf(s[x] * sk, f.x, -f.y);
-              s[x + 1] = fmaf(s[x + 1] * sk, f.z, -f.w);
-              if (partly) {
-                if (j >= limit[x]) s[x] = -INFINITY;
-                if (j >= limit[x + 1]) s[x + 1] = -INFINITY;
-              }
-              most = fmax3(most, s[x], s[x + 1]);
+            for (int x = b * 8; x < b * 8 + 8; x += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(fac + x), m = *reinterpret_cast<const float4*>(ref + x);
+              f2_split(f2_fma(f2_mul(f2(s[x], s[x + 1]), sk2), f2(f.x, f.y), f2(m.x, m.y)), s[x], s[x + 1]);
+              f2_split(f2_fma(f2_mul(f2(s[x + 2], s[x + 3]), sk2), f2(f.z, f.w), f2(m.z, m.w)), s[x + 2], s[x + 3]);
             }
           }
-        if (group_any(2 + w, fresh || most + lse_v > kTcTop)) {
-          // new references: the largest exponent of each row over the group's threads
+        if (partly) {
+#pragma unroll
+          for (int x = 0; x < N; ++x)
+            if (j >= limit[x < blocks * 8 ? x : 0]) s[x] = -INFINITY;
+        }
+#pragma unroll
+        for (int b = 0; b < N / 8; ++b) {
+          most[b] = kDec8Low;
+          if (b < blocks)
+#pragma unroll
+            for (int x = b * 8; x < b * 8 + 8; x += 2) most[b] = fmax3(most[b], s[x], s[x + 1]);
+        }
+        if (group_any(2 + w, fresh || fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) + lsv > kTcTop)) {
+          // new references: the largest exponent of each row over the group's threads; a warp looks
+          // at the blocks in which it has one past the top
 #pragma unroll
           for (int b = 0; b < N / 8; ++b)
-            if (b < blocks)
+            if (b < blocks) {
+              float m = kDec8Low;  // lane x < 8: of row 8 b + x
+              if (__any_sync(0xffffffffu, fresh || most[b] + lsv > kTcTop))
 #pragma unroll
-              for (int x = b * 8; x < b * 8 + 8; ++x) {
-                const float v = s[x] + lse_v;
-                const int m = __reduce_max_sync(0xffffffffu, v == v ? ordered(v) : ordered(-INFINITY));
-                if (lane == 0) red[quarter * N + x] = unordered(m);
-              }
+                for (int x = 0; x < 8; ++x) {
+                  const float v = s[b * 8 + x] + lsv;
+                  const int i = __reduce_max_sync(0xffffffffu, v == v ? ordered(v) : ordered(-INFINITY));
+                  if (lane == x) m = unordered(i);
+                }
+              if (lane < 8) red[quarter * N + b * 8 + lane] = m;
+            }
           __syncwarp();
           asm volatile("bar.sync %0, 128;" ::"r"(2 + w) : "memory");
           // the sums so far move to the new references (after the last product into them)
           if (!fresh && ok) ok = mbar_wait(p_done + (buf ^ 1u), ((n - 1) >> 1) & 1u);
           __syncwarp();
           tc_fence_after();
+          const float least = fresh ? -INFINITY : kTcTop;  // rows at most there keep their reference
 #pragma unroll
           for (int b = 0; b < N / 8; ++b)
             if (b < blocks) {
-              float up[8];
+              float up[8], any = -INFINITY;
 #pragma unroll
               for (int x = 0; x < 8; ++x) {
                 const int r = b * 8 + x;
-                const float m = fmaxf(fmaxf(red[r], red[N + r]), fmaxf(red[2 * N + r], red[3 * N + r]));
-                // rows that stay under the top keep theirs, but all get their first one here
-                up[x] = m > (fresh ? -INFINITY : kTcTop) ? m : 0.f;
+                up[x] = fmaxf(fmax3(red[r], red[N + r], red[2 * N + r]), red[3 * N + r]);
+                any = fmaxf(any, up[x]);
+              }
+              if (any <= least) continue;
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const int r = b * 8 + x;
+                up[x] = up[x] > least ? up[x] - kTcStart : 0.f;
                 s[r] -= up[x];
                 up[x] = ex2_approx(-up[x]);
-                l[r] *= up[x];
               }
+#pragma unroll
+              for (int x = 0; x < 8; x += 2) l2[b * 4 + x / 2] = f2_mul(l2[b * 4 + x / 2], f2(up[x], up[x + 1]));
               if (!fresh) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -417,8 +452,8 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
             }
           tmem_wait_st();
           if (row < blocks * 8) {  // (every thread has used the old references)
-            const float m = fmaxf(fmaxf(red[row], red[N + row]), fmaxf(red[2 * N + row], red[3 * N + row]));
-            if (m > (fresh ? -INFINITY : kTcTop)) fw[row].y += m;
+            const float m = fmaxf(fmax3(red[row], red[N + row], red[2 * N + row]), red[3 * N + row]);
+            if (m > least) ref[row] -= m - kTcStart;
           }
           __syncwarp();
           asm volatile("bar.sync %0, 128;" ::"r"(2 + w) : "memory");
@@ -458,28 +493,30 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         // the weights replace those of the chunk before the last once their product is done
         if (n >= 2 && ok) ok = mbar_wait(p_done + buf, (use - 1) & 1u);
         uint8_t* const prow = sm_p + buf * C::kP + row * 128;
+        const uint64_t sv2 = f2(sv, sv), sv16 = f2(sv * 16.f, sv * 16.f), m16 = f2(-16.f, -16.f);
 #pragma unroll
         for (int b = 0; b < N / 8; ++b)
           if (b < blocks) {
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              float wj[4];
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const int r = b * 8 + 4 * x + y;
-                const float pj = ex2_approx(s[r]);
-                l[r] += pj;
-                wj[y] = pj * sv;
-                if (partly && j >= limit[r]) wj[y] = 0.f;  // a NaN scale is not for this query
-              }
-              hi[x] = e4m3x4(wj[0], wj[1], wj[2], wj[3]);
+              const int r = b * 8 + 4 * x;
+              const uint64_t p0 = f2(ex2_approx(s[r]), ex2_approx(s[r + 1]));
+              const uint64_t p1 = f2(ex2_approx(s[r + 2]), ex2_approx(s[r + 3]));
+              l2[r / 2] = f2_add(l2[r / 2], p0);
+              l2[r / 2 + 1] = f2_add(l2[r / 2 + 1], p1);
+              float w0, w1, w2, w3;
+              f2_split(f2_mul(p0, sv2), w0, w1);
+              f2_split(f2_mul(p1, sv2), w2, w3);
+              hi[x] = e4m3x4(w0, w1, w2, w3);
               uint32_t b0, b1;
               e4m3x4_to_f16(hi[x], b0, b1);
               const float2 f0 = __half22float2(*reinterpret_cast<__half2*>(&b0));
               const float2 f1 = __half22float2(*reinterpret_cast<__half2*>(&b1));
-              lo[x] = e4m3x4(fmaf(-16.f, f0.x, wj[0] * 16.f), fmaf(-16.f, f0.y, wj[1] * 16.f),
-                             fmaf(-16.f, f1.x, wj[2] * 16.f), fmaf(-16.f, f1.y, wj[3] * 16.f));
+              // 16 (w - hi), with 16 w = p (16 sv) the same value
+              f2_split(f2_fma(f2(f0.x, f0.y), m16, f2_mul(p0, sv16)), w0, w1);
+              f2_split(f2_fma(f2(f1.x, f1.y), m16, f2_mul(p1, sv16)), w2, w3);
+              lo[x] = e4m3x4(w0, w1, w2, w3);
             }
             const int at = col0 + b * 8;  // byte of the row; its 16-byte unit is swizzled
             *reinterpret_cast<uint2*>(prow + (((at >> 4) ^ (row & 7)) << 4) + (at & 8)) = make_uint2(hi[0], hi[1]);
@@ -493,6 +530,9 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
       }
 
       // ------------------------------------------------------------ a unit's end
+      float l[N];
+#pragma unroll
+      for (int r = 0; r < N; r += 2) f2_split(l2[r / 2], l[r], l[r + 1]);
       // l of a row over the 128 threads: half of the rows are exchanged between lanes 16 apart, half
       // of the rest between lanes 8 apart, ..., so that lane x ends with the sum of row x
 #pragma unroll
@@ -524,7 +564,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
             const int r = b * 8 + x, tr = col0 + r, qr = tile * R + tr;
             if (tr >= rows) continue;
             const float L = red[r] + red[N + r] + red[2 * N + r] + red[3 * N + r];
-            const float M = L == 0.f ? kDec8Low : fw[r].y;  // nothing seen: no reference
+            const float M = L == 0.f ? kDec8Low : -ref[r];  // nothing seen: no reference
             float A = fmaf(lo[x], 0.0625f, hi[x]);
             if ((sm_nan[tr * 4 + (row >> 5)] >> (row & 31)) & 1u) A = __uint_as_float(0x7FC00000u);
             if (whole) {
