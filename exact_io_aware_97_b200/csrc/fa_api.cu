@@ -1072,7 +1072,7 @@ fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
 }
 
 // What a unit costs beside its chunks, in chunks (measured on ragged batches).
-constexpr int kDec8Lead = 1, kDec8TcLead = 3;
+constexpr int kDec8Lead = 4, kDec8TcLead = 10;
 // Query rows of a unit: one tensor-core tile of 16 where that holds them; else the kernel on tcgen05
 // products with 64 (d = 128: 40 rows in TCNEW us instead of 205 with 64 rows in registers), or
 // registers for 32 or 64 (d = 64, where a cache row is too short for those products' 128 rows).
