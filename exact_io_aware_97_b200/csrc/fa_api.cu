@@ -1081,9 +1081,10 @@ int dec8_tile(int64_t rows, int d) { return rows <= 16 ? 16 : rows <= 32 && d ==
 // not the loads, take the time then, and one head's queries are all that shared memory holds).
 int dec8_heads(int tile, int Hkv) { return tile > 16 ? 0 : Hkv % 4 == 0 ? 2 : Hkv % 2 == 0 ? 1 : 0; }
 // One wave of CTAs (where no device is present, the number of the B200's).
-int dec8_ctas(int tile) {
+int dec8_ctas(int tile, int d) {
   const int sms = sm_count_cached();
-  return (sms > 0 ? sms : 148) * (tile <= 32 ? 2 : 1);
+  return (sms > 0 ? sms : 148) * (tile == 16 ? (d == 64 ? Dec8Cfg<64, 1, 1>::kCtas : Dec8Cfg<128, 1, 1>::kCtas)
+                                  : tile == 32 ? Dec8Cfg<64, 2, 1>::kCtas : 1);
 }
 
 bool dec8_maps(CUtensorMap (&maps)[2], const void* kp, const void* vp, int d, const Dec8Params& prm) {
@@ -1129,7 +1130,7 @@ fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& pr
   auto kern = fa_decode_fp8_kernel<D, MT, RG>;
   static std::atomic<uint64_t> smem_set{0};  // a bit for each device
   if (!set_smem_once(kern, C::kSmem, smem_set)) return FA_ERR_CUDA;
-  const int ctas = dec8_ctas(C::kRows);
+  const int ctas = dec8_ctas(C::kRows, D);
   kern<<<ctas, C::kThreads, C::kSmem, st>>>(maps[0], maps[1], prm);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   return launch_decode_fp8_merge<D, C::kRows>(prm, ctas, st);
@@ -1141,7 +1142,7 @@ fa_status launch_decode_fp8_tc(const void* kp, const void* vp, const Dec8Params&
   if (!dec8_maps(maps, kp, vp, C::D, prm)) return FA_ERR_CUDA;
   static std::atomic<uint64_t> smem_set{0};
   if (!set_smem_once(fa_decode_fp8_tc_kernel, C::kSmem, smem_set)) return FA_ERR_CUDA;
-  const int ctas = dec8_ctas(C::kRows);
+  const int ctas = dec8_ctas(C::kRows, C::D);
   fa_decode_fp8_tc_kernel<<<ctas, C::kThreads, C::kSmem, st>>>(maps[0], maps[1], prm);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   return launch_decode_fp8_merge<C::D, C::kRows>(prm, ctas, st);
@@ -1186,7 +1187,7 @@ extern "C" size_t fa_decode_paged_fp8_workspace_size(int B, int Nq, int Hq, int 
   if (B <= 0 || Nq <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0) return 0;
   // two parts per CTA (sums, then m and l) and a descriptor per CTA
   const int tile = dec8_tile((int64_t)Nq * (Hq / Hkv), d);
-  const size_t ctas = (size_t)dec8_ctas(tile);
+  const size_t ctas = (size_t)dec8_ctas(tile, d);
   const size_t slots = (2 * ctas * tile) << dec8_heads(tile, Hkv);
   return align_up(slots * d * 4, 256) + align_up(slots * 8, 256) + align_up(ctas * 16, 256);
 }
@@ -1232,7 +1233,7 @@ extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, con
   prm.tiles = (prm.rows + tile - 1) / tile;
   prm.hs = dec8_heads(tile, Hkv);
   prm.box = std::min(page_size, kDec8Keys >> prm.hs);
-  const size_t ctas = (size_t)dec8_ctas(tile);
+  const size_t ctas = (size_t)dec8_ctas(tile, d);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   prm.ws_acc = reinterpret_cast<float*>(ws);
   const size_t slots = (2 * ctas * tile) << prm.hs;

@@ -260,8 +260,9 @@ __global__ void __launch_bounds__(kAppendCta * 32, 4) fa_cache_append_kernel(con
   const int end = p.cu ? __ldg(p.cu + b + 1) : b + 1;
   const int idx = p.cu ? u - ((max(start, 0) >> p.sb_shift) + 2 * b) : 0;
   const int n = end - start, len = __ldg(p.seqlens + b);
-  // a sequence without new rows, or one whose offsets or length cannot be used
-  if (start < 0 || end > p.total || n <= 0) return;
+  // a slot before the first sequence's (rows before cu[0] belong to none), a sequence without new
+  // rows, or one whose offsets or length cannot be used
+  if (idx < 0 || start < 0 || end > p.total || n <= 0) return;
   if (n > len || (long long)len > (long long)p.max_pages << p.page_shift) {
     if (threadIdx.x == 0) atomicOr(&g_error_word, kErrBadSeqlens);
     return;

@@ -73,11 +73,12 @@ struct Dec8Cfg {
   static constexpr bool kSplitRegs = MT > 1;
   static constexpr int kComputeRegs = RG == 1 ? 208 : 224;
   static constexpr int kThreads = (kWarps + (kSplitRegs ? 4 : 1)) * 32;
-  static constexpr int kCtas = RG == 1 ? 2 : 1;     // per SM
+  // per SM: what the registers allow; d = 64 has room for three (16 x 32K rows: 118 -> 105 us)
+  static constexpr int kCtas = MT == 1 && D == 64 ? 3 : RG == 1 ? 2 : 1;
   static constexpr int kHalf = kDec8Keys * D;       // bytes of K (or V) of a chunk
   static constexpr int kStage = 2 * kHalf;          // also the size of the merge of 16 rows of 4 slices
   static_assert(kStage >= 4 * 16 * D * 4, "a stage holds the sums of 16 query rows of the four slices");
-  static constexpr int kStages = (D == 128 ? 3 : 6) * (RG == 1 ? 1 : 2);
+  static constexpr int kStages = D == 128 ? 3 * RG : MT == 1 ? 4 : 6 * RG;
   static constexpr int kQBytes = MT == 1 ? 0 : RG * MT * (D / 16) * 32 * 16;
   static constexpr int kSmem = 1024 + kStages * kStage + kQBytes + RG * 4 * 16 * 8 + kStages * 16 * 4 +
                                2 * kStages * 8;

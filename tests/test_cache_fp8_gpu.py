@@ -300,6 +300,20 @@ def test_append_is_the_model_bit_for_bit(case, grow):
         _same(_run_append(kc2, ks2, vc2, vs2, table2, lens2, None, xs2), kc, ks, vc, vs)
 
 
+def test_append_rows_before_and_after_the_sequences():
+    """Offsets may start past 0 and end before the last row: those rows belong to no sequence."""
+    rng = np.random.default_rng(5012)
+    old, new, H, d, ps, sb = [3, 0, 40], [2, 35, 1], 2, 128, 32, 16
+    kc, ks, vc, vs, table, lens, xs = _append_problem(rng, old, new, H, d, ps, sb)
+    junk = [torch.full((n, H, d), float("nan"), dtype=torch.bfloat16) for n in (77, 50)]
+    cu = [77, 79, 114, 115]
+    dev = _run_append(kc, ks, vc, vs, table, lens, cu, [torch.cat([junk[0], x, junk[1]]) for x in xs])
+    for codes, scales, x in ((kc, ks, xs[0]), (vc, vs, xs[1])):
+        cache8.append(codes, scales, x.double().numpy(), table, lens, [0, 2, 37, 38], sb)
+    _same(dev, kc, ks, vc, vs)
+    assert fa.fa_last_device_error() == fa.FA_OK
+
+
 def test_append_special_values():
     """Zeros, signed zeros, the type's extremes, subnormals, and rows that are not finite."""
     rng = np.random.default_rng(5007)
