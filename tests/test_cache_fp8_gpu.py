@@ -380,6 +380,69 @@ def test_append_skips_and_records_what_it_cannot_use():
     assert fa.fa_last_device_error() == fa.FA_OK
 
 
+@pytest.mark.parametrize("Nq", [1, 3], ids=["16rows", "24rows"])
+def test_cache_past_32_bit_offsets(Nq):
+    """A pool of more than 2^32 bytes: a sequence in its last pages gives the bits that it gives in a
+    small pool, appended and read."""
+    rng = np.random.default_rng(5013)
+    lens, H, d, ps, sb = [150], 8, 128, 64, 16
+    kc, ks, vc, vs, table, lens, xs = _append_problem(rng, [100], [50], H, d, ps, sb)
+    cu = [0, 50]
+    q = torch.from_numpy(rng.standard_normal((1, Nq, 64, d))).cuda().bfloat16()
+    small = _run_append(kc, ks, vc, vs, table, lens, cu, xs)
+    want = fa.decode_paged_fp8(q, small[0], small[2], small[1], small[3], small[4], small[5])
+    P = (1 << 32) // (ps * H * d) + 10
+    base = P - kc.shape[0]
+    big = []
+    for host in (kc, ks, vc, vs):
+        t = torch.zeros(P, *host.shape[1:], dtype=torch.uint8 if host.dtype == np.uint8 else torch.float32, device="cuda")
+        t[base:] = torch.from_numpy(host.astype(np.uint8 if host.dtype == np.uint8 else np.float32)).cuda()
+        big.append(t)
+    t = torch.from_numpy(np.where(table >= 0, table + base, -1).astype(np.int32)).cuda()
+    fa.cache_append_fp8(xs[0].cuda(), xs[1].cuda(), big[0], big[2], big[1], big[3], t, small[5],
+                        torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    got = fa.decode_paged_fp8(q, big[0], big[2], big[1], big[3], t, small[5])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(big[0][base:], small[0].view(torch.uint8)) and not big[0][:base:997].any()
+    # and its pages move: compaction brings them to the front
+    t2, n = fa.pages_compact([*big], t, small[5], ps)
+    assert int(n) == 3 and int(t2.max()) <= 2
+    got = fa.decode_paged_fp8(q, big[0], big[2], big[1], big[3], t2, small[5])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert fa.fa_last_device_error() == fa.FA_OK
+
+
+def test_decode_fp8_two_streams_at_once():
+    """Calls with workspaces of their own do not disturb one another, nor does a captured one."""
+    rng = np.random.default_rng(5014)
+    jobs = []
+    for lens, Nq, Hq, H, d in (([700, 20, 300], 1, 16, 4, 128), ([900, 64], 4, 8, 1, 128), ([500], 2, 4, 2, 64)):
+        kc, ks, vc, vs, table = cache8.build(rng, lens, 32, 16, H, d)
+        dev = cache8.to_device(kc, ks, vc, vs, table, lens)
+        q = torch.from_numpy(rng.standard_normal((len(lens), Nq, Hq, d))).cuda().bfloat16()
+        jobs.append((q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5]))
+    want = [fa.decode_paged_fp8(*j) for j in jobs]
+    graphs = []
+    for j in jobs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = fa.decode_paged_fp8(*j)
+        graphs.append((g, out))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(6)]
+    got = []
+    for i in range(30):
+        with torch.cuda.stream(streams[i % 3]):
+            got.append((i % 3, fa.decode_paged_fp8(*jobs[i % 3])))
+        if i % 5 == 0:
+            with torch.cuda.stream(streams[3 + i % 3]):
+                graphs[i % 3][0].replay()
+    torch.cuda.synchronize()
+    got += [(i, out) for i, (_, out) in enumerate(graphs)]
+    for i, (o, lse) in got:
+        assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
 def test_prefill_then_decode_through_the_cache():
     """The whole path: rope, forward, append of the prompt, then steps of rope, append and decode,
     against attention in 64 bits over what the cache holds; once more through a captured graph on

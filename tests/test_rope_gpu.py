@@ -143,6 +143,43 @@ def test_rope_scores_depend_on_distance_only():
     assert (outs[0] - outs[1]).abs().max() <= 2 * 4 * 4 * 2.0 ** -7
 
 
+def test_rope_in_training():
+    """Forward and backward through rope and attention, against the oracle's backward on q and k
+    turned in 64 bits, turned back in 64 bits.  Bounds of check_grad: rounding q and k after the
+    turn adds one bf16 rounding (2^-8) to each element, of the size of those it already allows for."""
+    import oracle as oracle_mod
+    from parity import check_grad, host64
+    orc = oracle_mod.get()
+    B, N, Hq, H, d, rot = 1, 200, 4, 2, 64, 48
+    q, dy = (tensor(4008, t, (B, N, Hq, d), torch.bfloat16) for t in (1, 4))
+    k, v = (tensor(4008, t, (B, N, H, d), torch.bfloat16) for t in (2, 3))
+    freqs = fa.rope_frequencies(rot, 10000.0, "linear", 4.0)
+    pos = torch.arange(5000, 5000 + N, dtype=torch.int32, device="cuda").view(B, N)
+    tq, tk = fa.rope(q, k, freqs, pos, interleaved=True)
+    o, lse = fa.forward(tq, tk, v, causal=True)
+    gq, gk, gv = fa.backward(tq, tk, v, o, lse, dy, causal=True)
+    gq, gk = fa.rope_backward(gq, gk, freqs, pos, interleaved=True)
+    w, p = freqs.cpu().numpy(), pos.cpu().numpy().reshape(-1)
+    turn = lambda x, h, back: turn64(x.reshape(N, h, d), p, w, rot, True, 1.0, back)[0].reshape(B, N, h, d)  # noqa: E731
+    rq, rk, rv = orc.attention_bwd(turn(host64(q), Hq, False), turn(host64(k), H, False), host64(v), host64(dy),
+                                   d ** -0.5, causal=True)
+    check_grad(host64(gq), turn(np.asarray(rq, np.float64), Hq, True), "dQ")
+    check_grad(host64(gk), turn(np.asarray(rk, np.float64), H, True), "dK")
+    check_grad(host64(gv), np.asarray(rv, np.float64), "dV")
+
+
+def test_rope_past_32_bit_offsets():
+    """More than 2^31 elements: the last rows are those of a small call."""
+    N = (1 << 31) // (64 * 128) + 100
+    q = torch.zeros(N, 64, 128, dtype=torch.bfloat16, device="cuda")
+    tail = tensor(4009, si.Q, (100, 64, 128), torch.bfloat16)
+    q[-100:] = tail
+    freqs = fa.rope_frequencies(128)
+    want, _ = fa.rope(tail, None, freqs, torch.arange(N - 100, N, dtype=torch.int32, device="cuda"))
+    fa.rope(q, None, freqs, q_out=q)
+    assert torch.equal(q[-100:], want) and not q[:-100:9973].any()
+
+
 def test_rope_on_another_stream_and_captured():
     q, k = tensor(4007, si.Q, (40, 8, 128), torch.bfloat16), tensor(4007, si.K, (40, 2, 128), torch.bfloat16)
     freqs = fa.rope_frequencies(128)
