@@ -591,12 +591,9 @@ def _home(first, *others) -> int:
     return idx
 
 
-def _at(idx: int, call):
+def _elsewhere(idx: int) -> bool:
     import torch
-    if idx == torch._C._cuda_getDevice():
-        return call()
-    with torch.cuda.device(idx):
-        return call()
+    return idx != torch._C._cuda_getDevice()
 
 
 def _dense(**tensors) -> None:
@@ -675,23 +672,34 @@ def _rope(q, k, freqs, positions, interleaved, amplitude, q_out, k_out, stream, 
         raise ValueError(f"q_out: expected {dt} {tuple(qs)}, got {q_out.dtype} {tuple(q_out.shape)}")
     if k_out is not None and (k_out.shape != ks or k_out.dtype != dt):
         raise ValueError(f"k_out: expected {dt} {tuple(ks)}, got {k_out.dtype} {tuple(k_out.shape)}")
-    idx = _home(q, k, freqs, positions, q_out, k_out)
+    if _elsewhere(_home(q, k, freqs, positions, q_out, k_out)):
+        with torch.cuda.device(q.device):
+            return _rope(q, k, freqs, positions, interleaved, amplitude, q_out, k_out, stream, backward)
     # like the input where that is dense; empty_like would keep the strides of a slice's dimensions
+    dense = Hq * d
+    sq = syq = dense
+    if not q.is_contiguous():
+        sq = _row_stride(q, "q")
     if q_out is None:
-        q_out = torch.empty_like(q) if q.is_contiguous() else q.new_empty(qs)
-    if k is not None and k_out is None:
-        k_out = torch.empty_like(k) if k.is_contiguous() else k.new_empty(ks)
-    if rows == 0:
-        return q_out, k_out
-
-    def call():
-        _check(load().fa_rope(q.data_ptr(), k.data_ptr() if Hk else None, q_out.data_ptr(),
-                              k_out.data_ptr() if Hk else None, None if positions is None else positions.data_ptr(),
-                              freqs.data_ptr(), rows, period, Hq, Hk, d, rot, 1 if interleaved else 0, amplitude,
-                              1 if backward else 0, FA_BF16 if dt == torch.bfloat16 else FA_F32, _row_stride(q, "q"),
-                              _row_stride(k, "k") if Hk else 0, _row_stride(q_out, "q_out"),
-                              _row_stride(k_out, "k_out") if Hk else 0, _stream(stream)), "fa_rope")
-    _at(idx, call)
+        q_out = torch.empty_like(q) if sq == dense else q.new_empty(qs)
+    elif not q_out.is_contiguous():
+        syq = _row_stride(q_out, "q_out")
+    sk = syk = Hk * d
+    if k is not None:
+        if not k.is_contiguous():
+            sk = _row_stride(k, "k")
+        if k_out is None:
+            k_out = torch.empty_like(k) if sk == Hk * d else k.new_empty(ks)
+        elif not k_out.is_contiguous():
+            syk = _row_stride(k_out, "k_out")
+    if rows > 0:
+        st = load().fa_rope(q.data_ptr(), k.data_ptr() if Hk else None, q_out.data_ptr(),
+                            k_out.data_ptr() if Hk else None, None if positions is None else positions.data_ptr(),
+                            freqs.data_ptr(), rows, period, Hq, Hk, d, rot, 1 if interleaved else 0, amplitude,
+                            1 if backward else 0, FA_BF16 if dt == torch.bfloat16 else FA_F32, sq, sk, syq, syk,
+                            _stream(stream))
+        if st != FA_OK:
+            raise FaError(st, "fa_rope")
     return q_out, k_out
 
 
@@ -752,21 +760,21 @@ def cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seql
             raise ValueError(f"k: expected one row for each of {B} sequences without cu_seqlens, got {total}")
     elif cu_seqlens.dim() != 1 or cu_seqlens.shape[0] != B + 1:
         raise ValueError(f"cu_seqlens: expected [B + 1 = {B + 1}] offsets, got shape {tuple(cu_seqlens.shape)}")
-    idx = _home(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, cu_seqlens)
+    if _elsewhere(_home(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, cu_seqlens)):
+        with torch.cuda.device(k.device):
+            return cache_append_fp8(k, v, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, cu_seqlens, stream)
     if not (k.is_contiguous() and v.is_contiguous()):
         raise ValueError(f"k, v: expected contiguous tensors, got strides {tuple(k.stride())} and {tuple(v.stride())}")
     if cu_seqlens is not None:
         _is_i32(cu_seqlens=cu_seqlens)
         _dense(cu_seqlens=cu_seqlens)
 
-    def call():
+    if B > 0 and total > 0:
         _check(load().fa_cache_append_fp8(k.data_ptr(), v.data_ptr(),
                                           None if cu_seqlens is None else cu_seqlens.data_ptr(),
                                           block_table.data_ptr(), seqlens.data_ptr(), k_pages.data_ptr(),
                                           v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), B, total, Hkv, P,
                                           ps, maxp, sb, d, _stream(stream)), "fa_cache_append_fp8")
-    if B > 0 and total > 0:
-        _at(idx, call)
 
 
 def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, scale=None, out=None, lse=None,
@@ -790,28 +798,31 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens
         _expect(out, shape, "torch.bfloat16", "out")
     if lse is not None:
         _expect(lse, lse_shape, "torch.float32", "lse")
-    idx = _home(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace)
+    if _elsewhere(_home(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, out, lse, workspace)):
+        with torch.cuda.device(q.device):
+            return decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, scale, out, lse,
+                                    workspace, stream)
     if not q.is_contiguous():
         raise ValueError(f"q: expected a contiguous tensor, got strides {tuple(q.stride())} for shape {tuple(shape)}")
     if out is not None or lse is not None or workspace is not None:
         _dense(out=out, lse=lse, workspace=workspace)
 
-    def call():
-        lib = load()
-        o = out if out is not None else torch.empty_like(q)
-        ml = lse if lse is not None else q.new_empty(lse_shape, dtype=torch.float32)
-        if workspace is None:
-            nbytes = lib.fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d)
-            ws = q.new_empty(max(nbytes, 1), dtype=torch.uint8)
-        else:
-            ws, nbytes = workspace, workspace.numel() * workspace.element_size()
-        if B > 0 and Nq > 0 and Hq > 0:
-            _check(lib.fa_decode_paged_fp8(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
-                                           v_scale.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(),
-                                           o.data_ptr(), ml.data_ptr(), B, Nq, Hq, Hkv, P, ps, maxp, sb, d, scale,
-                                           ws.data_ptr(), nbytes, _stream(stream)), "fa_decode_paged_fp8")
-        return o, ml
-    return _at(idx, call)
+    lib = load()
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = q.new_empty(lse_shape, dtype=torch.float32)
+    if workspace is None:
+        nbytes = lib.fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d)
+        workspace = q.new_empty(max(nbytes, 1), dtype=torch.uint8)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    if B > 0 and Nq > 0 and Hq > 0:
+        _check(lib.fa_decode_paged_fp8(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+                                       v_scale.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), out.data_ptr(),
+                                       lse.data_ptr(), B, Nq, Hq, Hkv, P, ps, maxp, sb, d, scale,
+                                       workspace.data_ptr(), nbytes, _stream(stream)), "fa_decode_paged_fp8")
+    return out, lse
 
 
 def _paged_table(pools, block_table, seqlens, num_pages):
@@ -843,22 +854,23 @@ def pages_fork(pools, block_table, seqlens, parent, page_size, num_pages=None, w
     _is_i32(parent=parent)
     _dense(parent=parent, workspace=workspace)
 
-    def call():
-        lib = load()
-        arr = _pool_array(pools, num_pages)
-        # one allocation for the four results
-        buf = block_table.new_empty(R * (maxp + 1) + num_pages + 1)
-        table, lens, free, n_free = buf.split((R * maxp, R, num_pages, 1))
-        if workspace is None:
-            nbytes = lib.fa_pages_workspace_size(num_pages, R)
-            ws = block_table.new_empty(max(nbytes, 1), dtype=torch.uint8)
-        else:
-            ws, nbytes = workspace, workspace.numel() * workspace.element_size()
-        _check(lib.fa_pages_fork(arr, len(pools), block_table.data_ptr(), seqlens.data_ptr(), parent.data_ptr(),
-                                 table.data_ptr(), lens.data_ptr(), free.data_ptr(), n_free.data_ptr(), B, R,
-                                 num_pages, page_size, maxp, ws.data_ptr(), nbytes, _stream(stream)), "fa_pages_fork")
-        return table.view(R, maxp), lens, free, n_free
-    return _at(_home(block_table, seqlens, parent, workspace, *pools), call)
+    if _elsewhere(_home(block_table, seqlens, parent, workspace, *pools)):
+        with torch.cuda.device(block_table.device):
+            return pages_fork(pools, block_table, seqlens, parent, page_size, num_pages, workspace, stream)
+    lib = load()
+    arr = _pool_array(pools, num_pages)
+    # one allocation for the four results
+    buf = block_table.new_empty(R * (maxp + 1) + num_pages + 1)
+    table, lens, free, n_free = buf.split((R * maxp, R, num_pages, 1))
+    if workspace is None:
+        nbytes = lib.fa_pages_workspace_size(num_pages, R)
+        workspace = block_table.new_empty(max(nbytes, 1), dtype=torch.uint8)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(lib.fa_pages_fork(arr, len(pools), block_table.data_ptr(), seqlens.data_ptr(), parent.data_ptr(),
+                             table.data_ptr(), lens.data_ptr(), free.data_ptr(), n_free.data_ptr(), B, R, num_pages,
+                             page_size, maxp, workspace.data_ptr(), nbytes, _stream(stream)), "fa_pages_fork")
+    return table.view(R, maxp), lens, free, n_free
 
 
 def pages_compact(pools, block_table, seqlens, page_size, num_pages=None, workspace=None, stream=None):
@@ -867,17 +879,18 @@ def pages_compact(pools, block_table, seqlens, page_size, num_pages=None, worksp
     B, maxp, num_pages = _paged_table(pools, block_table, seqlens, num_pages)
     _dense(workspace=workspace)
 
-    def call():
-        lib = load()
-        arr = _pool_array(pools, num_pages)
-        table, n_live = torch.empty_like(block_table), block_table.new_empty(1)
-        if workspace is None:
-            nbytes = lib.fa_pages_workspace_size(num_pages, 0)
-            ws = block_table.new_empty(max(nbytes, 1), dtype=torch.uint8)
-        else:
-            ws, nbytes = workspace, workspace.numel() * workspace.element_size()
-        _check(lib.fa_pages_compact(arr, len(pools), block_table.data_ptr(), seqlens.data_ptr(), table.data_ptr(),
-                                    n_live.data_ptr(), B, num_pages, page_size, maxp, ws.data_ptr(), nbytes,
-                                    _stream(stream)), "fa_pages_compact")
-        return table, n_live
-    return _at(_home(block_table, seqlens, workspace, *pools), call)
+    if _elsewhere(_home(block_table, seqlens, workspace, *pools)):
+        with torch.cuda.device(block_table.device):
+            return pages_compact(pools, block_table, seqlens, page_size, num_pages, workspace, stream)
+    lib = load()
+    arr = _pool_array(pools, num_pages)
+    table, n_live = torch.empty_like(block_table), block_table.new_empty(1)
+    if workspace is None:
+        nbytes = lib.fa_pages_workspace_size(num_pages, 0)
+        workspace = block_table.new_empty(max(nbytes, 1), dtype=torch.uint8)
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(lib.fa_pages_compact(arr, len(pools), block_table.data_ptr(), seqlens.data_ptr(), table.data_ptr(),
+                                n_live.data_ptr(), B, num_pages, page_size, maxp, workspace.data_ptr(), nbytes,
+                                _stream(stream)), "fa_pages_compact")
+    return table, n_live

@@ -10,7 +10,7 @@ exponentials).  lse: 2^-17 (1 + t).
 More than 16 query rows of a K/V head at d = 128 take the kernel that multiplies e4m3 bytes, with q and
 the weights as two e4m3 terms.  Weights: the first term is off by at most 2^-4 of the weight and the
 second by 2^-4 of that, 2^-8 together, where its 16-fold is normal; below, by half of 2^-9 / 16 = 2^-14
-while the largest weight of the row is at least 2^-2, so by 2^-12 of it: 2^-12 sum|v| times the
+while the largest weight of the row is at least 2^2, so by 2^-16 of it: 2^-16 sum|v| times the
 largest over the smallest scale.  q: exact down to the step of the second term, 2^-9 where the
 row's largest element is at least 2^7, so off by at most 2^-17 of that element: 2^-17 u for scores,
 with u = max|q| sum|k| scale in place of t = sum|q||k| scale."""
@@ -37,7 +37,7 @@ def check(o, lse, ref, q, kv):
     _, Nq, Hq, d = q64.shape
     if Nq * Hq // kv[0].shape[2] > 16 and d == 128:
         used = kv[3][np.isfinite(kv[3]) & (kv[3] > 0)]
-        weight, small = 2.0 ** -8, 2.0 ** -12 * used.max() / used.min()
+        weight, small = 2.0 ** -8, 2.0 ** -16 * used.max() / used.min()
         u = _score_bound(q64, kv)
     t = t_abs + u
     tt = t.transpose(0, 2, 1)[..., None]
