@@ -20,7 +20,7 @@
 // Warps stay together: whatever lanes do alone ends in a __syncwarp before the next barrier or TMEM
 // access, which are for whole warps.
 //
-// One CTA per SM: TMA producer, MMA issuer, two warpgroups that share the query rows of every chunk
+// One CTA per SM: TMA producer, MMA issuer, four warpgroups that share the query rows of every chunk
 // (taking the chunks in turn with all 64 rows each meant 64 scores and 64 sums in registers, a merge
 // at each unit's end, and 385 us for 40 rows instead of TCNEW).  Scores and weights have two
 // buffers, so the products of one chunk run under the weights of the next.  K and V are slots of
@@ -34,15 +34,16 @@
 namespace fa {
 
 struct Dec8TcCfg {
-  static constexpr int D = 128, kRows = 64, kThreads = 384;
-  static constexpr int kControlRegs = 56, kWorkRegs = 216;  // 128 x 56 + 256 x 216 <= 384 x 168
+  static constexpr int D = 128, kRows = 64;
+  static constexpr int kGroups = 4, kWork = 128 * kGroups, kThreads = 128 + kWork;  // warpgroups on the weights
+  static constexpr int kControlRegs = 40, kWorkRegs = 104;  // 128 x 40 + 512 x 104 <= 640 x 96
   static constexpr int kSlot = kDec8Keys * D;               // bytes of K (or V) of a chunk
   static constexpr int kSlots = 10, kPairs = kSlots / 2;
   static constexpr int kScales = 8;                         // chunks whose scales are kept (> kPairs)
   static constexpr int kP = kDec8Keys * 128;                // weights of a chunk: hi | lo of 64 rows
   static constexpr int kQ = kRows * D;                      // hi (and lo) of the query tile
   static constexpr int kColS = 0, kColO = 128, kTmemCols = 256;  // S: 2 x 64 columns; O: hi and lo of 64
-  static constexpr int kCols = 32;                               // query rows of a warpgroup
+  static constexpr int kCols = kRows / kGroups;                  // query rows of a warpgroup, at most
   static constexpr int kOffP = kSlots * kSlot, kOffQ = kOffP + 2 * kP, kOffMisc = kOffQ + 2 * kQ;
   static constexpr int kSmem = 1024 + kOffMisc + kScales * 64 + kRows * 8 + kRows * 4 + kRows * 16 + 4 * kRows * 4 +
                                64 * 8;
@@ -105,11 +106,11 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
       mbar_init(full + s, 1 + 8);  // the producer's expect_tx, and eight lanes' scales
       mbar_init(empty + s, 1);
     }
-    mbar_init(q_full, 256);
+    mbar_init(q_full, C::kWork);
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full + w, 1);
-      mbar_init(s_empty + w, 256);
-      mbar_init(p_full + w, 256);
+      mbar_init(s_empty + w, C::kWork);
+      mbar_init(p_full + w, C::kWork);
       mbar_init(p_done + w, 1);
     }
     mbar_init(all_done, 1);
@@ -246,8 +247,8 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kWorkRegs));
-    // -------------------------------------------------------------- weights (two warpgroups)
-    const int w = (warp >> 2) - 1, tid = threadIdx.x - 128;  // group 0 or 1; 0..255
+    // -------------------------------------------------------------- weights
+    const int w = (warp >> 2) - 1, tid = threadIdx.x - 128;  // group; thread among the groups'
     const int row = tid & 127, quarter = row >> 5;           // cache row of a chunk = TMEM lane
     const uint32_t lanes = (uint32_t)quarter << 21;
     float* const red = sm_red + w * 4 * C::kCols;
@@ -259,33 +260,34 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
       if (dec8_len(p, b) > 0) continue;
       const long long n = (long long)p.Nq * p.Hq;
-      for (long long k = tid; k < n * D / 8; k += 256)
+      for (long long k = tid; k < n * D / 8; k += C::kWork)
         reinterpret_cast<uint4*>(p.o)[(long long)b * (n * D / 8) + k] = make_uint4(0u, 0u, 0u, 0u);
       if (p.lse)
-        for (long long k = tid; k < n; k += 256) p.lse[b * n + k] = -INFINITY;
+        for (long long k = tid; k < n; k += C::kWork) p.lse[b * n + k] = -INFINITY;
       if (p.by_unit)
-        for (int k = tid; k < p.units; k += 256) p.ws_desc[b * p.units + k] = make_int4(0, 0, 0, 0);
+        for (int k = tid; k < p.units; k += C::kWork) p.ws_desc[b * p.units + k] = make_int4(0, 0, 0, 0);
     }
 
     while (walk.next(p, seg)) {
       const int kvh = seg.unit / p.tiles, tile = seg.unit - kvh * p.tiles;
-      // this group's query rows: columns [col0, col0 + 8 blocks) of the tile, half of them rounded up
-      const int rows = min(R, p.rows - tile * R), share8 = (rows + 15) >> 4;
-      const int col0 = w * share8 * 8, blocks = w ? ((rows + 7) >> 3) - share8 : share8;
+      // this group's query rows: columns [col0, col0 + 8 blocks) of the tile
+      const int rows = min(R, p.rows - tile * R), all8 = (rows + 7) >> 3;
+      const int col0 = w * all8 / C::kGroups * 8, blocks = (w + 1) * all8 / C::kGroups - w * all8 / C::kGroups;
       const float* const fac = sm_f + col0;
       float* const ref = sm_ref + col0;
       const int* const limit = sm_limit + col0;
       {
-        // the query tile: four threads a row, 32 elements each
-        const int r = tid >> 2, part = tid & 3, qr = tile * R + r;
+        // the query tile: a few threads a row
+        constexpr int kPer = C::kWork / R, kVecs = D / 8 / kPer;  // threads of a row; 16-byte vectors of one
+        const int r = tid / kPer, part = tid % kPer, qr = tile * R + r;
         const bool in = qr < p.rows;
         const int i = in ? qr / p.G : 0, h = kvh * p.G + (in ? qr - i * p.G : 0);
         const uint4* src =
-            reinterpret_cast<const uint4*>(p.q + (((long long)seg.b * p.Nq + i) * p.Hq + h) * D) + part * 4;
-        uint4 x[4];
+            reinterpret_cast<const uint4*>(p.q + (((long long)seg.b * p.Nq + i) * p.Hq + h) * D) + part * kVecs;
+        uint4 x[kVecs];
         uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kVecs; ++k) {
           x[k] = in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -293,45 +295,43 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
             top = max(top, max((v << 16) & 0x7FFF0000u, v & 0x7FFF0000u));
           }
         }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+        for (int off = 1; off < kPer; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
         const bool finite = top < 0x7F800000u;
         const int be = (top == 0u || !finite) ? 127 : max((int)(top >> 23), 1);
         // 2^(7 - e) in two factors, each a normal number
         const float d0 = __uint_as_float((uint32_t)(127 + (127 - be) / 2) << 23);
         const float d1 = __uint_as_float((uint32_t)(127 + 7 + (127 - be) - (127 - be) / 2) << 23);
-        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t v0 = (&x[k >> 1].x)[2 * (k & 1)], v1 = (&x[k >> 1].x)[2 * (k & 1) + 1];
-          const float a[4] = {__uint_as_float(v0 << 16) * d0 * d1, __uint_as_float(v0 & 0xFFFF0000u) * d0 * d1,
-                              __uint_as_float(v1 << 16) * d0 * d1, __uint_as_float(v1 & 0xFFFF0000u) * d0 * d1};
-          hi[k] = e4m3x4(a[0], a[1], a[2], a[3]);
-          uint32_t b0, b1;
-          e4m3x4_to_f16(hi[k], b0, b1);
-          const float2 f0 = __half22float2(*reinterpret_cast<__half2*>(&b0));
-          const float2 f1 = __half22float2(*reinterpret_cast<__half2*>(&b1));
-          lo[k] = e4m3x4(a[0] - f0.x, a[1] - f0.y, a[2] - f1.x, a[3] - f1.y);
-        }
+        for (int k = 0; k < kVecs; ++k) {
+          uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int at = r * D + (((part * 2 + u) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(sm_q + at) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-          *reinterpret_cast<uint4*>(sm_q + C::kQ + at) =
-              make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
+          for (int y = 0; y < 2; ++y) {
+            const uint32_t v0 = (&x[k].x)[2 * y], v1 = (&x[k].x)[2 * y + 1];
+            const float a[4] = {__uint_as_float(v0 << 16) * d0 * d1, __uint_as_float(v0 & 0xFFFF0000u) * d0 * d1,
+                                __uint_as_float(v1 << 16) * d0 * d1, __uint_as_float(v1 & 0xFFFF0000u) * d0 * d1};
+            hi[y] = e4m3x4(a[0], a[1], a[2], a[3]);
+            uint32_t b0, b1;
+            e4m3x4_to_f16(hi[y], b0, b1);
+            const float2 f0 = __half22float2(*reinterpret_cast<__half2*>(&b0));
+            const float2 f1 = __half22float2(*reinterpret_cast<__half2*>(&b1));
+            lo[y] = e4m3x4(a[0] - f0.x, a[1] - f0.y, a[2] - f1.x, a[3] - f1.y);
+          }
+          const int byte = (part * kVecs + k) * 8, at = r * D + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 8);
+          *reinterpret_cast<uint2*>(sm_q + at) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(sm_q + C::kQ + at) = make_uint2(lo[0], lo[1]);
         }
         if (part == 0) {
           // scores are q . k times 2^(e - 7); a row that is not finite makes everything of its own NaN
-          const float f = finite ? p.tau * 0.0078125f * __uint_as_float((uint32_t)be << 23) : __uint_as_float(0x7FC00000u);
-          sm_f[r] = f;
+          sm_f[r] = finite ? p.tau * 0.0078125f * __uint_as_float((uint32_t)be << 23) : __uint_as_float(0x7FC00000u);
           sm_ref[r] = 0.f;
           sm_limit[r] = in ? seg.len - p.Nq + 1 + i : seg.len;
         }
-        sm_nan[tid] = 0u;  // R * 4 words
+        if (tid < R * 4) sm_nan[tid] = 0u;
       }
       fence_proxy_async_smem();
       __syncwarp();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(C::kWork) : "memory");
       mbar_arrive(q_full);
 
       constexpr int N = C::kCols;
@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         mbar_arrive(s_empty + buf);
         // exponents t - reference, and whether one is past the top
         float most[N / 8];
+        bool past_top = false;
         const uint64_t sk2 = f2(sk, sk);
 #pragma unroll
         for (int b = 0; b < N / 8; ++b)
@@ -394,8 +395,9 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
           if (b < blocks)
 #pragma unroll
             for (int x = b * 8; x < b * 8 + 8; x += 2) most[b] = fmax3(most[b], s[x], s[x + 1]);
+          past_top |= most[b] + lsv > kTcTop;
         }
-        if (group_any(2 + w, fresh || fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) + lsv > kTcTop)) {
+        if (group_any(2 + w, fresh || past_top)) {
           // new references: the largest exponent of each row over the group's threads; a warp looks
           // at the blocks in which it has one past the top
 #pragma unroll
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
           __syncwarp();
           asm volatile("bar.sync %0, 128;" ::"r"(2 + w) : "memory");
         }
-        // V rows that some query does not see (this group's half of the columns): past the end they
+        // V rows that some query does not see (this group's part of the columns): past the end they
         // may hold anything, and a NaN code would reach every query; it goes to the queries that see
         // it by hand
         if (partly) {
@@ -467,8 +469,8 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
           uint32_t nan = 0;
           const bool past = j >= seg.len;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            uint4* const at = reinterpret_cast<uint4*>(v) + ((4 * w + u) ^ (row & 7));
+          for (int u = 0; u < 8 / C::kGroups; ++u) {
+            uint4* const at = reinterpret_cast<uint4*>(v) + ((8 / C::kGroups * w + u) ^ (row & 7));
             uint4 y = *at;
             if (past) y = make_uint4(0u, 0u, 0u, 0u);
             *at = y;
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
           // (rare, and taken by whole warps)
           if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0u)) {
 #pragma unroll 1
-            for (int d = 64 * w; d < 64 * w + 64; ++d) {
+            for (int d = D / C::kGroups * w; d < D / C::kGroups * (w + 1); ++d) {
               uint8_t* const at = v + (((d >> 4) ^ (row & 7)) << 4) + (d & 15);
               const bool bad = (*at & 0x7Fu) == 0x7Fu;
               if (bad) *at = 0;
@@ -535,22 +537,27 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
 #pragma unroll
       for (int r = 0; r < N; r += 2) f2_split(l2[r / 2], l[r], l[r + 1]);
       // l of a row over the 128 threads: half of the rows are exchanged between lanes 16 apart, half
-      // of the rest between lanes 8 apart, ..., so that lane x ends with the sum of row x
+      // of the rest between lanes 8 apart, ..., so that lane x ends with the sum of row x (N = 32),
+      // or two lanes with halves of it (N = 16)
 #pragma unroll
-      for (int off = 16, m = N; off > 0; off >>= 1, m >>= 1) {
+      for (int off = 16, m = N; off > 0; off >>= 1, m = m > 1 ? m >> 1 : 1) {
         const bool upper = (lane & off) != 0;
+        if (m == 1) {
+          l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
+        } else {
 #pragma unroll
-        for (int r = 0; r < N / 2; ++r)
-          if (r < m / 2) {
-            const float give = upper ? l[r] : l[r + m / 2], keep = upper ? l[r + m / 2] : l[r];
-            l[r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-          }
+          for (int r = 0; r < N / 2; ++r)
+            if (r < m / 2) {
+              const float give = upper ? l[r] : l[r + m / 2], keep = upper ? l[r + m / 2] : l[r];
+              l[r] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+            }
+        }
       }
-      red[quarter * N + lane] = l[0];
+      if (lane % (32 / N) == 0) red[quarter * N + lane / (32 / N)] = l[0];
       if (ok) ok = mbar_wait(p_done + ((n - 1) & 1u), ((n - 1) >> 1) & 1u);
       __syncwarp();
       tc_fence_after();
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(C::kWork) : "memory");
       const bool whole = seg.c0 == 0 && seg.c1 == seg.chunks;
       const long long part = 2ll * blockIdx.x + (seg.c0 == 0 ? 1 : 0);
 #pragma unroll
@@ -583,7 +590,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
       tc_fence_before();
       if (tid == 0) dec8_describe(p, seg, share, kvh, tile, whole);
       __syncwarp();
-      asm volatile("bar.sync 1, 256;" ::: "memory");  // the tables are free for the next unit
+      asm volatile("bar.sync 1, %0;" ::"n"(C::kWork) : "memory");  // the tables are free for the next unit
     }
   }
   tc_fence_before();
