@@ -1074,7 +1074,7 @@ fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
 // What a unit costs beside its chunks, in chunks (measured on ragged batches).
 constexpr int kDec8Lead = 4, kDec8TcLead = 10;
 // Query rows of a unit: one tensor-core tile of 16 where that holds them; else the kernel on tcgen05
-// products with 64 (d = 128: 40 rows in TCNEW us instead of 205 with 64 rows in registers), or
+// products with 64 (d = 128: 40 rows in 103 us instead of 211 with 64 rows in registers), or
 // registers for 32 or 64 (d = 64, where a cache row is too short for those products' 128 rows).
 int dec8_tile(int64_t rows, int d) { return rows <= 16 ? 16 : rows <= 32 && d == 64 ? 32 : 64; }
 // K/V heads of a unit, as a shift: one where the query rows fill more than a tile (the products,

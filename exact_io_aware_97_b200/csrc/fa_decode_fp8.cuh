@@ -6,14 +6,17 @@
 //   t_j = scale * sk_j * (q . k_j),  p_j = e^(t_j - m),  o = sum_j p_j sv_j v_j / sum_j p_j,
 // where k_j, v_j are the stored e4m3 values and sk_j, sv_j the scales of their blocks.
 //
-// Bound by HBM: 2 d bytes per cache row and K/V head are read once.  What decides whether the
-// stream is kept up is the work per byte, twice that of a bf16 cache.
+// Bound by HBM: 2 d bytes per cache row and K/V head are read once (DRAM reads 1.00 times that).
+// 8 sequences of 32K rows, 64 query and 8 K/V heads, d = 128: 98 to 105 us, 5.1 to 5.5 TB/s of the
+// 6.55 that a copy reaches; 6.65 TB/s between 32K and 64K rows, so what is left is the start (5 us to
+// the first rows), CTAs that end up to 7 us after the mean although their shares are equal, and the
+// merge (5 us).
 //
 // Partition.  The Nq * G query rows of one K/V head form tiles of R rows; a unit is (sequence,
 // group of K/V heads, tile) and is cut into chunks of cache rows.  A group is four heads (two, one)
 // where that divides Hkv and a tile has 16 rows: a chunk then reads 4 d bytes side by side from
-// each cache row instead of d (streaming alone, d = 128: KSTREAM1 us for one head at a time, KSTREAM4
-// for four).  All units' chunks, one after the
+// each cache row instead of d (8 sequences of 64K rows, 8 heads, d = 128, loads without products: 190
+// us one head at a time, 175 us four).  All units' chunks, one after the
 // other, are dealt to the CTAs of one wave in equal contiguous shares, whatever the lengths, so
 // every CTA streams the same number of bytes.  A CTA writes the output of units that lie in its
 // share whole; of at most two others (its first and its last) it writes partial sums, which
@@ -65,7 +68,8 @@ struct Dec8Cfg {
   static constexpr int kRows = 16 * MT * RG;       // R: query rows of a unit
   static constexpr int kWarps = 4 * RG;            // compute warps: 4 slices of 32 rows of the chunk x RG row groups
   // 16-row tiles of the cache that a warp takes at once: two where the registers allow it, for
-  // twice the independent chains (one at a time: 128 us instead of KTWO us on the 32K decode)
+  // twice the independent chains (one at a time, with two exponentials for each score: 128 us instead
+  // of 112 on the 32K decode)
   static constexpr int kTiles = MT == 1 ? 2 : 1;
   // A warp with two row tiles needs more registers than its share: the producer then is a warp of
   // a warpgroup of its own, which gives registers up (threads x registers of a CTA: MT = 2, RG = 1:

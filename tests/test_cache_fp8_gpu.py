@@ -117,13 +117,11 @@ def test_decode_fp8_scales_of_very_different_size(sb):
     dev = cache8.to_device(kc, ks, vc, vs, table, lens)
     ref = cache8.attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, lens, sb, 1.0)
     o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5], scale=1.0)
-    # weights below 2^-14 of the largest product lose bits; that product is at most max p * scale
     r_o, r_lse, o_abs, v_sum, t_abs = ref
     got = o.double().cpu().numpy()
     t = t_abs.transpose(0, 2, 1)[..., None]
     n = np.array(lens).reshape(2, 1, 1, 1)
-    # 2^-25 of the largest weight (<= o_abs_max / |code| >= 2^-9 ...): bounded by n * 2^-25 * 448 * w,
-    # where w <= sum of weights; o_abs carries that sum times the codes
+    # a weight below fp16's normal range is off by 2^-25 of the largest one, times a code of at most 448
     wsum = _weight_max(q.double().cpu().numpy(), kc, ks, vs, table, lens, sb)
     tol = 2.0 ** -8 * np.abs(r_o) + (2.0 ** -11 + 2.0 ** -17 * (1 + t)) * o_abs + n * 2.0 ** -25 * 448 * wsum
     assert np.all(np.abs(got - r_o) <= tol)
@@ -441,6 +439,50 @@ def test_decode_fp8_two_streams_at_once():
     got += [(i, out) for i, (_, out) in enumerate(graphs)]
     for i, (o, lse) in got:
         assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_c_functions_by_their_names():
+    """The C functions through the binding's functions of the same names give what the helpers give."""
+    rng = np.random.default_rng(5015)
+    old, new, H, d, ps, sb = [20, 0], [13, 40], 2, 64, 32, 16
+    kc, ks, vc, vs, table, lens, xs = _append_problem(rng, old, new, H, d, ps, sb)
+    cu, P, maxp = [0, 13, 53], kc.shape[0], table.shape[1]
+    want = _run_append(kc, ks, vc, vs, table, lens, cu, xs)
+    dev = cache8.to_device(kc, ks, vc, vs, table, lens)
+    fa.fa_cache_append_fp8(xs[0].cuda(), xs[1].cuda(), torch.tensor(cu, dtype=torch.int32, device="cuda"), dev[4], dev[5],
+                           dev[0], dev[2], dev[1], dev[3], 2, 53, H, P, ps, maxp, sb, d)
+    for a, b in zip(dev, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    q = torch.from_numpy(rng.standard_normal((2, 3, 4, d))).cuda().bfloat16()
+    o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5], scale=0.25)
+    o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
+    n = fa.fa_decode_paged_fp8_workspace_size(2, 3, 4, H, d)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    fa.fa_decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5], o2, lse2, 2, 3, 4, H, P, ps, maxp, sb, d,
+                           0.25, ws, n)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    freqs = fa.rope_frequencies(32)
+    y, _ = fa.rope(q, None, freqs)
+    y2 = torch.empty_like(y)
+    fa.fa_rope(q, None, y2, None, None, freqs, 6, 3, 4, 0, d, 32, False, 1.0, False, fa.FA_BF16, 4 * d, 0, 4 * d, 0)
+    assert torch.equal(y, y2)
+    parent = torch.tensor([1, 1, 0], dtype=torch.int32, device="cuda")
+    pools = [dev[0], dev[1], dev[2], dev[3]]
+    room = [torch.cat([t, t[:2]]) for t in pools]  # two free pages more
+    got = fa.pages_fork(room, dev[4], dev[5], parent, ps)
+    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    t2, l2, f2, c2 = i32(3, maxp), i32(3), i32(P + 2), i32(1)
+    n = fa.fa_pages_workspace_size(P + 2, 3)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    raw = [(t.data_ptr(), t.nbytes // (P + 2)) for t in room]
+    fa.fa_pages_fork(raw, dev[4], dev[5], parent, t2, l2, f2, c2, 2, 3, P + 2, ps, maxp, ws, n)
+    for a, b in zip(got, (t2, l2, f2, c2)):
+        assert torch.equal(a, b)
+    t3, n3 = fa.pages_compact(room, t2, l2, ps)
+    t4, n4 = i32(3, maxp), i32(1)
+    fa.fa_pages_compact(room, t2, l2, t4, n4, 3, P + 2, ps, maxp, ws, n)
+    assert torch.equal(t3, t4) and torch.equal(n3, n4)
+    assert fa.fa_last_device_error() == fa.FA_OK
 
 
 def test_prefill_then_decode_through_the_cache():
