@@ -7,6 +7,7 @@ fallback.  If libfa.so is missing this module raises on first use.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional
@@ -327,23 +328,30 @@ def fa_decode_paged_fp8_workspace_size(B, Nq, Hq, Hkv, d) -> int:
 
 
 def _pool_array(pools, num_pages):
-    """fa_pool array of tensors [num_pages, ...]; raw (address, page_bytes) pairs pass through."""
-    flat = []
+    """fa_pool array (address and page_bytes in turn) of tensors [num_pages, ...]; raw pairs pass
+    through.  The caller keeps it for the call."""
+    flat = array.array("Q")
     for n, t in enumerate(pools):
         if isinstance(t, tuple):
-            flat += t
+            flat.extend(t)
             continue
         if t.dim() < 1 or t.shape[0] != num_pages:
             raise ValueError(f"pool {n}: expected [{num_pages}, ...], got shape {tuple(t.shape)}")
         if not t.is_cuda or not t.is_contiguous():
             _ptr(t)  # says what is wrong
-        flat += (t.data_ptr(), t.nbytes // num_pages)
-    return (ctypes.c_uint64 * len(flat))(*flat) if flat else None
+        flat.append(t.data_ptr())
+        flat.append(t.nbytes // num_pages)
+    return flat
+
+
+def _pool_ptr(flat) -> Optional[int]:
+    return flat.buffer_info()[0] if flat else None
 
 
 def fa_pages_fork(pools, block_table, seqlens, parent, block_table_out, seqlens_out, free_pages, n_free, B, B_out,
                   num_pages, page_size, max_pages_per_seq, workspace, workspace_bytes, stream=None) -> None:
-    st = load().fa_pages_fork(_pool_array(pools, int(num_pages)), len(pools), _ptr_i32(block_table, "block_table"), _ptr_i32(seqlens, "seqlens"),
+    arr = _pool_array(pools, int(num_pages))
+    st = load().fa_pages_fork(_pool_ptr(arr), len(pools), _ptr_i32(block_table, "block_table"), _ptr_i32(seqlens, "seqlens"),
                               _ptr_i32(parent, "parent"), _ptr_i32(block_table_out, "block_table_out"),
                               _ptr_i32(seqlens_out, "seqlens_out"), _ptr_i32(free_pages, "free_pages"),
                               _ptr_i32(n_free, "n_free"), int(B), int(B_out), int(num_pages), int(page_size),
@@ -353,7 +361,8 @@ def fa_pages_fork(pools, block_table, seqlens, parent, block_table_out, seqlens_
 
 def fa_pages_compact(pools, block_table, seqlens, block_table_out, n_live, B, num_pages, page_size,
                      max_pages_per_seq, workspace, workspace_bytes, stream=None) -> None:
-    st = load().fa_pages_compact(_pool_array(pools, int(num_pages)), len(pools), _ptr_i32(block_table, "block_table"),
+    arr = _pool_array(pools, int(num_pages))
+    st = load().fa_pages_compact(_pool_ptr(arr), len(pools), _ptr_i32(block_table, "block_table"),
                                  _ptr_i32(seqlens, "seqlens"), _ptr_i32(block_table_out, "block_table_out"),
                                  _ptr_i32(n_live, "n_live"), int(B), int(num_pages), int(page_size),
                                  int(max_pages_per_seq), _ptr(workspace), int(workspace_bytes), _stream(stream))
@@ -867,7 +876,7 @@ def pages_fork(pools, block_table, seqlens, parent, page_size, num_pages=None, w
         workspace = block_table.new_empty(max(nbytes, 1), dtype=torch.uint8)
     else:
         nbytes = workspace.numel() * workspace.element_size()
-    _check(lib.fa_pages_fork(arr, len(pools), block_table.data_ptr(), seqlens.data_ptr(), parent.data_ptr(),
+    _check(lib.fa_pages_fork(_pool_ptr(arr), len(pools), block_table.data_ptr(), seqlens.data_ptr(), parent.data_ptr(),
                              table.data_ptr(), lens.data_ptr(), free.data_ptr(), n_free.data_ptr(), B, R, num_pages,
                              page_size, maxp, workspace.data_ptr(), nbytes, _stream(stream)), "fa_pages_fork")
     return table.view(R, maxp), lens, free, n_free
@@ -890,7 +899,7 @@ def pages_compact(pools, block_table, seqlens, page_size, num_pages=None, worksp
         workspace = block_table.new_empty(max(nbytes, 1), dtype=torch.uint8)
     else:
         nbytes = workspace.numel() * workspace.element_size()
-    _check(lib.fa_pages_compact(arr, len(pools), block_table.data_ptr(), seqlens.data_ptr(), table.data_ptr(),
+    _check(lib.fa_pages_compact(_pool_ptr(arr), len(pools), block_table.data_ptr(), seqlens.data_ptr(), table.data_ptr(),
                                 n_live.data_ptr(), B, num_pages, page_size, maxp, workspace.data_ptr(), nbytes,
                                 _stream(stream)), "fa_pages_compact")
     return table, n_live
