@@ -1057,7 +1057,8 @@ fa_status check_cache8(const void* k_pages, const void* v_pages, const float* k_
     return FA_ERR_UNSUPPORTED;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if ((int64_t)num_pages * page_size >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
-  if ((int64_t)max_pages * page_size >= (int64_t(1) << 31)) return FA_ERR_UNSUPPORTED;
+  // (room for positions rounded up to a chunk)
+  if ((int64_t)max_pages * page_size > (int64_t(1) << 31) - 1024) return FA_ERR_UNSUPPORTED;
   if (B > 65535 || Hkv > 65535) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }

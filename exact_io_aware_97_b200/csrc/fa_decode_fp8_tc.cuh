@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
           if (bad) sv = 0.f;
           __syncwarp();
         }
-        const float lsv = fmaxf(__log2f(sv), -60.f);  // (a zero scale weighs nothing)
+        // (a zero scale weighs nothing; the bound keeps p = 2^(t - reference) finite)
+        const float lsv = fmaxf(__log2f(sv), -100.f);
         float s[N];
 #pragma unroll
         for (int b = 0; b < N / 8; ++b)

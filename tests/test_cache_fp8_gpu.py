@@ -77,6 +77,12 @@ CASES = [
     ([400, 70], 9, 12, 4, 128, 64, 64),
     ([150, 40], 40, 4, 2, 64, 64, 16),
     ([3000, 10], 2, 8, 1, 128, 16, 16),
+    ([200, 70], 20, 8, 2, 128, 32, 16),         # 80 query rows of a head: two tiles, the second part full
+    ([33, 1000], 1, 17, 1, 128, 16, 16),
+    ([129, 257], 16, 8, 2, 128, 64, 64),        # 64 rows: a full tile
+    ([100] * 90, 3, 12, 2, 128, 16, 16),        # more short units than CTAs
+    ([40, 0, 3] * 40, 1, 8, 4, 128, 16, 16),
+    ([520] * 30, 1, 6, 6, 64, 16, 16),
 ]
 
 
@@ -100,8 +106,9 @@ def test_decode_fp8_matches_64_bits(case):
     assert torch.equal(o2.view_as(o), o) and torch.equal(lse2.view_as(lse), lse)
 
 
+@pytest.mark.parametrize("Hq", [8, 48], ids=["4rows", "24rows"])
 @pytest.mark.parametrize("sb", [16, 64])
-def test_decode_fp8_scales_of_very_different_size(sb):
+def test_decode_fp8_scales_of_very_different_size(sb, Hq):
     """V scales from 2^-40 to 2^30 and K scales that swamp some blocks: weights are taken relative
     to the largest product of probability and scale, so the small blocks keep their bits."""
     rng = np.random.default_rng(5002)
@@ -113,20 +120,42 @@ def test_decode_fp8_scales_of_very_different_size(sb):
     for b in range(2):
         vs[table[b, 0], :, 0] = 2.0 ** 30
         ks[table[b, 0], :, 0] = 0.0
-    q = torch.from_numpy(rng.standard_normal((2, 1, 8, d)) * 4).cuda().bfloat16()
+    q = torch.from_numpy(rng.standard_normal((2, 1, Hq, d)) * 4).cuda().bfloat16()
     dev = cache8.to_device(kc, ks, vc, vs, table, lens)
     ref = cache8.attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, lens, sb, 1.0)
     o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5], scale=1.0)
     r_o, r_lse, o_abs, v_sum, t_abs = ref
     got = o.double().cpu().numpy()
-    t = t_abs.transpose(0, 2, 1)[..., None]
     n = np.array(lens).reshape(2, 1, 1, 1)
-    # a weight below fp16's normal range is off by 2^-25 of the largest one, times a code of at most 448
-    wsum = _weight_max(q.double().cpu().numpy(), kc, ks, vs, table, lens, sb)
-    tol = 2.0 ** -8 * np.abs(r_o) + (2.0 ** -11 + 2.0 ** -17 * (1 + t)) * o_abs + n * 2.0 ** -25 * 448 * wsum
+    # a small weight is off by 2^-25 of the largest one (fp16) or 2^-16 (two e4m3 terms), times a code
+    # of at most 448
+    weight, small = (2.0 ** -11, 2.0 ** -25) if Hq // H <= 16 else (2.0 ** -8, 2.0 ** -16)
+    q64 = q.double().cpu().numpy()
+    u = 0.0 if Hq // H <= 16 else _score_bound(q64, (kc, ks, vc, vs, table, lens, sb, 1.0))
+    wsum = _weight_max(q64, kc, ks, vs, table, lens, sb)
+    tt = (t_abs + u).transpose(0, 2, 1)[..., None]
+    tol = 2.0 ** -8 * np.abs(r_o) + (weight + 2.0 ** -17 * (1 + tt)) * o_abs + n * small * 448 * wsum
     assert np.all(np.abs(got - r_o) <= tol)
-    check_lse = np.abs(lse.double().cpu().numpy() - r_lse)
-    assert np.all(check_lse <= 2.0 ** -17 * (1 + t_abs))
+    assert np.all(np.abs(lse.double().cpu().numpy() - r_lse) <= 2.0 ** -17 * (1 + t_abs + u))
+
+
+@pytest.mark.parametrize("Hq", [4, 40], ids=["4rows", "40rows"])
+@pytest.mark.parametrize("way", ["up", "down", "steps"])
+def test_decode_fp8_scores_that_rise_and_fall(way, Hq):
+    """K scales that double every few blocks: running maxima move in most chunks, or never again."""
+    rng = np.random.default_rng(5016)
+    lens, H, d, ps, sb = [1500, 700], 1, 128, 32, 16
+    kc, ks, vc, vs, table = cache8.build(rng, lens, ps, sb, H, d, spread=0.5)
+    for b, n in enumerate(lens):
+        j = np.arange(n // sb + (n % sb > 0)) * sb
+        at = np.linspace(0, 1, len(j))
+        grow = {"up": 9 * at, "down": 9 * at[::-1], "steps": np.round(6 * np.sin(20 * at))}[way]
+        ks[table[b, j // ps], :, j % ps // sb] *= np.exp2(np.round(grow))[:, None]
+    q = torch.from_numpy(rng.standard_normal((2, 1, Hq, d))).cuda().bfloat16()
+    dev = cache8.to_device(kc, ks, vc, vs, table, lens)
+    ref = cache8.attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, lens, sb, 1 / math.sqrt(d))
+    o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5])
+    check(o, lse, ref, q, (kc, ks, vc, vs, table, lens, sb, 1 / math.sqrt(d)))
 
 
 def _weight_max(q, kc, ks, vs, table, lens, sb):
