@@ -394,6 +394,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
           if (++slot == NS) slot = 0, phase ^= 1u;
         }
       }
+      if (!ok)  // a wait ran out: leave no copy in flight (the last fill of each slot)
+        for (int s = 0; s < NS; ++s) (void)mbar_wait(full + s, s < slot ? phase ^ 1u : phase);
       // the merge may be launched once every CTA has its last loads under way
       if (lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     }
@@ -498,10 +500,12 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
     }
 
     for (int c = seg.c0; c < seg.c1; ++c) {
-      if (ok && !mbar_wait(full + slot, phase)) ok = false;
+      // (after a wait that ran out, recorded, the products go on: whole warps over whatever is there)
+      if (ok) ok = mbar_wait(full + slot, phase);
+      __syncwarp();
       uint8_t* const st = ring + slot * C::kStage;
       const int jw = c * chunk + 32 * slice;
-      if (ok && !idle && jw < seg.len) {
+      if (!idle && jw < seg.len) {
 #pragma unroll
         for (int t0 = 0; t0 < 2; t0 += KT) {
           const int j0 = jw + 16 * t0;

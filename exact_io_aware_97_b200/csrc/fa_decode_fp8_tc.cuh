@@ -184,6 +184,8 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
             entry = (entry + 1) % C::kScales;
           }
         }
+        if (!ok)  // a wait ran out: leave no copy in flight (the last fill of each slot)
+          for (int s = 0; s < C::kSlots; ++s) (void)mbar_wait(full + s, s >> 1 < pair ? phase ^ 1u : phase);
         if (lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
       }
     } else if (warp == 1) {
@@ -384,8 +386,8 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
 #pragma unroll
             for (int x = b * 8; x < b * 8 + 8; x += 4) {
               const float4 f = *reinterpret_cast<const float4*>(fac + x), m = *reinterpret_cast<const float4*>(ref + x);
-              f2_split(f2_fma(f2_mul(f2(s[x], s[x + 1]), sk2), f2(f.x, f.y), f2(m.x, m.y)), s[x], s[x + 1]);
-              f2_split(f2_fma(f2_mul(f2(s[x + 2], s[x + 3]), sk2), f2(f.z, f.w), f2(m.z, m.w)), s[x + 2], s[x + 3]);
+              f2_split(f2_fma(f2(s[x], s[x + 1]), f2_mul(f2(f.x, f.y), sk2), f2(m.x, m.y)), s[x], s[x + 1]);
+              f2_split(f2_fma(f2(s[x + 2], s[x + 3]), f2_mul(f2(f.z, f.w), sk2), f2(m.z, m.w)), s[x + 2], s[x + 3]);
             }
           }
         if (partly) {

@@ -418,13 +418,18 @@ __global__ void __launch_bounds__(kCopyThreads + 32, 2)
 #pragma unroll
   for (int s = 0; s < kBulkStages - 1; ++s) load(s);
   bool ok = true;
+  int late = 0;  // parities of the slots' last fills, once a wait ran out
   for (uint32_t phase = 0; ok; phase ^= 1u) {
 #pragma unroll
     for (int s = 0; s < kBulkStages; ++s) {
       if (ok) {
         bulk_wait_group_read0();
         load((s + kBulkStages - 1) % kBulkStages);
-        ok = bytes[s] != 0 && mbar_wait(full + s, phase);
+        ok = bytes[s] != 0;
+        if (ok && !mbar_wait(full + s, phase)) {
+          ok = false;
+          late = 1 << kBulkStages | (phase ? (1 << kBulkStages) - (1 << s) : (1 << s) - 1);
+        }
       }
       if (ok) {
         bulk_store(to[s], smem_raw + s * kBulkBytes, bytes[s]);
@@ -432,6 +437,10 @@ __global__ void __launch_bounds__(kCopyThreads + 32, 2)
       }
     }
   }
+  if (late)  // leave no copy in flight
+#pragma unroll
+    for (int s = 0; s < kBulkStages; ++s)
+      if (bytes[s] != 0) (void)mbar_wait(full + s, late >> s & 1);
   bulk_wait_group0();
 }
 

@@ -318,22 +318,21 @@ FA_EXPORT fa_status fa_cache_append_fp8(const void* k, const void* v, const int3
  * q [B, Nq, Hq, d] bf16: the Nq newest tokens of each sequence, whose K and V rows are in the
  * cache already; o likewise; lse [B, Hq, Nq] fp32 (may be NULL).  Query i of sequence b sees
  * cache rows j <= seqlens[b] - Nq + i (every row for Nq = 1); a query that sees no row gets o = 0
- * and lse = -inf.  Cache, scales, block_table and seqlens as in fa_cache_append_fp8 (scales
- * finite or NaN, none negative); lengths below 0 count as 0, larger ones than max_pages_per_seq * page_size
- * as that.  Rows past a sequence's end may hold anything; a NaN code or scale makes NaN of what
+ * and lse = -inf.  Cache, scales, block_table and seqlens as in fa_cache_append_fp8
+ * (scales 0 .. 2^120 or NaN; the append writes no larger ones for finite rows); lengths below 0
+ * count as 0, larger ones than max_pages_per_seq * page_size as that.  Rows past a sequence's end may hold anything; a NaN code or scale makes NaN of what
  * attends to it, and of nothing else.  An entry of the table outside [0, num_pages) is
  * read as page 0 and recorded (FA_ERR_INVALID_ARG from fa_last_device_error).
  * The stored values are exact in the products and all sums are fp32.  P times the V scale is
  * rounded to fp16 relative to its largest value so far; for more than 16 query rows of a K/V head
- * (Nq * Hq / Hkv) and d = 128 it is the sum of two e4m3 terms instead (8 bits, like bf16; 2^-16 of the
- * largest value at the least), and so is q (2^-17 of a row's largest element at the least); V scales
- * outside 2^-100 .. 2^100 lose accuracy there.  o is rounded to bf16.
+ * (Nq * Hq / Hkv) and d = 128 it is the sum of two e4m3 terms instead (8 bits, like bf16; 2^-16 of
+ * the largest value at the least), and so is q (2^-17 of a row's largest element at the least);
+ * V scales outside 2^-100 .. 2^100 lose accuracy there.  o is rounded to bf16.
  * Hq a multiple of Hkv; d 64 or 128; sizes as in fa_cache_append_fp8, and B * Hkv *
  * max_pages_per_seq * page_size * (Nq * (Hq / Hkv) / 64, rounded up) < 2^37 (FA_ERR_UNSUPPORTED
- * beyond).  workspace: at least
- * fa_decode_paged_fp8_workspace_size(...) bytes (with the call's device current), 16-byte
- * aligned, not initialised; calls that share one must not overlap on the GPU.  o and lse must not
- * overlap the inputs. */
+ * beyond).  workspace: at least fa_decode_paged_fp8_workspace_size(...) bytes (with the call's
+ * device current), 16-byte aligned, not initialised; calls that share one must not overlap on the
+ * GPU.  o and lse must not overlap the inputs. */
 FA_EXPORT fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
                                         const float* k_scale, const float* v_scale, const int32_t* block_table,
                                         const int32_t* seqlens, void* o, float* lse, int B, int Nq, int Hq, int Hkv,
@@ -361,8 +360,9 @@ typedef struct {
  * that the copies took (the lowest ones, in the order of the new sequences), then -1;
  * n_free [1] their number.  Entries of a row past the sequence's pages become -1.
  * Pages are copied in every pool of `pools` (a HOST array of n_pools; any element types; 0 pools:
- * tables only; at most 4096; pages under 2^31 bytes).  block_table [B, max_pages_per_seq], block_table_out [B_out, max_pages_per_seq],
- * all device int32; outputs must not overlap inputs.  page_size is a power of two.
+ * tables only; at most 4096; pages under 2^31 bytes).  block_table [B, max_pages_per_seq] and
+ * block_table_out [B_out, max_pages_per_seq], all device int32; outputs must not overlap inputs.
+ * page_size is a power of two.
  * Recorded for fa_last_device_error (FA_ERR_INVALID_ARG): a parent outside [-1, B) (taken as
  * -1), a length that is negative or past the table (taken as 0), an entry outside [0, num_pages)
  * (passed on, never copied), and too few free pages (those new sequences become empty).

@@ -158,6 +158,26 @@ def test_decode_fp8_scores_that_rise_and_fall(way, Hq):
     check(o, lse, ref, q, (kc, ks, vc, vs, table, lens, sb, 1 / math.sqrt(d)))
 
 
+@pytest.mark.parametrize("Hq", [4, 40], ids=["4rows", "40rows"])
+@pytest.mark.parametrize("e", [-100, 100])
+def test_decode_fp8_scales_that_queries_undo(e, Hq):
+    """K scales times 2^e and queries times 2^-e change no bit (powers of two round nothing); V scales
+    times 2^(e / 2) scale o, the references t + log2(scale) being rounded at 64 at most (2^-18)."""
+    rng = np.random.default_rng(5017)
+    lens, H, d, ps, sb = [300, 41], 1, 128, 32, 16
+    kc, ks, vc, vs, table = cache8.build(rng, lens, ps, sb, H, d, spread=0.5)
+    q = torch.from_numpy(rng.standard_normal((2, 1, Hq, d))).cuda().bfloat16()
+    dkc, dks, dvc, dvs, dt, dl = cache8.to_device(kc, ks, vc, vs, table, lens)
+    o, lse = fa.decode_paged_fp8(q, dkc, dvc, dks, dvs, dt, dl)
+    q2 = (q.float() * 2.0 ** -e).bfloat16()
+    o2, lse2 = fa.decode_paged_fp8(q2, dkc, dvc, dks * 2.0 ** e, dvs, dt, dl)
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    vs = vs * 2.0 ** (e // 2)
+    o2, lse2 = fa.decode_paged_fp8(q, dkc, dvc, dks, dvs * 2.0 ** (e // 2), dt, dl)
+    ref = cache8.attend(q.double().cpu().numpy(), kc, ks, vc, vs, table, lens, sb, 1 / math.sqrt(d))
+    check(o2, lse2, ref, q, (kc, ks, vc, vs, table, lens, sb, 1 / math.sqrt(d)))
+
+
 def _weight_max(q, kc, ks, vs, table, lens, sb):
     """Largest p_j * scale_j / sum p of each query, [B, 1, Hq, 1]."""
     B, _, Hq, _ = q.shape
