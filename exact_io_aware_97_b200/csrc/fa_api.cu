@@ -1075,7 +1075,7 @@ fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
 // What a unit costs beside its chunks, in chunks (measured on ragged batches).
 constexpr int kDec8Lead = 4, kDec8TcLead = 10;
 // Query rows of a unit: one tensor-core tile of 16 where that holds them; else the kernel on tcgen05
-// products with 64 (d = 128: 40 rows in 103 us instead of 211 with 64 rows in registers), or
+// products with 64 (d = 128: 40 rows in 101 us instead of 211 with 64 rows in registers), or
 // registers for 32 or 64 (d = 64, where a cache row is too short for those products' 128 rows).
 int dec8_tile(int64_t rows, int d) { return rows <= 16 ? 16 : rows <= 32 && d == 64 ? 32 : 64; }
 // K/V heads of a unit, as a shift: one where the query rows fill more than a tile (the products,
@@ -1313,7 +1313,8 @@ fa_status launch_copies(const fa_pool* pools, int n_pools, const int32_t* src, c
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, pages_copy_kernel, list, src, dst, count, tickets++) != cudaSuccess) return FA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, pages_copy_kernel, list, src, dst, count, tickets++) != cudaSuccess)
+      return FA_ERR_CUDA;
   }
   return FA_OK;
 }

@@ -10,9 +10,9 @@
 // of its block NaN.
 //
 // Bound by HBM for prompts (2 bytes read and 1 written per element; 67.6K rows of 8 heads, d = 128: 80
-// us, 5.6 TB/s of the copy's 6.55) and by the chain of dependent loads (lengths, block table, scale, rows) for single tokens.  A unit is one
-// (block, head): its warps hold the rows of K and V in registers, so a row is read once for the
-// maximum and the rounding alike.
+// us, 5.6 TB/s of the copy's 6.55) and by the chain of dependent loads (lengths, block table, scale,
+// rows) for single tokens.  A unit is one (block, head): its warps hold the rows of K and V in
+// registers, so a row is read once for the maximum and the rounding alike.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -103,7 +103,8 @@ struct AppendUnit {
 // One warp's rows of K and of V.  INSIDE: every row of the block is new.  The rows are loaded
 // before the page (a load of its own, under way) and the scale are looked at.
 template <int D, bool INSIDE>
-__device__ __forceinline__ void append_rows(const AppendParams& p, const AppendUnit& t, uint32_t (&sm_max)[2][kAppendCta]) {
+__device__ __forceinline__ void append_rows(const AppendParams& p, const AppendUnit& t,
+                                            uint32_t (&sm_max)[2][kAppendCta]) {
   constexpr int kLanes = D / 8;       // lanes of one row (8 values each)
   constexpr int kRows = 32 / kLanes;  // rows of one pass of a warp
   constexpr int kPass = kAppendRows<D> / kRows;

@@ -7,7 +7,7 @@
 // where k_j, v_j are the stored e4m3 values and sk_j, sv_j the scales of their blocks.
 //
 // Bound by HBM: 2 d bytes per cache row and K/V head are read once (DRAM reads 1.00 times that).
-// 8 sequences of 32K rows, 64 query and 8 K/V heads, d = 128: 98 to 105 us, 5.1 to 5.5 TB/s of the
+// 8 sequences of 32K rows, 64 query and 8 K/V heads, d = 128: 100 to 105 us, 5.1 to 5.4 TB/s of the
 // 6.55 that a copy reaches; 6.65 TB/s between 32K and 64K rows, so what is left is the start (5 us to
 // the first rows), CTAs that end up to 7 us after the mean although their shares are equal, and the
 // merge (5 us).
@@ -717,52 +717,52 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
               m_r[0][hr], l);
       }
     } else {
-    float* const mg = reinterpret_cast<float*>(ring + slot * C::kStage);
-    float2* const ml = sm_ml + rg * 64;
+      float* const mg = reinterpret_cast<float*>(ring + slot * C::kStage);
+      float2* const ml = sm_ml + rg * 64;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int turn = 0; turn < RG; ++turn) {  // the slot holds one row group's sums
-        asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
-        if (turn == rg) {
+        for (int turn = 0; turn < RG; ++turn) {  // the slot holds one row group's sums
+          asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
+          if (turn == rg) {
 #pragma unroll
-          for (int hr = 0; hr < 2; ++hr) {
-            float l = l_r[mt][hr];
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            // weights so far are relative to 2^w_r: relative to 2^m from here on
-            const float e = ex2_approx(w_r[mt][hr] - m_r[mt][hr]);
-            if (tig == 0) ml[w4 * 16 + g + 8 * hr] = make_float2(m_r[mt][hr], l);
-            float* to = mg + (w4 * 16 + g + 8 * hr) * D + 4 * tig;
+            for (int hr = 0; hr < 2; ++hr) {
+              float l = l_r[mt][hr];
+              l += __shfl_xor_sync(0xffffffffu, l, 1);
+              l += __shfl_xor_sync(0xffffffffu, l, 2);
+              // weights so far are relative to 2^w_r: relative to 2^m from here on
+              const float e = ex2_approx(w_r[mt][hr] - m_r[mt][hr]);
+              if (tig == 0) ml[w4 * 16 + g + 8 * hr] = make_float2(m_r[mt][hr], l);
+              float* to = mg + (w4 * 16 + g + 8 * hr) * D + 4 * tig;
 #pragma unroll
-            for (int k = 0; k < KS; ++k)
-              *reinterpret_cast<float4*>(to + 16 * k) =
-                  make_float4(acc[mt][2 * k][2 * hr] * e, acc[mt][2 * k + 1][2 * hr] * e,
-                              acc[mt][2 * k][2 * hr + 1] * e, acc[mt][2 * k + 1][2 * hr + 1] * e);
+              for (int k = 0; k < KS; ++k)
+                *reinterpret_cast<float4*>(to + 16 * k) =
+                    make_float4(acc[mt][2 * k][2 * hr] * e, acc[mt][2 * k + 1][2 * hr] * e,
+                                acc[mt][2 * k][2 * hr + 1] * e, acc[mt][2 * k + 1][2 * hr + 1] * e);
+            }
+          }
+          asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
+          const int row_at = tile * R + (turn * MT + mt) * 16;  // of the rows now in the slot
+          for (int idx = threadIdx.x; idx < (16 << p.hs) * (D / 4); idx += C::kWarps * 32) {
+            const int hd = idx / (16 * (D / 4)), r = idx / (D / 4) & 15, col = 4 * (idx % (D / 4));
+            const int row = row_at + r, w0 = hd << (2 - p.hs), w1 = (hd + 1) << (2 - p.hs);
+            if (row >= p.rows) continue;
+            const float2* from = sm_ml + turn * 64 + r;
+            float M = kDec8Low, L = 0.f;
+            for (int w = w0; w < w1; ++w) M = fmaxf(M, from[w * 16].x);
+            float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = w0; w < w1; ++w) {
+              const float e = ex2_approx(from[w * 16].x - M);
+              L += e * from[w * 16].y;
+              const float4 x = *reinterpret_cast<const float4*>(mg + (w * 16 + r) * D + col);
+              A.x += e * x.x;
+              A.y += e * x.y;
+              A.z += e * x.z;
+              A.w += e * x.w;
+            }
+            put((group << p.hs) + hd, row, col, A, M, L);
           }
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
-        const int row_at = tile * R + (turn * MT + mt) * 16;  // of the rows now in the slot
-        for (int idx = threadIdx.x; idx < (16 << p.hs) * (D / 4); idx += C::kWarps * 32) {
-          const int hd = idx / (16 * (D / 4)), r = idx / (D / 4) & 15, col = 4 * (idx % (D / 4));
-          const int row = row_at + r, w0 = hd << (2 - p.hs), w1 = (hd + 1) << (2 - p.hs);
-          if (row >= p.rows) continue;
-          const float2* from = sm_ml + turn * 64 + r;
-          float M = kDec8Low, L = 0.f;
-          for (int w = w0; w < w1; ++w) M = fmaxf(M, from[w * 16].x);
-          float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int w = w0; w < w1; ++w) {
-            const float e = ex2_approx(from[w * 16].x - M);
-            L += e * from[w * 16].y;
-            const float4 x = *reinterpret_cast<const float4*>(mg + (w * 16 + r) * D + col);
-            A.x += e * x.x;
-            A.y += e * x.y;
-            A.z += e * x.z;
-            A.w += e * x.w;
-          }
-          put((group << p.hs) + hd, row, col, A, M, L);
-        }
-      }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();

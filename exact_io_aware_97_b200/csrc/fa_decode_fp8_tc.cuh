@@ -14,22 +14,25 @@
 // 0..63 and 64..127 of one product).  The largest w of a row is 2^2 when its reference is set and may
 // grow to 2^8.5; only a score that goes beyond raises the reference and rescales the sums, of its
 // block of eight rows.  (From 2^4: 124 us for 40 rows instead of 113, o off by 1.67e-3 of its norm
-// where a bf16 rounding alone gives 1.65e-3; from 2^2: 1.73e-3; from 2^-2: 109 us, 2.55e-3.)  l sums p in fp32.  Both p and w are
-// relative to the one reference, which follows t + log2(sv).
+// where a bf16 rounding alone gives 1.65e-3; from 2^2: 1.73e-3; from 2^-2: 109 us, 2.55e-3.)  l sums
+// p in fp32.  Both p and w are relative to the one reference, which follows t + log2(sv).
 //
 // Warps stay together: whatever lanes do alone ends in a __syncwarp before the next barrier or TMEM
 // access, which are for whole warps.
 //
 // One CTA per SM: TMA producer, MMA issuer, four warpgroups that share the query rows of every chunk
 // (two that take the chunks in turn, with 64 scores and 64 sums in registers and a merge at each
-// unit's end: 385 us for 40 rows; two that share the rows: 113 us; four: 103 us).  Scores and weights have two
-// buffers, so the products of one chunk run under the weights of the next.  K and V are slots of
-// their own in the ring, since a K slot is free as soon as its product is done.
+// unit's end: 385 us for 40 rows; two that share the rows: 113 us; four in two pairs that take the
+// chunks in turn: 118 us; four: 101 us).  Scores and weights have two buffers, so the products of one
+// chunk run under the weights of the next, and the scores of the chunk after that are issued before
+// this one's sums (2 % faster than after).  K and V are slots of their own in the ring, since a K
+// slot is free as soon as its product is done.
 //
-// Bound by the weights: per chunk each warp spends about 220 instructions that do not depend on its
-// rows (waits, scales, a vote, loads) and 14 a row, at 55 % of the issue slots; the products take 20 %
-// of the tensor pipe.  8 sequences of up to 32K rows, 5 new tokens, 64 query and 8 K/V heads (40 rows):
-// 103 us for 311 MB, 3.0 TB/s, where 64 rows take 118 us and the registers' kernel took 211 us.
+// Bound by the weights: per chunk each warp spends about 180 instructions that do not depend on its
+// rows (waits, scales, a vote, loads) and 14 a row, at 54 % of the issue slots; the products take 19 %
+// of the tensor pipe, and the vote on new references 9 % of the time.  8 sequences of up to 32K rows,
+// 5 new tokens, 64 query and 8 K/V heads (40 rows): 101 us for 311 MB, 3.1 TB/s, where the kernel of
+// products in registers took 211 us.
 #pragma once
 
 #include "fa_decode_fp8.cuh"
@@ -242,8 +245,9 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         ok = warp_wait(q_full, qphase);
         qphase ^= 1u;
         if (ok) product_s();
+        if (ok && n > 1) product_s();
         for (int k = 0; k < n && ok; ++k) {
-          if (k + 1 < n) product_s();
+          if (k + 2 < n) product_s();
           product_o(k == 0);
         }
       }
@@ -372,7 +376,8 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         float s[N];
 #pragma unroll
         for (int b = 0; b < N / 8; ++b)
-          if (b < blocks) tmem_ld8(tmem + C::kColS + buf * R + col0 + b * 8 + lanes, reinterpret_cast<uint32_t(&)[8]>(s[b * 8]));
+          if (b < blocks)
+            tmem_ld8(tmem + C::kColS + buf * R + col0 + b * 8 + lanes, reinterpret_cast<uint32_t(&)[8]>(s[b * 8]));
         tmem_wait_ld();
         tc_fence_before();
         mbar_arrive(s_empty + buf);
@@ -529,7 +534,8 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
             }
             const int at = col0 + b * 8;  // byte of the row; its 16-byte unit is swizzled
             *reinterpret_cast<uint2*>(prow + (((at >> 4) ^ (row & 7)) << 4) + (at & 8)) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(prow + (((4 + (at >> 4)) ^ (row & 7)) << 4) + (at & 8)) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2*>(prow + (((4 + (at >> 4)) ^ (row & 7)) << 4) + (at & 8)) =
+                make_uint2(lo[0], lo[1]);
           }
         fence_proxy_async_smem();
         tc_fence_before();

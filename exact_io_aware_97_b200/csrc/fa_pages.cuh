@@ -327,7 +327,8 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) comp
 // Large pages (the pools before `bulk`) go through shared memory in pieces of up to 16 KB by bulk
 // copies, which one thread issues: a ring of six pieces in flight each way per CTA, two CTAs per SM
 // (four vectors a thread in registers instead: 189 to 217 us for the 178 us of a compaction that moves
-// 543 MB; the copies alone then run at 6.4 TB/s, read and written, of the 6.55 of a plain copy).  Small pages go in vectors, four a thread, loaded before the first is stored.
+// 543 MB; the copies alone then run at 6.4 TB/s, read and written, of the 6.55 of a plain copy).
+// Small pages go in vectors, four a thread, loaded before the first is stored.
 constexpr int kCopyVecs = 1024, kCopyThreads = 256;
 constexpr int kBulkBytes = 16384, kBulkStages = 6, kCopySmem = kBulkStages * kBulkBytes + 128;
 
