@@ -340,7 +340,7 @@ def _pool_array(pools, num_pages):
         if not t.is_cuda or not t.is_contiguous():
             _ptr(t)  # says what is wrong
         flat.append(t.data_ptr())
-        flat.append(t.nbytes // num_pages)
+        flat.append(t.nbytes // max(num_pages, 1))
     return flat
 
 
