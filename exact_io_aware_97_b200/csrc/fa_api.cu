@@ -209,6 +209,25 @@ cudaError_t set_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+// A launch whose blocks may come while the stream's last kernel ends; the kernel waits for its results
+// (grid_wait) before it touches memory.  (1 to 2 us less between kernels, and 0.5 us less on the host.)
+template <class... P, class... A>
+bool launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return true;
+  (void)cudaGetLastError();  // reported here, not by a later call
+  return false;
+}
+
 // set_smem, once for each device (a call on this path is a few microseconds altogether).
 template <class K>
 bool set_smem_once(K kernel, int bytes, std::atomic<uint64_t>& done) {
@@ -950,13 +969,10 @@ fa_status launch_rope(RopeParams prm, cudaStream_t st) {
   prm.per_chunk = per * heads_at_once;
   prm.chunks = (nh + prm.per_chunk - 1) / prm.per_chunk;
   const unsigned blocks = (unsigned)((prm.rows * prm.chunks + 7) / 8);
-  if (prm.interleaved)
-    fa_rope_vec_kernel<T, D, true><<<blocks, 256, 0, st>>>(prm);
-  else if (prm.rot / 2 % V == 0)
-    fa_rope_vec_kernel<T, D, false><<<blocks, 256, 0, st>>>(prm);
-  else
-    fa_rope_kernel<T, D><<<blocks, 256, 0, st>>>(prm);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const auto kern = prm.interleaved         ? fa_rope_vec_kernel<T, D, true>
+                    : prm.rot / 2 % V == 0 ? fa_rope_vec_kernel<T, D, false>
+                                           : fa_rope_kernel<T, D>;
+  return launch_early(kern, blocks, 256, 0, st, prm) ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1068,8 +1084,7 @@ fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
   const int upc = kAppendCta / append_warps<D>(prm.sb_shift);
   const dim3 grid((unsigned)(prm.cu ? (prm.total >> prm.sb_shift) + 2ll * prm.B : prm.B),
                   (unsigned)((prm.Hkv + upc - 1) / upc));
-  fa_cache_append_kernel<D><<<grid, kAppendCta * 32, 0, st>>>(prm);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_early(fa_cache_append_kernel<D>, grid, kAppendCta * 32, 0, st, prm) ? FA_OK : FA_ERR_CUDA;
 }
 
 // What a unit costs beside its chunks, in chunks (measured on ragged batches).
@@ -1109,18 +1124,9 @@ fa_status launch_decode_fp8_merge(const Dec8Params& prm, int ctas, cudaStream_t 
   // The merge starts on the SMs that the last CTAs leave and waits there for their results.
   const int items = std::min(prm.rows, R) << prm.hs, gx = prm.by_unit ? prm.B * prm.units : ctas;
   const bool wide = (int64_t)gx * items <= 8ll * ctas;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(gx, wide ? items : (items + 7) / 8);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t err = wide ? cudaLaunchKernelEx(&cfg, fa_decode_fp8_combine_kernel<D, R, true>, prm)
-                               : cudaLaunchKernelEx(&cfg, fa_decode_fp8_combine_kernel<D, R, false>, prm);
-  return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  const dim3 grid(gx, wide ? items : (items + 7) / 8);
+  const auto kern = wide ? fa_decode_fp8_combine_kernel<D, R, true> : fa_decode_fp8_combine_kernel<D, R, false>;
+  return launch_early(kern, grid, 256, 0, st, prm) ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D, int MT, int RG>
@@ -1132,8 +1138,7 @@ fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& pr
   static std::atomic<uint64_t> smem_set{0};  // a bit for each device
   if (!set_smem_once(kern, C::kSmem, smem_set)) return FA_ERR_CUDA;
   const int ctas = dec8_ctas(C::kRows, D);
-  kern<<<ctas, C::kThreads, C::kSmem, st>>>(maps[0], maps[1], prm);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (!launch_early(kern, ctas, C::kThreads, C::kSmem, st, maps[0], maps[1], prm)) return FA_ERR_CUDA;
   return launch_decode_fp8_merge<D, C::kRows>(prm, ctas, st);
 }
 
@@ -1144,8 +1149,8 @@ fa_status launch_decode_fp8_tc(const void* kp, const void* vp, const Dec8Params&
   static std::atomic<uint64_t> smem_set{0};
   if (!set_smem_once(fa_decode_fp8_tc_kernel, C::kSmem, smem_set)) return FA_ERR_CUDA;
   const int ctas = dec8_ctas(C::kRows, C::D);
-  fa_decode_fp8_tc_kernel<<<ctas, C::kThreads, C::kSmem, st>>>(maps[0], maps[1], prm);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (!launch_early(fa_decode_fp8_tc_kernel, ctas, C::kThreads, C::kSmem, st, maps[0], maps[1], prm))
+    return FA_ERR_CUDA;
   return launch_decode_fp8_merge<C::D, C::kRows>(prm, ctas, st);
 }
 
@@ -1303,17 +1308,7 @@ fa_status launch_copies(const fa_pool* pools, int n_pools, const int32_t* src, c
       }
       if (turn == 0) list.bulk = list.n;
     }
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sms * 2);
-    cfg.blockDim = dim3(kCopyThreads + 32);
-    cfg.dynamicSmemBytes = kCopySmem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, pages_copy_kernel, list, src, dst, count, tickets++) != cudaSuccess)
+    if (!launch_early(pages_copy_kernel, sms * 2, kCopyThreads + 32, kCopySmem, st, list, src, dst, count, tickets++))
       return FA_ERR_CUDA;
   }
   return FA_OK;
@@ -1367,8 +1362,7 @@ extern "C" fa_status fa_pages_fork(const fa_pool* pools, int n_pools, const int3
   prm.max_pages = max_pages_per_seq;
   prm.page_shift = __builtin_ctz((unsigned)page_size);
   prm.num_pages = num_pages;
-  fork_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(prm);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (!launch_early(fork_plan_kernel, kPlanCtas, kPlanThreads, 0, st, prm)) return FA_ERR_CUDA;
   return launch_copies(pools, n_pools, prm.src, prm.dst, prm.count, prm.tickets, st);
 }
 
@@ -1403,7 +1397,6 @@ extern "C" fa_status fa_pages_compact(const fa_pool* pools, int n_pools, const i
   prm.max_pages = max_pages_per_seq;
   prm.page_shift = __builtin_ctz((unsigned)page_size);
   prm.num_pages = num_pages;
-  compact_plan_kernel<<<kPlanCtas, kPlanThreads, 0, st>>>(prm);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (!launch_early(compact_plan_kernel, kPlanCtas, kPlanThreads, 0, st, prm)) return FA_ERR_CUDA;
   return launch_copies(pools, n_pools, prm.src, prm.dst, prm.count, prm.tickets, st);
 }

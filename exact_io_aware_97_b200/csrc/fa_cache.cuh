@@ -247,6 +247,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, const AppendU
 template <int D>
 __global__ void __launch_bounds__(kAppendCta * 32, 4) fa_cache_append_kernel(const AppendParams p) {
   __shared__ uint32_t sm_max[2][kAppendCta];
+  grid_wait();
   const int warp = threadIdx.x >> 5;
   const int wpu = append_warps<D>(p.sb_shift), upc = kAppendCta / wpu;  // warps of a unit, heads of a CTA
 

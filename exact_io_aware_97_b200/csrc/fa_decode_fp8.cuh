@@ -333,6 +333,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
     prefetch_tensormap(&tmV);
   }
 
+  grid_wait();
   Dec8Walk walk = dec8_share<C::kThreads>(p, share);
   Dec8Seg seg;
 
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
       if (!ok)  // a wait ran out: leave no copy in flight (the last fill of each slot)
         for (int s = 0; s < NS; ++s) (void)mbar_wait(full + s, s < slot ? phase ^ 1u : phase);
       // the merge may be launched once every CTA has its last loads under way
-      if (lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      if (lane == 0) grid_release();
     }
     return;
   }
@@ -783,7 +784,7 @@ __global__ void __launch_bounds__(256) fa_decode_fp8_combine_kernel(const Dec8Pa
   constexpr int V = D / 32, W = 8;
   __shared__ float sm_l[W], sm_o[W][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
   const int4 d = p.ws_desc[blockIdx.x];
   const int parts = d.x & 0xFFFF, x = d.x >> 16;
   if (parts == 0) return;

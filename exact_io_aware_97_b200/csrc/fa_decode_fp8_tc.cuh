@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
+  grid_wait();
   Dec8Walk walk = dec8_share<C::kThreads>(p, share);  // synchronises the CTA
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         }
         if (!ok)  // a wait ran out: leave no copy in flight (the last fill of each slot)
           for (int s = 0; s < C::kSlots; ++s) (void)mbar_wait(full + s, s >> 1 < pair ? phase ^ 1u : phase);
-        if (lane == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        if (lane == 0) grid_release();
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer

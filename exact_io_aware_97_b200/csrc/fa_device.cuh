@@ -98,6 +98,13 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// ---------------------------------------------------------------- early launches
+// A kernel that was launched to come while the stream's last one ends: waits until that has ended and
+// its writes are visible.  Nothing that it wrote is read, and nothing is written, before.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets a following kernel of that kind come once every block has got here.
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- TMA
 // 3-D tiled load of a box into shared memory, completing on `bar` (transaction bytes).
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2,

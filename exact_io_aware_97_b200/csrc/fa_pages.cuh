@@ -127,8 +127,9 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork
   const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tid = cta * kPlanThreads + threadIdx.x, threads = kPlanCtas * kPlanThreads;
   const int psm = (1 << p.page_shift) - 1;
+  grid_wait();
   // the copies' blocks may come to the idle SMs now; they wait for this kernel's end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
   if (tid < kMaxLaunches) p.tickets[tid] = 0;
   for (int g = tid; g < p.num_pages; g += threads) p.mark[g] = kFreeMark;
   // this thread's first row of the steps after the marks; lookups that fill the cache meanwhile
@@ -243,8 +244,9 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) comp
   const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tid = cta * kPlanThreads + threadIdx.x, threads = kPlanCtas * kPlanThreads;
   const int psm = (1 << p.page_shift) - 1;
+  grid_wait();
   // the copies' blocks may come to the idle SMs now; they wait for this kernel's end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_release();
   if (tid < kMaxLaunches) p.tickets[tid] = 0;
   for (int g = tid; g < p.num_pages; g += threads) p.mark[g] = kFreeMark;
   cluster_sync();
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kCopyThreads + 32, 2)
     pages_copy_kernel(const __grid_constant__ PoolList pools, const int32_t* src, const int32_t* dst,
                       const int32_t* count, int32_t* next) {
   extern __shared__ uint8_t smem_raw[];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
   const int n = *count;
   if (threadIdx.x < kCopyThreads) {
     CopyWalk w{pools.bulk, pools.n, blockIdx.x, 0};

@@ -55,6 +55,7 @@ __device__ __forceinline__ void rope_store(__nv_bfloat16* y, float v) { *y = __f
 // vectors below cannot take (8192 rows as above in this way: 184 us).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) fa_rope_kernel(const RopeParams p) {
+  grid_wait();
   const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const long long row = unit / p.chunks;
@@ -122,6 +123,7 @@ template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(256) fa_rope_vec_kernel(const RopeParams p) {
   using X = RopeVec<T>;
   constexpr int V = X::N, kSlots = D / (2 * V), kHeads = 32 / kSlots, kShare = V / kHeads, kUnroll = 4;
+  grid_wait();
   const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31, slot = lane % kSlots, sub = lane / kSlots;
   const long long row = unit / p.chunks;

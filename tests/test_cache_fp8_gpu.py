@@ -595,3 +595,63 @@ def test_prefill_then_decode_through_the_cache():
         s.synchronize()
         verify(*out)
     assert fa.fa_last_device_error() == fa.FA_OK
+
+
+def test_captured_after_copies_and_joined_streams():
+    """Launches may come early, while what is before them in the stream ends: in a captured graph
+    that can be a copy, a fill, or the join of two streams.  Every replay reads what came before it."""
+    B, H, Hq, d, ps, sb, maxp = 3, 2, 48, 128, 32, 16, 2
+    P = B * maxp + 4
+    src = [torch.randn(B, h, d, device="cuda").bfloat16() for h in (Hq, H, H)]
+    q, k, v = (torch.zeros_like(t) for t in src)
+    kp, vp = (torch.zeros(P, ps, H, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.zeros(P, H, ps // sb, device="cuda") for _ in range(2))
+    dt = torch.arange(B * maxp, dtype=torch.int32, device="cuda").view(B, maxp)
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    parent = torch.tensor([2, 2, 0], dtype=torch.int32, device="cuda")
+    freqs = fa.rope_frequencies(d)
+    side = torch.cuda.Stream()
+
+    def chain():
+        q.copy_(src[0])  # a copy straight before the rotation
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            k.copy_(src[1])
+            v.copy_(src[2])
+            fa.rope(k, None, freqs, lens, q_out=k)
+        fa.rope(q, None, freqs, lens, q_out=q)
+        torch.cuda.current_stream().wait_stream(side)  # both streams before the append
+        lens.add_(1)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            lens2 = lens.clone()
+        torch.cuda.current_stream().wait_stream(side)
+        fa.cache_append_fp8(k, v, kp, vp, ks, vs, dt, lens2)
+        o, lse = fa.decode_paged_fp8(q, kp, vp, ks, vs, dt, lens)
+        table, ln, free, n = fa.pages_fork([kp, vp, ks, vs], dt, lens, parent, ps)
+        o2, lse2 = fa.decode_paged_fp8(q, kp, vp, ks, vs, table, ln)
+        return o, lse, table, ln, free, n, o2, lse2
+
+    def fresh(n):
+        for t in src:
+            t.copy_(torch.randn(t.shape, device="cuda"))
+        for t in (kp.view(torch.uint8), vp.view(torch.uint8), ks, vs, lens):
+            t.zero_()
+        lens.fill_(n)
+
+    state = torch.cuda.get_rng_state()
+    want = []
+    for n in (0, 17, 30):
+        fresh(n)
+        want.append([t.clone() for t in chain()])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = chain()
+    torch.cuda.set_rng_state(state)
+    for n, w in zip((0, 17, 30), want):
+        fresh(n)
+        g.replay()
+        for a, b in zip(out, w):
+            assert torch.equal(a, b)
+    assert torch.isfinite(out[0].float()).all() and fa.fa_last_device_error() == fa.FA_OK
