@@ -13,6 +13,7 @@
 #include "fa_bwd_sm100.cuh"
 #include "fa_cache.cuh"
 #include "fa_decode_fp8.cuh"
+#include "fa_decode_fp8_narrow.cuh"
 #include "fa_decode_fp8_tc.cuh"
 #include "fa_decode_sm100.cuh"
 #include "fa_fwd_sm100.cuh"
@@ -1089,18 +1090,22 @@ fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
 
 // What a unit costs beside its chunks, in chunks (measured on ragged batches).
 constexpr int kDec8Lead = 4, kDec8TcLead = 10;
-// Query rows of a unit: one tensor-core tile of 16 where that holds them; else the kernel on tcgen05
-// products with 64 (d = 128: 40 rows in 101 us instead of 211 with 64 rows in registers), or
-// registers for 32 or 64 (d = 64, where a cache row is too short for those products' 128 rows).
-int dec8_tile(int64_t rows, int d) { return rows <= 16 ? 16 : rows <= 32 && d == 64 ? 32 : 64; }
+// Query rows of a unit: the 8 columns of a tensor-core product, or its 16 rows, where that holds them
+// (8 rows: 91 us instead of 100 as 16); else the kernel on tcgen05 products with 64 (d = 128: 40 rows in
+// 101 us instead of 211 with 64 rows in registers), or registers for 32 or 64 (d = 64, where a cache
+// row is too short for those products' 128 rows).
+int dec8_tile(int64_t rows, int d) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 && d == 64 ? 32 : 64; }
 // K/V heads of a unit, as a shift: one where the query rows fill more than a tile (the products,
 // not the loads, take the time then, and one head's queries are all that shared memory holds).
 int dec8_heads(int tile, int Hkv) { return tile > 16 ? 0 : Hkv % 4 == 0 ? 2 : Hkv % 2 == 0 ? 1 : 0; }
 // One wave of CTAs (where no device is present, the number of the B200's).
 int dec8_ctas(int tile, int d) {
   const int sms = sm_count_cached();
-  return (sms > 0 ? sms : 148) * (tile == 16 ? (d == 64 ? Dec8Cfg<64, 1, 1>::kCtas : Dec8Cfg<128, 1, 1>::kCtas)
-                                  : tile == 32 ? Dec8Cfg<64, 2, 1>::kCtas : 1);
+  const int per_sm = tile == 8    ? Dec8Cfg<128>::kCtas
+                     : tile == 16 ? (d == 64 ? Dec8WideCfg<64, 1, 1>::kCtas : Dec8WideCfg<128, 1, 1>::kCtas)
+                     : tile == 32 ? Dec8WideCfg<64, 2, 1>::kCtas
+                                  : 1;
+  return (sms > 0 ? sms : 148) * per_sm;
 }
 
 bool dec8_maps(CUtensorMap (&maps)[2], const void* kp, const void* vp, int d, const Dec8Params& prm) {
@@ -1129,12 +1134,10 @@ fa_status launch_decode_fp8_merge(const Dec8Params& prm, int ctas, cudaStream_t 
   return launch_early(kern, grid, 256, 0, st, prm) ? FA_OK : FA_ERR_CUDA;
 }
 
-template <int D, int MT, int RG>
-fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& prm, cudaStream_t st) {
-  using C = Dec8Cfg<D, MT, RG>;
+template <class C, int D, class K>
+fa_status launch_decode_fp8(K kern, const void* kp, const void* vp, const Dec8Params& prm, cudaStream_t st) {
   CUtensorMap maps[2];
   if (!dec8_maps(maps, kp, vp, D, prm)) return FA_ERR_CUDA;
-  auto kern = fa_decode_fp8_kernel<D, MT, RG>;
   static std::atomic<uint64_t> smem_set{0};  // a bit for each device
   if (!set_smem_once(kern, C::kSmem, smem_set)) return FA_ERR_CUDA;
   const int ctas = dec8_ctas(C::kRows, D);
@@ -1142,16 +1145,18 @@ fa_status launch_decode_fp8(const void* kp, const void* vp, const Dec8Params& pr
   return launch_decode_fp8_merge<D, C::kRows>(prm, ctas, st);
 }
 
+template <int D>
+fa_status launch_decode_fp8_narrow(const void* kp, const void* vp, const Dec8Params& prm, cudaStream_t st) {
+  return launch_decode_fp8<Dec8Cfg<D>, D>(fa_decode_fp8_kernel<D>, kp, vp, prm, st);
+}
+
+template <int D, int MT, int RG>
+fa_status launch_decode_fp8_wide(const void* kp, const void* vp, const Dec8Params& prm, cudaStream_t st) {
+  return launch_decode_fp8<Dec8WideCfg<D, MT, RG>, D>(fa_decode_fp8_wide_kernel<D, MT, RG>, kp, vp, prm, st);
+}
+
 fa_status launch_decode_fp8_tc(const void* kp, const void* vp, const Dec8Params& prm, cudaStream_t st) {
-  using C = Dec8TcCfg;
-  CUtensorMap maps[2];
-  if (!dec8_maps(maps, kp, vp, C::D, prm)) return FA_ERR_CUDA;
-  static std::atomic<uint64_t> smem_set{0};
-  if (!set_smem_once(fa_decode_fp8_tc_kernel, C::kSmem, smem_set)) return FA_ERR_CUDA;
-  const int ctas = dec8_ctas(C::kRows, C::D);
-  if (!launch_early(fa_decode_fp8_tc_kernel, ctas, C::kThreads, C::kSmem, st, maps[0], maps[1], prm))
-    return FA_ERR_CUDA;
-  return launch_decode_fp8_merge<C::D, C::kRows>(prm, ctas, st);
+  return launch_decode_fp8<Dec8TcCfg, Dec8TcCfg::D>(fa_decode_fp8_tc_kernel, kp, vp, prm, st);
 }
 
 }  // namespace
@@ -1255,11 +1260,13 @@ extern "C" fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, con
   prm.by_unit = B * units <= (int64_t)ctas;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (d == 64)
-    return tile == 16   ? launch_decode_fp8<64, 1, 1>(k_pages, v_pages, prm, st)
-           : tile == 32 ? launch_decode_fp8<64, 2, 1>(k_pages, v_pages, prm, st)
-                        : launch_decode_fp8<64, 2, 2>(k_pages, v_pages, prm, st);
-  return tile == 16 ? launch_decode_fp8<128, 1, 1>(k_pages, v_pages, prm, st)
-                    : launch_decode_fp8_tc(k_pages, v_pages, prm, st);
+    return tile == 8    ? launch_decode_fp8_narrow<64>(k_pages, v_pages, prm, st)
+           : tile == 16 ? launch_decode_fp8_wide<64, 1, 1>(k_pages, v_pages, prm, st)
+           : tile == 32 ? launch_decode_fp8_wide<64, 2, 1>(k_pages, v_pages, prm, st)
+                        : launch_decode_fp8_wide<64, 2, 2>(k_pages, v_pages, prm, st);
+  return tile == 8    ? launch_decode_fp8_narrow<128>(k_pages, v_pages, prm, st)
+         : tile == 16 ? launch_decode_fp8_wide<128, 1, 1>(k_pages, v_pages, prm, st)
+                      : launch_decode_fp8_tc(k_pages, v_pages, prm, st);
 }
 
 // ---------------------------------------------------------------------------------------

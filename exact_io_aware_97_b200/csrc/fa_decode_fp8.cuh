@@ -29,6 +29,9 @@
 // a bf16 cache, has 8) relative to their own running maximum, so neither a scale far from the
 // others' nor a small p loses bits; p itself is summed in fp32 for l.  A warp owns 16 consecutive
 // rows of each chunk, which lie in one scale block: one K and one V scale per warp and chunk.
+//
+// Up to 8 query rows take fa_decode_fp8_kernel (fa_decode_fp8_narrow.cuh); this file has what the
+// kernels share, the kernel for more of them, and the merge.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -61,10 +64,13 @@ struct Dec8Params {
 
 constexpr int kDec8Keys = 128;  // cache rows of a chunk, counted over its K/V heads
 constexpr int kDec8Whole = 4;   // units of at most this many chunks are not cut
-constexpr float kDec8Low = -3e38f;  // running maxima before anything was seen
+constexpr float kDec8Low = -3e38f;  // references before anything was seen
+// A score may be that far (base 2) above its row's reference; only one farther up moves the reference to
+// the largest so far, and only then are the lanes' maxima brought together.
+constexpr float kDec8Slack = 6.f;
 
 template <int D, int MT, int RG>
-struct Dec8Cfg {
+struct Dec8WideCfg {
   static constexpr int kRows = 16 * MT * RG;       // R: query rows of a unit
   static constexpr int kWarps = 4 * RG;            // compute warps: 4 slices of 32 rows of the chunk x RG row groups
   // 16-row tiles of the cache that a warp takes at once: two where the registers allow it, for
@@ -306,11 +312,92 @@ __device__ __noinline__ void dec8_nan_v(uint8_t* vs, int j0, int len, const int 
   __syncwarp();
 }
 
+// The producer warp's part.  Lanes 0..15: (K or V, K/V head, 16-row tile of the chunk), in the order of
+// the warps that take them.  Each fetches the scale of its tile, and the first head's lanes at the head
+// of a page's rows the box of them, all heads at once; tiles past the end are left out.  The table
+// entry of the next chunk is loaded while this one is issued.
+template <int D, int NS>
+__device__ __forceinline__ void dec8_produce(const CUtensorMap& tmK, const CUtensorMap& tmV, const Dec8Params& p,
+                                             Dec8Walk walk, uint8_t* ring, float* sm_scale, uint64_t* full,
+                                             uint64_t* empty) {
+  constexpr int kHalf = kDec8Keys * D, kStage = 2 * kHalf;
+  const int lane = threadIdx.x & 31;
+  if (lane >= 16) return;
+  const int which = lane >> 3, sub = lane & 7;
+  const uint64_t pol = policy_evict_first();
+  const int psm = (1 << p.page_shift) - 1, nb_shift = p.page_shift - p.sb_shift;
+  const int chunk = kDec8Keys >> p.hs;
+  const int headi = (sub >> 1) >> (2 - p.hs);
+  const int ro = 16 * (2 * ((sub >> 1) & ((4 >> p.hs) - 1)) + (sub & 1));  // first row in the chunk
+  const bool leads = headi == 0 && ro % p.box == 0;
+  Dec8Seg seg;
+  int slot = 0;
+  uint32_t phase = 1;  // of the slot's release: the first round finds it free
+  bool ok = true;
+  while (ok && walk.next(p, seg)) {
+    const int kvh0 = (seg.unit / p.tiles) << p.hs;
+    const int32_t* bt = p.block_table + (long long)seg.b * p.max_pages;
+    int tok = seg.c0 * chunk + ro;
+    int page_next = tok < seg.len ? __ldg(bt + (tok >> p.page_shift)) : 0;
+    for (int c = seg.c0; c < seg.c1; ++c, tok += chunk) {
+      int page = page_next;
+      const bool here = tok < seg.len;
+      if (c + 1 < seg.c1 && tok + chunk < seg.len) page_next = __ldg(bt + ((tok + chunk) >> p.page_shift));
+      if (page < 0 || page >= p.num_pages) {
+        atomicOr(&g_error_word, kErrBadPage);
+        page = 0;
+      }
+      ok = __all_sync(0xffffu, mbar_wait(empty + slot, phase));
+      if (!ok) break;
+      uint8_t* st = ring + slot * kStage;
+      if (lane == 0) {
+        const int rows = min(chunk, (seg.len - c * chunk + p.box - 1) / p.box * p.box);
+        mbar_arrive_expect_tx(full + slot, 2 * (rows << p.hs) * D);
+      }
+      __syncwarp(0xffffu);
+      const int r = tok & psm;
+      if (here) {
+        if (leads)
+          tma_load_3d_hint(st + which * kHalf + (ro << p.hs) * D, which ? &tmV : &tmK, 0, (page << p.page_shift) + r,
+                           kvh0, full + slot, pol);
+        const float* src =
+            p.scales[which] + (((long long)page * p.Hkv + kvh0 + headi) << nb_shift) + (r >> p.sb_shift);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sm_scale + slot * 16 + lane)), "l"(src)
+                     : "memory");
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + slot)) : "memory");
+      } else {
+        sm_scale[slot * 16 + lane] = 0.f;  // a tile past the end may share a warp's step with one before it
+        mbar_arrive(full + slot);
+      }
+      if (++slot == NS) slot = 0, phase ^= 1u;
+    }
+  }
+  if (!ok)  // a wait ran out: leave no copy in flight (the last fill of each slot)
+    for (int s = 0; s < NS; ++s) (void)mbar_wait(full + s, s < slot ? phase ^ 1u : phase);
+  // the merge may be launched once every CTA has its last loads under way
+  if (lane == 0) grid_release();
+}
+
+// Sequences without rows, dealt to the CTAs: o = 0, lse = -inf; thread `tid` of THREADS.
+template <int D, int THREADS>
+__device__ __forceinline__ void dec8_empty(const Dec8Params& p, int tid) {
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (dec8_len(p, b) > 0) continue;
+    const long long n = (long long)p.Nq * p.Hq;
+    for (long long k = tid; k < n * D / 8; k += THREADS)
+      reinterpret_cast<uint4*>(p.o)[(long long)b * (n * D / 8) + k] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse)
+      for (long long k = tid; k < n; k += THREADS) p.lse[b * n + k] = -INFINITY;
+    if (p.by_unit)
+      for (int k = tid; k < p.units; k += THREADS) p.ws_desc[b * p.units + k] = make_int4(0, 0, 0, 0);
+  }
+}
+
 template <int D, int MT, int RG>
-__global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, RG>::kCtas)
-    fa_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+__global__ void __launch_bounds__(Dec8WideCfg<D, MT, RG>::kThreads, Dec8WideCfg<D, MT, RG>::kCtas)
+    fa_decode_fp8_wide_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const Dec8Params p) {
-  using C = Dec8Cfg<D, MT, RG>;
+  using C = Dec8WideCfg<D, MT, RG>;
   constexpr int NS = C::kStages, KS = D / 16, R = C::kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -340,66 +427,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
   if (warp >= C::kWarps) {
     // ------------------------------------------------------------ producer
     if constexpr (C::kSplitRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-    // Lanes 0..15: (K or V, K/V head, 16-row tile of the chunk), in the order of the warps that take
-    // them.  Each fetches the scale of its tile, and the first head's lanes at the head of a page's
-    // rows the box of them, all heads at once; tiles past the end are left out.
-    // The table entry of the next chunk is loaded while this one is issued.
-    if (warp == C::kWarps && lane < 16) {
-      const int which = lane >> 3, sub = lane & 7;
-      const uint64_t pol = policy_evict_first();
-      const int psm = (1 << p.page_shift) - 1, nb_shift = p.page_shift - p.sb_shift;
-      const int chunk = kDec8Keys >> p.hs;
-      const int headi = (sub >> 1) >> (2 - p.hs);
-      const int ro = 16 * (2 * ((sub >> 1) & ((4 >> p.hs) - 1)) + (sub & 1));  // first row in the chunk
-      const bool leads = headi == 0 && ro % p.box == 0;
-      int slot = 0;
-      uint32_t phase = 1;  // of the slot's release: the first round finds it free
-      bool ok = true;
-      while (ok && walk.next(p, seg)) {
-        const int kvh0 = (seg.unit / p.tiles) << p.hs;
-        const int32_t* bt = p.block_table + (long long)seg.b * p.max_pages;
-        int tok = seg.c0 * chunk + ro;
-        int page_next = tok < seg.len ? __ldg(bt + (tok >> p.page_shift)) : 0;
-        for (int c = seg.c0; c < seg.c1; ++c, tok += chunk) {
-          int page = page_next;
-          const bool here = tok < seg.len;
-          if (c + 1 < seg.c1 && tok + chunk < seg.len) page_next = __ldg(bt + ((tok + chunk) >> p.page_shift));
-          if (page < 0 || page >= p.num_pages) {
-            atomicOr(&g_error_word, kErrBadPage);
-            page = 0;
-          }
-          ok = __all_sync(0xffffu, mbar_wait(empty + slot, phase));
-          if (!ok) break;
-          uint8_t* st = ring + slot * C::kStage;
-          if (lane == 0) {
-            const int rows = min(chunk, (seg.len - c * chunk + p.box - 1) / p.box * p.box);
-            mbar_arrive_expect_tx(full + slot, 2 * (rows << p.hs) * D);
-          }
-          __syncwarp(0xffffu);
-          const int r = tok & psm;
-          if (here) {
-            if (leads)
-              tma_load_3d_hint(st + which * C::kHalf + (ro << p.hs) * D, which ? &tmV : &tmK, 0,
-                               (page << p.page_shift) + r, kvh0, full + slot, pol);
-            const float* src =
-                p.scales[which] + (((long long)page * p.Hkv + kvh0 + headi) << nb_shift) + (r >> p.sb_shift);
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sm_scale + slot * 16 + lane)),
-                         "l"(src)
-                         : "memory");
-            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + slot))
-                         : "memory");
-          } else {
-            sm_scale[slot * 16 + lane] = 0.f;  // a tile past the end may share a warp's step with one before it
-            mbar_arrive(full + slot);
-          }
-          if (++slot == NS) slot = 0, phase ^= 1u;
-        }
-      }
-      if (!ok)  // a wait ran out: leave no copy in flight (the last fill of each slot)
-        for (int s = 0; s < NS; ++s) (void)mbar_wait(full + s, s < slot ? phase ^ 1u : phase);
-      // the merge may be launched once every CTA has its last loads under way
-      if (lane == 0) grid_release();
-    }
+    if (warp == C::kWarps) dec8_produce<D, NS>(tmK, tmV, p, walk, ring, sm_scale, full, empty);
     return;
   }
 
@@ -423,17 +451,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
   uint32_t phase = 0;
   bool ok = true;
 
-  // sequences without rows: o = 0, lse = -inf
-  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-    if (dec8_len(p, b) > 0) continue;
-    const long long n = (long long)p.Nq * p.Hq;
-    for (long long k = threadIdx.x; k < n * D / 8; k += C::kWarps * 32)
-      reinterpret_cast<uint4*>(p.o)[(long long)b * (n * D / 8) + k] = make_uint4(0u, 0u, 0u, 0u);
-    if (p.lse)
-      for (long long k = threadIdx.x; k < n; k += C::kWarps * 32) p.lse[b * n + k] = -INFINITY;
-    if (p.by_unit)
-      for (int k = threadIdx.x; k < p.units; k += C::kWarps * 32) p.ws_desc[b * p.units + k] = make_int4(0, 0, 0, 0);
-  }
+  dec8_empty<D, C::kWarps * 32>(p, threadIdx.x);
 
   while (walk.next(p, seg)) {
     const int group = seg.unit / p.tiles, tile = seg.unit - group * p.tiles;
@@ -488,7 +506,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
     const bool idle = row0 >= p.rows;  // a row group without rows
 
     float acc[MT][D / 8][4];
-    float m_r[MT][2], l_r[MT][2], w_r[MT][2];  // running maxima of t and of t + log2(sv); sum of p
+    float m_r[MT][2], l_r[MT][2], w_r[MT][2];  // references of t and of t + log2(sv); sum of p
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -590,16 +608,13 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
                   s1[0] = j + 8 < lim ? s1[0] : -INFINITY;
                   s1[1] = j + 9 < lim ? s1[1] : -INFINITY;
                 }
-                float x = fmaxf(fmax3(s0[0], s0[1], s1[0]), s1[1]);
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
                 f[mt][hr][kt] = fac[mt][hr] * sk[kt];
-                x *= f[mt][hr][kt];
+                const float x = fmaxf(fmax3(s0[0], s0[1], s1[0]), s1[1]) * f[mt][hr][kt];
                 mx[mt][hr][kt] = x;
-                moved |= x > m_r[mt][hr] || x + lsv[kt] > w_r[mt][hr];
+                moved |= x > m_r[mt][hr] + kDec8Slack || x + lsv[kt] > w_r[mt][hr] + kDec8Slack;
               }
           if (__any_sync(0xffffffffu, moved)) {
-            // some maximum rises: bring the sums to the new references (NaN never raises one)
+            // some score is far above its reference: bring the sums to new ones (NaN never raises one)
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               float aw[2];
@@ -610,6 +625,11 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
                 for (int kt = 0; kt < KT; ++kt) {
                   m = fmaxf(m, mx[mt][hr][kt]);
                   w = fmaxf(w, mx[mt][hr][kt] + lsv[kt]);
+                }
+#pragma unroll
+                for (int off = 1; off < 4; off <<= 1) {
+                  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                  w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, off));
                 }
                 l_r[mt][hr] *= ex2_approx(m_r[mt][hr] - m);
                 aw[hr] = ex2_approx(w_r[mt][hr] - w);
@@ -631,10 +651,10 @@ __global__ void __launch_bounds__(Dec8Cfg<D, MT, RG>::kThreads, Dec8Cfg<D, MT, R
             for (int hr = 0; hr < 2; ++hr)
 #pragma unroll
               for (int kt = 0; kt < KT; ++kt) {
-                // p = 2^(t - m); the weight is p times cw = sv 2^(m - w), at most 1 (the bound keeps
+                // p = 2^(t - m); the weight is p times cw = sv 2^(m - w), 2^6 at most (the bound keeps
                 // 0 * cw at 0 where a scale dwarfs the ones that m came from)
                 const float ec = m_r[mt][hr] - w_r[mt][hr] + lsv[kt];
-                const float cw = ex2_approx(ec > 126.f ? 126.f : ec);  // NaN stays
+                const float cw = ex2_approx(ec > 120.f ? 120.f : ec);  // NaN stays
                 const float ff = f[mt][hr][kt], m = m_r[mt][hr];
                 float p0 = ex2_approx(fmaf(sc[mt][2 * kt][2 * hr], ff, -m));
                 float p1 = ex2_approx(fmaf(sc[mt][2 * kt][2 * hr + 1], ff, -m));
