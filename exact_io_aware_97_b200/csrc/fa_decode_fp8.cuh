@@ -7,31 +7,31 @@
 // where k_j, v_j are the stored e4m3 values and sk_j, sv_j the scales of their blocks.
 //
 // Bound by HBM: 2 d bytes per cache row and K/V head are read once (DRAM reads 1.00 times that).
-// 8 sequences of 32K rows, 64 query and 8 K/V heads, d = 128: 100 to 105 us, 5.1 to 5.4 TB/s of the
-// 6.55 that a copy reaches; 6.65 TB/s between 32K and 64K rows, so what is left is the start (5 us to
-// the first rows), CTAs that end up to 7 us after the mean although their shares are equal, and the
-// merge (5 us).
+// 8 sequences of 32K rows, 64 query and 8 K/V heads, d = 128: 90 to 92 us, 5.8 to 6.0 TB/s of the 6.55
+// that a copy reaches.  What is left is the start (5 us to the first rows), CTAs that end a little
+// after the mean although their shares are equal, and the merge (5 us).
 //
 // Partition.  The Nq * G query rows of one K/V head form tiles of R rows; a unit is (sequence,
 // group of K/V heads, tile) and is cut into chunks of cache rows.  A group is four heads (two, one)
-// where that divides Hkv and a tile has 16 rows: a chunk then reads 4 d bytes side by side from
-// each cache row instead of d (8 sequences of 64K rows, 8 heads, d = 128, loads without products: 190
-// us one head at a time, 175 us four).  All units' chunks, one after the
-// other, are dealt to the CTAs of one wave in equal contiguous shares, whatever the lengths, so
-// every CTA streams the same number of bytes.  A CTA writes the output of units that lie in its
-// share whole; of at most two others (its first and its last) it writes partial sums, which
-// fa_decode_fp8_combine_kernel merges with the m / l rule.
+// where that divides Hkv and a tile has at most 16 rows: a chunk then reads 4 d bytes side by side
+// from each cache row instead of d (8 sequences of 64K rows, 8 heads, d = 128, loads without products:
+// 190 us one head at a time, 175 us four).  All units' chunks, one after the other, are dealt to the
+// CTAs of one wave in equal contiguous shares, whatever the lengths, so every CTA streams the same
+// number of bytes.  A CTA writes the output of units that lie in its share whole; of at most two
+// others (its first and its last) it writes partial sums, which fa_decode_fp8_combine_kernel merges
+// with the m / l rule.
 //
 // Products.  e4m3 values are exact in fp16, so K and V are widened in registers (one conversion
 // for two values, after ldmatrix) and multiplied on m16n8k16 fp16 tensor-core products with fp32
 // sums.  A query row is scaled by a power of two into [1, 2) at its largest element, which keeps
 // its bf16 bits in fp16.  The weights p_j sv_j go through fp16 (11 bits; p alone in bf16, as over
-// a bf16 cache, has 8) relative to their own running maximum, so neither a scale far from the
-// others' nor a small p loses bits; p itself is summed in fp32 for l.  A warp owns 16 consecutive
-// rows of each chunk, which lie in one scale block: one K and one V scale per warp and chunk.
+// a bf16 cache, has 8) relative to a reference of their own near their largest one, so neither a scale
+// far from the others' nor a small p loses bits; p itself is summed in fp32 for l.  A warp takes 16
+// consecutive rows at a time, which lie in one scale block: one K and one V scale.
 //
-// Up to 8 query rows take fa_decode_fp8_kernel (fa_decode_fp8_narrow.cuh); this file has what the
-// kernels share, the kernel for more of them, and the merge.
+// Up to 8 query rows take fa_decode_fp8_kernel (fa_decode_fp8_narrow.cuh), more than 16 with d = 128
+// fa_decode_fp8_tc_kernel (fa_decode_fp8_tc.cuh).  This file has what the three share, the kernel for
+// the others and the merge.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -75,7 +75,7 @@ struct Dec8WideCfg {
   static constexpr int kWarps = 4 * RG;            // compute warps: 4 slices of 32 rows of the chunk x RG row groups
   // 16-row tiles of the cache that a warp takes at once: two where the registers allow it, for
   // twice the independent chains (one at a time, with two exponentials for each score: 128 us instead
-  // of 112 on the 32K decode)
+  // of 112 for 8 of 16 rows, 8 sequences of 32K)
   static constexpr int kTiles = MT == 1 ? 2 : 1;
   // A warp with two row tiles needs more registers than its share: the producer then is a warp of
   // a warpgroup of its own, which gives registers up (threads x registers of a CTA: MT = 2, RG = 1:
@@ -83,7 +83,8 @@ struct Dec8WideCfg {
   static constexpr bool kSplitRegs = MT > 1;
   static constexpr int kComputeRegs = RG == 1 ? 208 : 224;
   static constexpr int kThreads = (kWarps + (kSplitRegs ? 4 : 1)) * 32;
-  // per SM: what the registers allow; d = 64 has room for three (16 x 32K rows: 118 -> 105 us)
+  // per SM: what the registers allow; d = 64 has room for three (8 of 16 rows, 16 sequences of 32K: 118 ->
+  // 105 us)
   static constexpr int kCtas = MT == 1 && D == 64 ? 3 : RG == 1 ? 2 : 1;
   static constexpr int kHalf = kDec8Keys * D;       // bytes of K (or V) of a chunk
   static constexpr int kStage = 2 * kHalf;          // also the size of the merge of 16 rows of 4 slices
