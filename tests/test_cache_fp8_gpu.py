@@ -83,6 +83,12 @@ CASES = [
     ([100] * 90, 3, 12, 2, 128, 16, 16),        # more short units than CTAs
     ([40, 0, 3] * 40, 1, 8, 4, 128, 16, 16),
     ([520] * 30, 1, 6, 6, 64, 16, 16),
+    ([300, 40, 0, 2], 3, 16, 4, 64, 32, 16),    # 9 to 16 rows: four, two and one K/V heads at a time
+    ([700, 33], 2, 14, 2, 64, 16, 16),
+    ([513, 12], 11, 2, 2, 128, 64, 64),
+    ([260, 259], 1, 12, 1, 64, 64, 32),
+    ([290, 7, 5], 8, 3, 3, 128, 32, 32),        # 8 new tokens, each its own row
+    ([1030, 4], 4, 4, 2, 128, 512, 256),
 ]
 
 
@@ -242,21 +248,22 @@ def test_decode_fp8_nan_reaches_only_what_attends_to_it():
     assert fa.fa_last_device_error() == fa.FA_OK
 
 
-@pytest.mark.parametrize("Hq", [4, 24], ids=["16rows", "48rows"])
-def test_decode_fp8_nan_of_a_later_token_is_not_seen_before_it(Hq):
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Hq", [4, 8, 24], ids=["8rows", "16rows", "48rows"])
+def test_decode_fp8_nan_of_a_later_token_is_not_seen_before_it(Hq, d):
     """Four new tokens; the third one's V row holds a NaN code, the last one's block scale is NaN."""
     rng = np.random.default_rng(5011)
-    lens, H, d, ps, sb, Nq = [49], 2, 128, 16, 16, 4
+    lens, H, ps, sb, Nq = [49], 2, 16, 16, 4
     kc, ks, vc, vs, table = cache8.build(rng, lens, ps, sb, H, d)
     q = torch.from_numpy(rng.standard_normal((1, Nq, Hq, d))).cuda().bfloat16()
     clean = cache8.to_device(kc, ks, vc, vs, table, lens)
     o0, l0 = fa.decode_paged_fp8(q, clean[0], clean[2], clean[1], clean[3], clean[4], clean[5])
-    vc[table[0, 2], 15, 0, 77] = 0x7F  # token 47, K/V head 0, one column
+    vc[table[0, 2], 15, 0, 57] = 0x7F  # token 47, K/V head 0, one column
     vs[table[0, 3], 1, 0] = np.nan     # token 48, K/V head 1
     dev = cache8.to_device(kc, ks, vc, vs, table, lens)
     o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5])
     want = torch.zeros(1, Nq, Hq, d, dtype=torch.bool, device="cuda")
-    want[0, 2:, :Hq // 2, 77] = True
+    want[0, 2:, :Hq // 2, 57] = True
     want[0, 3, Hq // 2:] = True
     assert torch.equal(torch.isnan(o), want)
     assert torch.equal(o[~want], o0[~want]) and torch.equal(lse, l0)
