@@ -23,16 +23,18 @@
 // One CTA per SM: TMA producer, MMA issuer, four warpgroups that share the query rows of every chunk
 // (two that take the chunks in turn, with 64 scores and 64 sums in registers and a merge at each
 // unit's end: 385 us for 40 rows; two that share the rows: 113 us; four in two pairs that take the
-// chunks in turn: 118 us; four: 101 us).  Scores and weights have two buffers, so the products of one
+// chunks in turn: 118 us; four: 99 us).  Scores and weights have two buffers, so the products of one
 // chunk run under the weights of the next, and the scores of the chunk after that are issued before
 // this one's sums (2 % faster than after).  K and V are slots of their own in the ring, since a K
 // slot is free as soon as its product is done.
 //
-// Bound by the weights: per chunk each warp spends about 180 instructions that do not depend on its
+// Bound by the weights: per chunk each warp spends about 170 instructions that do not depend on its
 // rows (waits, scales, a vote, loads) and 14 a row, at 54 % of the issue slots; the products take 19 %
 // of the tensor pipe, and the vote on new references 9 % of the time.  8 sequences of up to 32K rows,
-// 5 new tokens, 64 query and 8 K/V heads (40 rows): 101 us for 311 MB, 3.1 TB/s, where the kernel of
-// products in registers took 211 us.
+// 5 new tokens, 64 query and 8 K/V heads (40 rows): 99 us for 311 MB, 3.2 TB/s, where the kernel of
+// products in registers took 211 us.  (One barrier for the scales of K and V, scales that are not finite
+// found by the vote, one arrival a warp: 102 -> 99 us.  Three buffers of weights, so that nothing waits
+// for the product before the last, take two slots from the ring: 100.)
 #pragma once
 
 #include "fa_decode_fp8.cuh"
@@ -109,14 +111,14 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(full + s, 1 + 8);  // the producer's expect_tx, and eight lanes' scales
+      mbar_init(full + s, s & 1 ? 1 + 16 : 1);  // the producer's expect_tx; with V, sixteen lanes' scales
       mbar_init(empty + s, 1);
     }
-    mbar_init(q_full, C::kWork);
+    mbar_init(q_full, C::kWork / 32);
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full + w, 1);
-      mbar_init(s_empty + w, C::kWork);
-      mbar_init(p_full + w, C::kWork);
+      mbar_init(s_empty + w, C::kWork / 32);
+      mbar_init(p_full + w, C::kWork / 32);
       mbar_init(p_done + w, 1);
     }
     mbar_init(all_done, 1);
@@ -178,11 +180,11 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
                                  kvh, full + slot, pol);
               const float* src = p.scales[which] + (((long long)page * p.Hkv + kvh) << nb_shift) + (r >> p.sb_shift);
               asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(src) : "memory");
-              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + slot))
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full + 2 * pair + 1))
                            : "memory");
             } else {
               *to = 0.f;
-              mbar_arrive(full + slot);
+              mbar_arrive(full + 2 * pair + 1);
             }
             if (++pair == C::kPairs) pair = 0, phase ^= 1u;
             entry = (entry + 1) % C::kScales;
@@ -278,6 +280,12 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         for (int k = tid; k < p.units; k += C::kWork) p.ws_desc[b * p.units + k] = make_int4(0, 0, 0, 0);
     }
 
+    // one arrival for the warp
+    auto arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+
     while (walk.next(p, seg)) {
       const int kvh = seg.unit / p.tiles, tile = seg.unit - kvh * p.tiles;
       // this group's query rows: columns [col0, col0 + 8 blocks) of the tile
@@ -342,7 +350,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       asm volatile("bar.sync 1, %0;" ::"n"(C::kWork) : "memory");
-      mbar_arrive(q_full);
+      arrive(q_full);
 
       constexpr int N = C::kCols;
       uint64_t l2[N / 2];  // sums of p, two rows a register pair
@@ -353,27 +361,16 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
       for (int c = seg.c0; c < seg.c1; ++c, ++n) {
         const uint32_t buf = n & 1u, use = n >> 1;
         // the chunk's scores, scales, and V rows (which may be cleaned here)
-        if (ok) ok = mbar_wait(s_full + buf, use & 1u) && mbar_wait(full + 2 * pair, kphase) &&
-                     mbar_wait(full + 2 * pair + 1, kphase);
+        if (ok) ok = mbar_wait(s_full + buf, use & 1u) && mbar_wait(full + 2 * pair + 1, kphase);
         __syncwarp();
         tc_fence_after();
         const int j = c * kDec8Keys + row;
         const float sk = sm_scale[entry * 16 + (row >> 4)];
         float sv = sm_scale[entry * 16 + 8 + (row >> 4)];
         const bool partly = (c + 1) * kDec8Keys > first_limit, fresh = c == seg.c0;
-        if (__any_sync(0xffffffffu, !(sv < INFINITY))) {
-          // (rare) a scale that is not finite makes NaN of what sees its rows, and of nothing else
-          const bool bad = !(sv < INFINITY);
-          if (w == 0)
-#pragma unroll 1
-            for (int r = 0; r < rows; ++r)
-              if (bad && j < sm_limit[r])
-                for (int k = 0; k < 4; ++k) atomicOr(sm_nan + r * 4 + k, 0xFFFFFFFFu);
-          if (bad) sv = 0.f;
-          __syncwarp();
-        }
         // (a zero scale weighs nothing; the bound keeps p = 2^(t - reference) finite)
-        const float lsv = fmaxf(__log2f(sv), -100.f);
+        float lsv = __log2f(sv);
+        lsv = lsv < -100.f ? -100.f : lsv;  // (NaN stays, for the vote)
         float s[N];
 #pragma unroll
         for (int b = 0; b < N / 8; ++b)
@@ -381,7 +378,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
             tmem_ld8(tmem + C::kColS + buf * R + col0 + b * 8 + lanes, reinterpret_cast<uint32_t(&)[8]>(s[b * 8]));
         tmem_wait_ld();
         tc_fence_before();
-        mbar_arrive(s_empty + buf);
+        arrive(s_empty + buf);
         // exponents t - reference, and whether one is past the top
         float most[N / 8];
         bool past_top = false;
@@ -407,9 +404,20 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
           if (b < blocks)
 #pragma unroll
             for (int x = b * 8; x < b * 8 + 8; x += 2) most[b] = fmax3(most[b], s[x], s[x + 1]);
-          past_top |= most[b] + lsv > kTcTop;
+          past_top |= !(most[b] + lsv <= kTcTop);
         }
         if (group_any(2 + w, fresh || past_top)) {
+          if (__any_sync(0xffffffffu, !(sv < INFINITY))) {
+            // (rare) a scale that is not finite makes NaN of what sees its rows, and of nothing else
+            const bool bad = !(sv < INFINITY);
+            if (w == 0)
+#pragma unroll 1
+              for (int r = 0; r < rows; ++r)
+                if (bad && j < sm_limit[r])
+                  for (int k = 0; k < 4; ++k) atomicOr(sm_nan + r * 4 + k, 0xFFFFFFFFu);
+            if (bad) sv = 0.f, lsv = -100.f;
+            __syncwarp();
+          }
           // new references: the largest exponent of each row over the group's threads; a warp looks
           // at the blocks in which it has one past the top
 #pragma unroll
@@ -540,7 +548,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
           }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(p_full + buf);
+        arrive(p_full + buf);
         if (++pair == C::kPairs) pair = 0, kphase ^= 1u;
         entry = (entry + 1) % C::kScales;
       }
