@@ -324,7 +324,7 @@ FA_EXPORT fa_status fa_cache_append_fp8(const void* k, const void* v, const int3
  * attends to it, and of nothing else.  An entry of the table outside [0, num_pages) is
  * read as page 0 and recorded (FA_ERR_INVALID_ARG from fa_last_device_error).
  * The stored values are exact in the products and all sums are fp32.  P times the V scale is
- * rounded to fp16 relative to its largest value so far; for more than 16 query rows of a K/V head
+ * rounded to fp16 relative to a value within 2^6 of its largest; for more than 16 query rows of a K/V head
  * (Nq * Hq / Hkv) and d = 128 it is the sum of two e4m3 terms instead (8 bits, like bf16; 2^-16 of
  * the largest value at the least), and so is q (2^-17 of a row's largest element at the least);
  * V scales outside 2^-100 .. 2^100 lose accuracy there.  o is rounded to bf16.
