@@ -662,3 +662,42 @@ def test_captured_after_copies_and_joined_streams():
         for a, b in zip(out, w):
             assert torch.equal(a, b)
     assert torch.isfinite(out[0].float()).all() and fa.fa_last_device_error() == fa.FA_OK
+
+
+@pytest.mark.parametrize("Hq,Nq", [(8, 1), (32, 1), (64, 3)], ids=["1row", "4rows", "24rows"])
+def test_calls_back_to_back_repeat_bit_for_bit(Hq, Nq):
+    """A chain in which every call reads what the one before wrote, many times without a pause: a call
+    that began before its inputs were complete would differ."""
+    B, H, d, ps, sb, maxp = 6, 8, 128, 16, 16, 40
+    P = B * maxp + 8
+    lens0 = torch.tensor([600, 1, 333, 17, 500, 64], dtype=torch.int32, device="cuda")
+    total = int(lens0.sum())
+    cu = torch.cat([torch.zeros(1, dtype=torch.int32, device="cuda"), lens0.cumsum(0).int()])
+    pos = torch.cat([torch.arange(n) for n in lens0.tolist()]).int().cuda()
+    k0, v0 = (torch.randn(total, H, d, device="cuda").bfloat16() for _ in range(2))
+    q0 = torch.randn(B * Nq, Hq, d, device="cuda").bfloat16()
+    qpos = (lens0[:, None] - Nq + torch.arange(Nq, device="cuda").int()).reshape(-1).int().contiguous()
+    freqs = fa.rope_frequencies(d)
+    table = torch.randperm(P, device="cuda")[:B * maxp].int().view(B, maxp)
+    parent = torch.tensor([5, 0, 0, 2, 4, 0], dtype=torch.int32, device="cuda")
+    pages = [torch.zeros(P, ps, H, d, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.zeros(P, H, ps // sb, device="cuda") for _ in range(2)]
+    first = None
+    for turn in range(60):
+        for t in (*pages, *scales):
+            t.view(torch.uint8).zero_()
+        k, _ = fa.rope(k0, None, freqs, pos)
+        q, _ = fa.rope(q0, None, freqs, qpos)
+        fa.cache_append_fp8(k, v0, *pages, *scales, table, lens0, cu)
+        q = q.view(B, Nq, Hq, d)
+        o, lse = fa.decode_paged_fp8(q, *pages, *scales, table, lens0)
+        t1, l1, free, n = fa.pages_fork([*pages, *scales], table, lens0, parent, ps)
+        t2, live = fa.pages_compact([*pages, *scales], t1, l1, ps)
+        o2, lse2 = fa.decode_paged_fp8(q, *pages, *scales, t2, l1)
+        got = [x.clone() for x in (o, lse, t1, l1, free, n, t2, live, o2, lse2)]
+        if first is None:
+            first = got
+        for a, b in zip(got, first):
+            assert torch.equal(a.view(torch.uint8) if a.is_floating_point() else a,
+                               b.view(torch.uint8) if b.is_floating_point() else b), turn
+    assert fa.fa_last_device_error() == fa.FA_OK
