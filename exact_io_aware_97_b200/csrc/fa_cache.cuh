@@ -9,8 +9,8 @@
 // token ends as if filled at once, up to those bits.  A row that is not finite makes the scale
 // of its block NaN.
 //
-// Bound by HBM for prompts (2 bytes read and 1 written per element; 67.6K rows of 8 heads, d = 128: 80
-// us, 5.6 TB/s of the copy's 6.55) and by the chain of dependent loads (lengths, block table, scale,
+// Bound by HBM for prompts (2 bytes read and 1 written per element; 67.6K rows of 8 heads, d = 128: 78
+// us, 5.7 TB/s of the copy's 6.55) and by the chain of dependent loads (lengths, block table, scale,
 // rows) for single tokens.  A unit is one (block, head): its warps hold the rows of K and V in
 // registers, so a row is read once for the maximum and the rounding alike.
 #pragma once
@@ -181,7 +181,9 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, const AppendU
   float s[2];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    if (wpu > 1)
+    if (wpu == kAppendCta)
+      top[w] = __reduce_max_sync(0xffffffffu, sm_max[w][lane & (kAppendCta - 1)]);
+    else if (wpu > 1)
       for (int k = 0; k < wpu; ++k) top[w] = max(top[w], sm_max[w][t.warp0 + k]);
     const float nan = __uint_as_float(0x7FC00000u);
     s[w] = top[w] >= 0x7F800000u ? nan : top[w] == 0u ? 0.f : pow2_scale(__uint_as_float(top[w]));
@@ -193,10 +195,13 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, const AppendU
     for (int w = 0; w < 2; ++w) {
       uint8_t* const base = p.pages[w] + ((long long)t.page * ps + row_in_page + r0) * pitch + t.head * D + col;
       uint8_t* dst = base;
-      if ((__float_as_uint(s[w]) & 0x7FFFFFu) == 0u) {
-        // x / s is x * (1 / s): both round the same value once
-        const __nv_bfloat162 inv = __float2bfloat162_rn(s[w] == 0.f ? 0.f : __fdiv_rn(1.f, s[w]));
-        const uint32_t keep = s[w] == 0.f ? 0u : 0xFFFFFFFFu;
+      const uint32_t bits = __float_as_uint(s[w]);
+      if ((bits & 0x7FFFFFu) == 0u && bits <= 0x7E800000u) {  // 0 or a power of two up to 2^126
+        // x / s is x * (1 / s): both round the same value once.  (Scale 0: all x are 0, and so are the
+        // codes, without a sign.)
+        const uint32_t up = (0x7F000000u - bits) >> 16, keep = bits ? 0xFFFFFFFFu : 0u;
+        const uint32_t inv2 = up | up << 16;
+        const __nv_bfloat162 inv = *reinterpret_cast<const __nv_bfloat162*>(&inv2);
 #pragma unroll
         for (int k = 0; k < kPass; ++k, dst += kRows * pitch) {
           const uint4 v = x[w][k];
