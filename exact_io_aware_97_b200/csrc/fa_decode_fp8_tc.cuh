@@ -456,11 +456,12 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
                 const int r = b * 8 + x;
                 up[x] = up[x] > least ? up[x] - kTcStart : 0.f;
                 s[r] -= up[x];
-                up[x] = ex2_approx(-up[x]);
               }
+              if (!fresh) {  // (a first reference may lie anywhere: no factor for sums of 0, which may be infinite)
 #pragma unroll
-              for (int x = 0; x < 8; x += 2) l2[b * 4 + x / 2] = f2_mul(l2[b * 4 + x / 2], f2(up[x], up[x + 1]));
-              if (!fresh) {
+                for (int x = 0; x < 8; ++x) up[x] = ex2_approx(-up[x]);
+#pragma unroll
+                for (int x = 0; x < 8; x += 2) l2[b * 4 + x / 2] = f2_mul(l2[b * 4 + x / 2], f2(up[x], up[x + 1]));
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                   float o[8];
