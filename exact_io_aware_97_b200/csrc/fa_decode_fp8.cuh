@@ -828,8 +828,10 @@ __global__ void __launch_bounds__(256) fa_decode_fp8_combine_kernel(const Dec8Pa
     for (int s = s0; s < parts; s += step) {
       const long long at = first + s * pitch + (s ? 0 : odd);
       const float2 ml = p.ws_ml[at];
-      const float e = ex2_approx(ml.x - M);
-      L += e * ml.y;
+      const float d = ml.x - M, e = ex2_approx(d);
+      // l of a part whose V scales are far smaller is not: in two halves where the factor is too small for fp32
+      const float h = ex2_approx(0.5f * d);
+      L += d < -100.f ? ml.y * h * h : e * ml.y;
       if constexpr (V == 4) {
         const float4 f = *reinterpret_cast<const float4*>(p.ws_acc + at * D + lane * 4);
         a[0] += e * f.x, a[1] += e * f.y, a[2] += e * f.z, a[3] += e * f.w;

@@ -15,7 +15,9 @@
 // grow to 2^8.5; only a score that goes beyond raises the reference and rescales the sums, of its
 // block of eight rows.  (From 2^4: 124 us for 40 rows instead of 113, o off by 1.67e-3 of its norm
 // where a bf16 rounding alone gives 1.65e-3; from 2^2: 1.73e-3; from 2^-2: 109 us, 2.55e-3.)  l sums
-// p in fp32.  Both p and w are relative to the one reference, which follows t + log2(sv).
+// p in fp32.  Both p and w are relative to the one reference, which follows t + log2(sv): p may then be
+// as far from 1 as the V scales are from one another (2^-100 .. 2^108 for scales 2^-100 .. 2^100), and
+// moves of l by more than fp32's range are taken in two halves.
 //
 // Warps stay together: whatever lanes do alone ends in a __syncwarp before the next barrier or TMEM
 // access, which are for whole warps.
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         const float sk = sm_scale[entry * 16 + (row >> 4)];
         float sv = sm_scale[entry * 16 + 8 + (row >> 4)];
         const bool partly = (c + 1) * kDec8Keys > first_limit, fresh = c == seg.c0;
-        // (a zero scale weighs nothing; the bound keeps p = 2^(t - reference) finite)
+        // (a zero scale weighs nothing; the bound keeps p = 2^(t - reference), up to 2^8.5 / sv, finite)
         float lsv = __log2f(sv);
         lsv = lsv < -100.f ? -100.f : lsv;  // (NaN stays, for the vote)
         float s[N];
@@ -458,10 +460,18 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
                 s[r] -= up[x];
               }
               if (!fresh) {  // (a first reference may lie anywhere: no factor for sums of 0, which may be infinite)
+                // l holds every key whatever its V scale, so a factor too small for fp32 is taken in two halves
+                const bool far = any > 100.f;
+#pragma unroll
+                for (int x = 0; x < 8; x += 2) {
+                  const float k = far ? -0.5f : -1.f;
+                  const uint64_t down = f2(ex2_approx(k * up[x]), ex2_approx(k * up[x + 1]));
+                  uint64_t& l = l2[b * 4 + x / 2];
+                  l = f2_mul(l, down);
+                  if (far) l = f2_mul(l, down);
+                }
 #pragma unroll
                 for (int x = 0; x < 8; ++x) up[x] = ex2_approx(-up[x]);
-#pragma unroll
-                for (int x = 0; x < 8; x += 2) l2[b * 4 + x / 2] = f2_mul(l2[b * 4 + x / 2], f2(up[x], up[x + 1]));
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                   float o[8];
