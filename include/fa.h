@@ -325,8 +325,9 @@ FA_EXPORT fa_status fa_cache_append_fp8(const void* k, const void* v, const int3
  * read as page 0 and recorded (FA_ERR_INVALID_ARG from fa_last_device_error).
  * The stored values are exact in the products and all sums are fp32.  P times the V scale is
  * rounded to fp16 relative to a value within 2^6 of its largest; for more than 16 query rows of a K/V head
- * (Nq * Hq / Hkv) and d = 128 it is the sum of two e4m3 terms instead (8 bits, like bf16; 2^-16 of
- * the largest value at the least), and so is q (2^-17 of a row's largest element at the least);
+ * (Nq * Hq / Hkv) and d = 128 it is the sum of two e4m3 terms instead (8 bits, like bf16, in steps of
+ * 2^-15 of the largest value at the least; values between two such steps go up or down in proportion, so
+ * that the sum of many is kept), and so is q (2^-17 of a row's largest element at the least);
  * V scales outside 2^-100 .. 2^100 lose accuracy there.  o is rounded to bf16.
  * Hq a multiple of Hkv; d 64 or 128; sizes as in fa_cache_append_fp8, and B * Hkv *
  * max_pages_per_seq * page_size * (Nq * (Hq / Hkv) / 64, rounded up) < 2^37 (FA_ERR_UNSUPPORTED
