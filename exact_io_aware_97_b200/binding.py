@@ -605,6 +605,30 @@ def _elsewhere(idx: int) -> bool:
     return idx != torch._C._cuda_getDevice()
 
 
+def _other_stream(stream, t):
+    """None, or the context of a launch on `stream` that is not torch's current stream of t's device:
+    what the call allocates then belongs to `stream`, so that its memory is not given out again
+    while kernels there use it."""
+    import torch
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if handle == torch.cuda.current_stream(t.device).cuda_stream:
+        return None
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, t.device) if handle else torch.cuda.default_stream(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream: expected one of {t.device}, got one of {stream.device}")
+    return torch.cuda.stream(stream)
+
+
+def _results_from(results):
+    """Results that were allocated on another stream, for use on the current one too."""
+    import torch
+    for r in results:
+        if r is not None:
+            r.record_stream(torch.cuda.current_stream(r.device))
+    return results
+
+
 def _dense(**tensors) -> None:
     for what, t in tensors.items():
         if t is not None and not t.is_contiguous():
@@ -684,6 +708,12 @@ def _rope(q, k, freqs, positions, interleaved, amplitude, q_out, k_out, stream, 
     if _elsewhere(_home(q, k, freqs, positions, q_out, k_out)):
         with torch.cuda.device(q.device):
             return _rope(q, k, freqs, positions, interleaved, amplitude, q_out, k_out, stream, backward)
+    if stream is not None:
+        other = _other_stream(stream, q)
+        if other:
+            with other:
+                done = _rope(q, k, freqs, positions, interleaved, amplitude, q_out, k_out, None, backward)
+            return _results_from(done)
     # like the input where that is dense; empty_like would keep the strides of a slice's dimensions
     dense = Hq * d
     sq = syq = dense
@@ -811,6 +841,13 @@ def decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens
         with torch.cuda.device(q.device):
             return decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, scale, out, lse,
                                     workspace, stream)
+    if stream is not None:
+        other = _other_stream(stream, q)
+        if other:
+            with other:
+                done = decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seqlens, scale, out, lse,
+                                        workspace)
+            return _results_from(done)
     if not q.is_contiguous():
         raise ValueError(f"q: expected a contiguous tensor, got strides {tuple(q.stride())} for shape {tuple(shape)}")
     if out is not None or lse is not None or workspace is not None:
@@ -866,6 +903,12 @@ def pages_fork(pools, block_table, seqlens, parent, page_size, num_pages=None, w
     if _elsewhere(_home(block_table, seqlens, parent, workspace, *pools)):
         with torch.cuda.device(block_table.device):
             return pages_fork(pools, block_table, seqlens, parent, page_size, num_pages, workspace, stream)
+    if stream is not None:
+        other = _other_stream(stream, block_table)
+        if other:
+            with other:
+                done = pages_fork(pools, block_table, seqlens, parent, page_size, num_pages, workspace)
+            return _results_from(done)
     lib = load()
     arr = _pool_array(pools, num_pages)
     # one allocation for the four results
@@ -891,6 +934,12 @@ def pages_compact(pools, block_table, seqlens, page_size, num_pages=None, worksp
     if _elsewhere(_home(block_table, seqlens, workspace, *pools)):
         with torch.cuda.device(block_table.device):
             return pages_compact(pools, block_table, seqlens, page_size, num_pages, workspace, stream)
+    if stream is not None:
+        other = _other_stream(stream, block_table)
+        if other:
+            with other:
+                done = pages_compact(pools, block_table, seqlens, page_size, num_pages, workspace)
+            return _results_from(done)
     lib = load()
     arr = _pool_array(pools, num_pages)
     table, n_live = torch.empty_like(block_table), block_table.new_empty(1)
