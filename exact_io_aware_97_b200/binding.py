@@ -387,6 +387,33 @@ def fa_device_sm_count() -> int:
 
 
 # ------------------------------------------------------------------ tensor-level helpers
+# (a `stream` argument is a torch stream or a raw handle; a call with one runs as under torch.cuda.stream(stream))
+def _other_stream(stream, t):
+    """None, or the context of a launch on `stream` that is not torch's current stream of t's device:
+    what the call allocates then belongs to `stream`, so that its memory is not given out again
+    while kernels there use it."""
+    import torch
+    if not t.is_cuda:
+        return None  # refused where its address is taken
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if handle == torch.cuda.current_stream(t.device).cuda_stream:
+        return None
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, t.device) if handle else torch.cuda.default_stream(t.device)
+    if stream.device != t.device:
+        raise ValueError(f"stream: expected one of {t.device}, got one of {stream.device}")
+    return torch.cuda.stream(stream)
+
+
+def _results_from(results):
+    """Results that were allocated on another stream, for use on the current one too."""
+    import torch
+    for r in results:
+        if r is not None:
+            r.record_stream(torch.cuda.current_stream(r.device))
+    return results
+
+
 def forward(q, k, v, causal=False, scale=None, cu_seqlens=None, out=None, lse=None, workspace=None, stream=None,
             tf32=False):
     """O, lse for q [B,Nq,Hq,d] / k,v [B,Nk,Hkv,d] (or packed [total,H,d] with cu_seqlens).
@@ -419,6 +446,12 @@ def forward(q, k, v, causal=False, scale=None, cu_seqlens=None, out=None, lse=No
         scale = d ** -0.5
     _expect(out, q.shape, "torch.bfloat16" if in_dtype == FA_BF16 else "torch.float32", "out")
     _expect(lse, lse_shape, "torch.float32", "lse")
+    if stream is not None:
+        other = _other_stream(stream, q)
+        if other:
+            with other:
+                done = forward(q, k, v, causal, scale, cu_seqlens, out, lse, workspace, None, tf32)
+            return _results_from(done)
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16 if in_dtype == FA_BF16 else torch.float32, device=q.device)
     if lse is None:
@@ -448,6 +481,12 @@ def decode(q, kcache, vcache, seqlens=None, scale=None, split_len=1024, out=None
         scale = d ** -0.5
     _expect(out, (B, Hq, d), "torch.bfloat16", "out")
     _expect(lse, (B, Hq), "torch.float32", "lse")
+    if stream is not None:
+        other = _other_stream(stream, q)
+        if other:
+            with other:
+                done = decode(q, kcache, vcache, seqlens, scale, split_len, out, lse, workspace)
+            return _results_from(done)
     if out is None:
         out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=q.device)
     if lse is None:
@@ -482,6 +521,13 @@ def decode_paged(q, k_pages, v_pages, block_table, seqlens, scale=None, split_le
         scale = d ** -0.5
     _expect(out, (B, Hq, d), "torch.bfloat16", "out")
     _expect(lse, (B, Hq), "torch.float32", "lse")
+    if stream is not None:
+        other = _other_stream(stream, q)
+        if other:
+            with other:
+                done = decode_paged(q, k_pages, v_pages, block_table, seqlens, scale, split_len, out, lse,
+                                    workspace)
+            return _results_from(done)
     if out is None:
         out = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=q.device)
     if lse is None:
@@ -509,6 +555,12 @@ def backward(q, k, v, o, lse, dout, causal=False, scale=None, workspace=None, st
     _expect(lse, (B, Hq, Nq), "torch.float32", "lse")
     if scale is None:
         scale = d ** -0.5
+    if stream is not None:
+        other = _other_stream(stream, q)
+        if other:
+            with other:
+                done = backward(q, k, v, o, lse, dout, causal, scale, workspace)
+            return _results_from(done)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ws_bytes = fa_bwd_workspace_size(B, Hq, Nq, d)
     if workspace is None:
@@ -536,6 +588,12 @@ def backward_varlen(q, k, v, o, lse, dout, cu_seqlens, causal=False, scale=None,
     _expect(lse, (Hq, total), "torch.float32", "lse")
     if scale is None:
         scale = d ** -0.5
+    if stream is not None:
+        other = _other_stream(stream, q)
+        if other:
+            with other:
+                done = backward_varlen(q, k, v, o, lse, dout, cu_seqlens, causal, scale, workspace)
+            return _results_from(done)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ws_bytes = fa_bwd_varlen_workspace_size(B, Hq, total, d)
     if workspace is None:
@@ -603,30 +661,6 @@ def _home(first, *others) -> int:
 def _elsewhere(idx: int) -> bool:
     import torch
     return idx != torch._C._cuda_getDevice()
-
-
-def _other_stream(stream, t):
-    """None, or the context of a launch on `stream` that is not torch's current stream of t's device:
-    what the call allocates then belongs to `stream`, so that its memory is not given out again
-    while kernels there use it."""
-    import torch
-    handle = stream if isinstance(stream, int) else stream.cuda_stream
-    if handle == torch.cuda.current_stream(t.device).cuda_stream:
-        return None
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(handle, t.device) if handle else torch.cuda.default_stream(t.device)
-    if stream.device != t.device:
-        raise ValueError(f"stream: expected one of {t.device}, got one of {stream.device}")
-    return torch.cuda.stream(stream)
-
-
-def _results_from(results):
-    """Results that were allocated on another stream, for use on the current one too."""
-    import torch
-    for r in results:
-        if r is not None:
-            r.record_stream(torch.cuda.current_stream(r.device))
-    return results
 
 
 def _dense(**tensors) -> None:

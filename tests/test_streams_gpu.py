@@ -53,10 +53,34 @@ def _inputs():
                                                               stream=stream),
         "rope": lambda stream=None: fa.rope(q, None, freqs, stream=stream)[:1],
         "rope_backward": lambda stream=None: fa.rope_backward(q, None, freqs, stream=stream)[:1],
+        **_attention(),
     }
 
 
-@pytest.mark.parametrize("what", ["decode_paged_fp8", "pages_fork", "pages_compact", "rope", "rope_backward"])
+def _attention():
+    g = torch.Generator(device="cuda").manual_seed(6402)
+    q, k, v, dout = (torch.randn(2, 200, h, 64, generator=g, device="cuda").bfloat16() for h in (4, 2, 2, 4))
+    cu = torch.tensor([0, 150, 200], dtype=torch.int32, device="cuda")
+    o, lse = fa.forward(q, k, v, causal=True)
+    ov, lv = fa.forward(q[0], k[0], v[0], causal=True, cu_seqlens=cu)
+    lens = torch.tensor([200, 77], dtype=torch.int32, device="cuda")
+    pool = [x.reshape(-1, 16, 2, 64)[:24].contiguous() for x in (k, v)]
+    table = torch.arange(24, dtype=torch.int32, device="cuda").view(2, 12)
+    plens = torch.tensor([190, 5], dtype=torch.int32, device="cuda")
+    q32, k32, v32 = (x.float() for x in (q, k, v))
+    q1 = q[:, 0].contiguous()
+    return {
+        "forward": lambda stream=None: fa.forward(q32, k32, v32, causal=True, stream=stream),
+        "backward": lambda stream=None: fa.backward(q, k, v, o, lse, dout, causal=True, stream=stream)[1:],
+        "backward_varlen": lambda stream=None: fa.backward_varlen(q[0], k[0], v[0], ov, lv, dout[0], cu, causal=True,
+                                                                  stream=stream)[1:],
+        "decode": lambda stream=None: fa.decode(q1, k, v, lens, split_len=64, stream=stream),
+        "decode_paged": lambda stream=None: fa.decode_paged(q1, *pool, table, plens, split_len=64, stream=stream),
+    }
+
+
+@pytest.mark.parametrize("what", ["decode_paged_fp8", "pages_fork", "pages_compact", "rope", "rope_backward", "forward",
+                                  "backward", "backward_varlen", "decode", "decode_paged"])
 @pytest.mark.parametrize("form", ["stream", "handle"])
 def test_memory_belongs_to_the_stream_of_the_call(what, form, monkeypatch):
     call = _inputs()[what]
