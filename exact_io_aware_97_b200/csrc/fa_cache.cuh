@@ -60,7 +60,7 @@ __device__ __forceinline__ int append_find(const int32_t* cu, int B, int sb_shif
   int lo = 0, hi = B;  // slot start of lo is <= u; that of hi (if < B) is > u
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if ((max(__ldg(cu + mid), 0) >> sb_shift) + 2 * mid <= u) lo = mid;
+    if ((max(load_in(cu + mid), 0) >> sb_shift) + 2 * mid <= u) lo = mid;
     else hi = mid;
   }
   return lo;
@@ -128,7 +128,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, const AppendU
 #pragma unroll
       for (int k = 0; k < kPass; ++k, src += kRows * pitch) {
         if (!INSIDE) x[w][k] = make_uint4(0u, 0u, 0u, 0u);
-        if (alive && is_new(k)) x[w][k] = __ldg(reinterpret_cast<const uint4*>(src));
+        if (alive && is_new(k)) x[w][k] = load_in(reinterpret_cast<const uint4*>(src));
       }
     }
   };
@@ -257,16 +257,16 @@ __global__ void __launch_bounds__(kAppendCta * 32, 4) fa_cache_append_kernel(con
   const int wpu = append_warps<D>(p.sb_shift), upc = kAppendCta / wpu;  // warps of a unit, heads of a CTA
 
   if (p.cu && blockIdx.x == 0 && blockIdx.y == 0) {
-    bool bad = threadIdx.x == 0 && (__ldg(p.cu) < 0 || __ldg(p.cu + p.B) > p.total);
-    for (int b = threadIdx.x; b < p.B; b += blockDim.x) bad |= __ldg(p.cu + b) > __ldg(p.cu + b + 1);
+    bool bad = threadIdx.x == 0 && (load_in(p.cu) < 0 || load_in(p.cu + p.B) > p.total);
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) bad |= load_in(p.cu + b) > load_in(p.cu + b + 1);
     if (bad) atomicOr(&g_error_word, kErrBadSeqlens);
   }
   const int u = blockIdx.x;
   const int b = p.cu ? append_find(p.cu, p.B, p.sb_shift, u) : u;
-  const int start = p.cu ? __ldg(p.cu + b) : b;
-  const int end = p.cu ? __ldg(p.cu + b + 1) : b + 1;
+  const int start = p.cu ? load_in(p.cu + b) : b;
+  const int end = p.cu ? load_in(p.cu + b + 1) : b + 1;
   const int idx = p.cu ? u - ((max(start, 0) >> p.sb_shift) + 2 * b) : 0;
-  const int n = end - start, len = __ldg(p.seqlens + b);
+  const int n = end - start, len = load_in(p.seqlens + b);
   // a slot before the first sequence's (rows before cu[0] belong to none), a sequence without new
   // rows, or one whose offsets or length cannot be used
   if (idx < 0 || start < 0 || end > p.total || n <= 0) return;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kAppendCta * 32, 4) fa_cache_append_kernel(con
   t.len = len;
   t.blk0 = ((old >> p.sb_shift) + idx) << p.sb_shift;
   if (t.blk0 >= len) return;
-  t.page = __ldg(p.block_table + (long long)b * p.max_pages + (t.blk0 >> p.page_shift));
+  t.page = load_in(p.block_table + (long long)b * p.max_pages + (t.blk0 >> p.page_shift));
   t.head = blockIdx.y * upc + warp / wpu;
   t.warp0 = warp / wpu * wpu;
   if (t.blk0 >= old && t.blk0 + (1 << p.sb_shift) <= len)

@@ -102,7 +102,7 @@ struct Dec8Seg {
   int c0, c1;          // chunks [c0, c1)
 };
 
-__device__ __forceinline__ int dec8_len(const Dec8Params& p, int b) { return min(max(__ldg(p.seqlens + b), 0), p.cap); }
+__device__ __forceinline__ int dec8_len(const Dec8Params& p, int b) { return min(max(load_in(p.seqlens + b), 0), p.cap); }
 
 // Positions count chunks and, before each unit's first, p.lead more that stand for what a unit costs
 // on its own (its queries, the start and the end of its pipeline), so that shares of many short units
@@ -348,11 +348,11 @@ __device__ __forceinline__ void dec8_produce(const CUtensorMap& tmK, const CUten
     const int kvh0 = (seg.unit / p.tiles) << p.hs;
     const int32_t* bt = p.block_table + (long long)seg.b * p.max_pages;
     int tok = seg.c0 * chunk + ro;
-    int page_next = tok < seg.len ? __ldg(bt + (tok >> p.page_shift)) : 0;
+    int page_next = tok < seg.len ? load_in(bt + (tok >> p.page_shift)) : 0;
     for (int c = seg.c0; c < seg.c1; ++c, tok += chunk) {
       int page = page_next;
       const bool here = tok < seg.len;
-      if (c + 1 < seg.c1 && tok + chunk < seg.len) page_next = __ldg(bt + ((tok + chunk) >> p.page_shift));
+      if (c + 1 < seg.c1 && tok + chunk < seg.len) page_next = load_in(bt + ((tok + chunk) >> p.page_shift));
       if (page < 0 || page >= p.num_pages) {
         atomicOr(&g_error_word, kErrBadPage);
         page = 0;
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(Dec8WideCfg<D, MT, RG>::kThreads, Dec8WideCfg<
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
-          x[k] = in ? __ldg(src + 4 * k) : make_uint2(0u, 0u);
+          x[k] = in ? load_in(src + 4 * k) : make_uint2(0u, 0u);
           top = max(max(top, max((x[k].x << 16) & 0x7FFF0000u, x[k].x & 0x7FFF0000u)),
                     max((x[k].y << 16) & 0x7FFF0000u, x[k].y & 0x7FFF0000u));
         }

@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D>::kThreads, Dec8Cfg<D>::kCtas)
       uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        x[k] = in ? __ldg(src + 4 * k) : make_uint2(0u, 0u);
+        x[k] = in ? load_in(src + 4 * k) : make_uint2(0u, 0u);
         top = max(max(top, max((x[k].x << 16) & 0x7FFF0000u, x[k].x & 0x7FFF0000u)),
                   max((x[k].y << 16) & 0x7FFF0000u, x[k].y & 0x7FFF0000u));
       }

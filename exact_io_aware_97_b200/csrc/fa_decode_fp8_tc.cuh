@@ -160,12 +160,12 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
           const int kvh = seg.unit / p.tiles;
           const int32_t* bt = p.block_table + (long long)seg.b * p.max_pages;
           int tok = seg.c0 * kDec8Keys + ro;
-          int page_next = tok < seg.len ? __ldg(bt + (tok >> p.page_shift)) : 0;
+          int page_next = tok < seg.len ? load_in(bt + (tok >> p.page_shift)) : 0;
           for (int c = seg.c0; c < seg.c1; ++c, tok += kDec8Keys) {
             int page = page_next;
             const bool here = tok < seg.len;
             if (c + 1 < seg.c1 && tok + kDec8Keys < seg.len)
-              page_next = __ldg(bt + ((tok + kDec8Keys) >> p.page_shift));
+              page_next = load_in(bt + ((tok + kDec8Keys) >> p.page_shift));
             if (page < 0 || page >= p.num_pages) {
               atomicOr(&g_error_word, kErrBadPage);
               page = 0;
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-          x[k] = in ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+          x[k] = in ? load_in(src + k) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t v = (&x[k].x)[j];

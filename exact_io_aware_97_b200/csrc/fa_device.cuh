@@ -102,6 +102,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
 // A kernel that was launched to come while the stream's last one ends: waits until that has ended and
 // its writes are visible.  Nothing that it wrote is read, and nothing is written, before.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Loads what such a kernel reads, after grid_wait.  (Not through the read-only path, as __ldg: that is for
+// memory that nothing writes while the kernel exists, and this one exists while the last one writes.)
+template <typename T>
+__device__ __forceinline__ T load_in(const T* p) {
+  return *p;
+}
 // Lets a following kernel of that kind come once every block has got here.
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

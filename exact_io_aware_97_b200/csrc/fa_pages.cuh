@@ -56,7 +56,7 @@ struct CompactParams {
 
 // Length of a sequence, or 0 (recorded) for one that the table cannot hold.
 __device__ __forceinline__ int pages_len(const int32_t* lens, int b, int max_pages, int page_shift) {
-  const int n = __ldg(lens + b);
+  const int n = load_in(lens + b);
   if (n < 0 || (long long)n > (long long)max_pages << page_shift) {
     atomicOr(&g_error_word, kErrBadSeqlens);
     return 0;
@@ -65,7 +65,7 @@ __device__ __forceinline__ int pages_len(const int32_t* lens, int b, int max_pag
 }
 
 __device__ __forceinline__ int fork_len(const ForkParams& p, int i, int* parent) {
-  const int b = __ldg(p.parent + i);
+  const int b = load_in(p.parent + i);
   *parent = b;
   if (b < -1 || b >= p.B) {
     atomicOr(&g_error_word, kErrBadSeqlens);
@@ -119,7 +119,7 @@ __device__ __forceinline__ int fork_tail(const ForkParams& p, int i) {
   int b;
   const int n = fork_len(p, i, &b);
   if ((n & ((1 << p.page_shift) - 1)) == 0) return -1;
-  return __ldg(p.table + (long long)b * p.max_pages + (n >> p.page_shift));
+  return load_in(p.table + (long long)b * p.max_pages + (n >> p.page_shift));
 }
 
 __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkParams p) {
@@ -151,7 +151,7 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork
     int page[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      page[j] = t0 + 32 * j < np ? __ldg(p.table + (long long)b * p.max_pages + t0 + 32 * j) : 0;
+      page[j] = t0 + 32 * j < np ? load_in(p.table + (long long)b * p.max_pages + t0 + 32 * j) : 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (t0 + 32 * j < np && pages_ok(page[j], p.num_pages))
@@ -230,7 +230,7 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) fork
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int t = t0 + 32 * j;
-      page[j] = t >= np ? -1 : t == full && k >= 0 ? __ldcg(p.dst + k) : __ldg(from + t);
+      page[j] = t >= np ? -1 : t == full && k >= 0 ? __ldcg(p.dst + k) : load_in(from + t);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -257,7 +257,7 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) comp
     int page[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      page[j] = t0 + 32 * j < np ? __ldg(p.table + (long long)b * p.max_pages + t0 + 32 * j) : 0;
+      page[j] = t0 + 32 * j < np ? load_in(p.table + (long long)b * p.max_pages + t0 + 32 * j) : 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (t0 + 32 * j < np && pages_ok(page[j], p.num_pages)) p.mark[page[j]] = page[j];
@@ -314,7 +314,7 @@ __global__ void __cluster_dims__(kPlanCtas) __launch_bounds__(kPlanThreads) comp
     int page[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      page[j] = t0 + 32 * j < np ? __ldg(p.table + (long long)b * p.max_pages + t0 + 32 * j) : -1;
+      page[j] = t0 + 32 * j < np ? load_in(p.table + (long long)b * p.max_pages + t0 + 32 * j) : -1;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (page[j] >= 0 && page[j] < p.num_pages) page[j] = __ldcg(p.mark + page[j]);
@@ -348,7 +348,7 @@ __device__ __forceinline__ void copy_item(uint8_t* base, unsigned vpp, unsigned 
     to[j] = nullptr;
     if (v < vn) {
       const unsigned k = pages ? v / vpp : 0u, in = pages ? v - k * vpp : v0 + v;
-      const long long from = __ldg(src + k0 + k), at = __ldg(dst + k0 + k);
+      const long long from = load_in(src + k0 + k), at = load_in(dst + k0 + k);
       x[j] = __ldcs(reinterpret_cast<const T*>(base) + from * vpp + in);
       to[j] = reinterpret_cast<T*>(base) + at * vpp + in;
     }
@@ -412,9 +412,9 @@ __global__ void __launch_bounds__(kCopyThreads + 32, 2)
     const unsigned long long page = (unsigned long long)pools.vpp[walk.pool] * 16;
     uint8_t* const base = pools.base[walk.pool] + piece * kBulkBytes;
     bytes[slot] = (unsigned)min(page - piece * kBulkBytes, (unsigned long long)kBulkBytes);
-    to[slot] = base + (unsigned long long)__ldg(dst + k) * page;
+    to[slot] = base + (unsigned long long)load_in(dst + k) * page;
     mbar_arrive_expect_tx(full + slot, bytes[slot]);
-    bulk_load(smem_raw + slot * kBulkBytes, base + (unsigned long long)__ldg(src + k) * page, bytes[slot], full + slot);
+    bulk_load(smem_raw + slot * kBulkBytes, base + (unsigned long long)load_in(src + k) * page, bytes[slot], full + slot);
   };
   // the store of a piece follows its load; the load of the piece five further on follows the store
   // of the one before, once that has read its slot

@@ -35,7 +35,7 @@ struct RopeParams {
 
 // cos and sin of pair i at a position, times the amplitude
 __device__ __forceinline__ float2 rope_cs(const RopeParams& p, int i, double pos) {
-  const double t = pos * __ldg(p.freqs + i) * 0.15915494309189533577;  // turns
+  const double t = pos * load_in(p.freqs + i) * 0.15915494309189533577;  // turns
   float s, c;
   sincospif((float)(2.0 * (t - rint(t))), &s, &c);
   s *= p.amplitude;
@@ -43,7 +43,7 @@ __device__ __forceinline__ float2 rope_cs(const RopeParams& p, int i, double pos
 }
 
 __device__ __forceinline__ double rope_pos(const RopeParams& p, long long row) {
-  return p.positions ? (double)__ldg(p.positions + row) : (double)(row % p.period);
+  return p.positions ? (double)load_in(p.positions + row) : (double)(row % p.period);
 }
 
 __device__ __forceinline__ float rope_load(const float* x) { return *x; }
