@@ -171,10 +171,12 @@ def _bf16(what: str, *ts) -> None:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
-        if not torch.cuda.is_initialized():
+        # the raw handle of torch.cuda.current_stream(), without building the Stream object where torch
+        # has a function for that
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None or not torch.cuda.is_initialized():
             return torch.cuda.current_stream().cuda_stream or None
-        # the raw handle of torch.cuda.current_stream(), without building the Stream object
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) or None
+        return raw(torch.cuda.current_device()) or None
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
@@ -660,7 +662,7 @@ def _home(first, *others) -> int:
 
 def _elsewhere(idx: int) -> bool:
     import torch
-    return idx != torch._C._cuda_getDevice()
+    return idx != torch.cuda.current_device()
 
 
 def _dense(**tensors) -> None:

@@ -144,3 +144,19 @@ def test_the_current_stream_by_its_handle_and_the_default_one():
         assert _owner(o.data_ptr()) == 0
         torch.cuda.synchronize()
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_the_current_stream_without_torchs_raw_handle(monkeypatch):
+    """The function that gives it is not a public one: where torch has none, calls find the stream."""
+    calls = _inputs()
+    want = calls["decode_paged_fp8"]()
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        assert fa._stream(None) == s.cuda_stream
+    s.wait_stream(torch.cuda.current_stream())
+    for n in ("rope", "decode_paged_fp8"):
+        with torch.cuda.stream(s):
+            got = calls[n]()
+        s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
