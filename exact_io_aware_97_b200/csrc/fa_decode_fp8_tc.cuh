@@ -1,46 +1,44 @@
 // Decode attention over an e4m3 paged cache for many query rows: more than 16 of a K/V head (several
 // new tokens, large head groups), d = 128 (sm_100a).
 //
-// The sums of fa_decode_fp8.cuh, with the cache side as M of tcgen05 products on the bytes as they
-// are in the cache: nothing of K or V is widened, and a product costs the same for 17 query rows
-// as for 64.  For a chunk of 128 cache rows and a tile of 64 query rows:
-//   S^T [128 rows of K x 64] = K q^T               (A = K, K-major; q from shared memory)
+// The sums of fa_decode_fp8.cuh, with the cache side as M of tcgen05 products, which cost the same for 17
+// query rows as for 64.  For a chunk of 128 cache rows and a tile of 64 query rows:
+//   S^T [128 rows of K x 64] = K q^T               (A = K's bytes as they are, K-major; q from shared memory)
 //   P^T: thread = cache row, its 64 scores to weights
-//   O^T [128 columns of V x 64] += V^T P^T         (A = V, read column-major; P from shared memory)
-// q and the weights go to e4m3 as the sum of two terms.  q: a row is scaled by a power of two to a
-// largest element in [128, 256); hi = e4m3(q), lo = e4m3(q - hi), so hi + lo holds the 8 bits of a
-// bf16 down to 2^-9 of that scale, 2^-17 of the row's largest element (both terms into one sum).
-// Weights w = p sv: hi = e4m3(w), lo = e4m3(16 (w - hi)), 8 bits down to 2^-14, in two sums (columns
-// 0..63 and 64..127 of one product).  A weight below that lies between two steps of 2^-13: it goes to either,
-// by a nudge of up to half a step that is even over the rows (multiples of the golden ratio), so that many
-// small weights keep their sum.  (To the nearest step, 32K keys each e^-12 of one far above them, a sixth of
-// the sum together, were all rounded to 0, and with e^-11 all up; nudged, o is off by 0.6 % at worst over up
-// to 2M keys, of which bf16 alone takes 0.4.)  The largest w of a row is 2^2 when its reference is set and may
-// grow to 2^8.5; only a score that goes beyond raises the reference and rescales the sums, of its
-// block of eight rows.  (From 2^4: 124 us for 40 rows instead of 113, o off by 1.67e-3 of its norm
-// where a bf16 rounding alone gives 1.65e-3; from 2^2: 1.73e-3; from 2^-2: 109 us, 2.55e-3.)  l sums
-// p in fp32.  Both p and w are relative to the one reference, which follows t + log2(sv): p may then be
+//   O^T [128 columns of V x 64] += V^T P^T         (fp16; A = V widened, read column-major; P from shared memory)
+// q goes to e4m3 as the sum of two terms: a row is scaled by a power of two to a largest element in [128,
+// 256); hi = e4m3(q), lo = e4m3(q - hi), so hi + lo holds the 8 bits of a bf16 down to 2^-9 of that scale,
+// 2^-17 of the row's largest element (both terms into one sum).
+// The weights are p sv 2^6 in fp16 (11 bits).  The largest of a row is 2^8 when its reference is set and may
+// grow to 2^14.5; only a score that goes beyond raises the reference and rescales the sums, of its block of
+// eight rows.  Small weights are in steps of 2^-24, 2^-32 of the largest.  (Weights as two e4m3 terms, with
+// V's bytes as they are, took the same time but had steps of 2^-15 of the largest: where one key outweighed
+// 32K others by e^11, o was off by 45 %, and by several times bf16's rounding wherever a first token took most
+// of the sum.  O is off by 1.65e-3 of its norm on normal data, what bf16 alone gives; it was 1.73e-3.)
+// l sums p in fp32.  Both p and w are relative to the one reference, which follows t + log2(sv): p may then be
 // as far from 1 as the V scales are from one another (2^-100 .. 2^108 for scales 2^-100 .. 2^100), and
 // moves of l by more than fp32's range are taken in two halves.
 //
 // Warps stay together: whatever lanes do alone ends in a __syncwarp before the next barrier or TMEM
 // access, which are for whole warps.
 //
-// One CTA per SM: TMA producer, MMA issuer, four warpgroups that share the query rows of every chunk
-// (two that take the chunks in turn, with 64 scores and 64 sums in registers and a merge at each
-// unit's end: 385 us for 40 rows; two that share the rows: 113 us; four in two pairs that take the
-// chunks in turn: 118 us; four: 99 us).  Scores and weights have two buffers, so the products of one
-// chunk run under the weights of the next, and the scores of the chunk after that are issued before
-// this one's sums (2 % faster than after).  K and V are slots of their own in the ring, since a K
-// slot is free as soon as its product is done.
+// One CTA per SM: TMA producer, MMA issuer, two warps that widen V, four warpgroups that share the query
+// rows of every chunk (as two e4m3 terms, two that take the chunks in turn, with 64 scores and 64 sums in
+// registers and a merge at each unit's end: 385 us for 40 rows; two that share the rows: 113 us; four in two
+// pairs that take the chunks in turn: 118 us; four: 99 us).  Scores, widened V and weights have two buffers,
+// so the products of one chunk run under the weights of the next, and the scores of the chunk after that are
+// issued before this one's sums (2 % faster than after).  K and V are slots of their own in the ring, since a
+// K slot is free as soon as its product is done, a V slot once it is widened and its scales are read.
+// (V widened by the warps of the weights: 120 us; by two warps that load 16 bytes, store 32 and so on: 128,
+// each load waiting for the stores before it; one row's loads before its first store: 103; one buffer of
+// widened V and four chunks in the ring instead of two and three: 104; registers moved between the
+// warpgroups: 106 to 136, with spills.)
 //
 // Bound by the weights: per chunk each warp spends about 170 instructions that do not depend on its
-// rows (waits, scales, a vote, loads) and 14 a row, at 54 % of the issue slots; the products take 19 %
-// of the tensor pipe, and the vote on new references 9 % of the time.  8 sequences of up to 32K rows,
-// 5 new tokens, 64 query and 8 K/V heads (40 rows): 99 us for 311 MB, 3.2 TB/s, where the kernel of
-// products in registers took 211 us.  (One barrier for the scales of K and V, scales that are not finite
-// found by the vote, one arrival a warp: 102 -> 99 us.  Three buffers of weights, so that nothing waits
-// for the product before the last, take two slots from the ring: 100.)
+// rows (waits, scales, a vote, loads) and 11 a row.  8 sequences of up to 32K rows, 5 new tokens, 64 query and
+// 8 K/V heads (40 rows): 99 to 103 us for 311 MB, 3.1 TB/s, where the kernel of products in registers took 211
+// us.  For 40 rows the four warpgroups have 8, 8, 8 and 16 rows (TMEM is read in blocks of eight), and the
+// chunk waits for the last: an even split would save it a quarter of its rows' instructions.
 #pragma once
 
 #include "fa_decode_fp8.cuh"
@@ -50,23 +48,28 @@ namespace fa {
 struct Dec8TcCfg {
   static constexpr int D = 128, kRows = 64;
   static constexpr int kGroups = 4, kWork = 128 * kGroups, kThreads = 128 + kWork;  // warpgroups on the weights
-  static constexpr int kControlRegs = 40, kWorkRegs = 104;  // 128 x 40 + 512 x 104 <= 640 x 96
   static constexpr int kSlot = kDec8Keys * D;               // bytes of K (or V) of a chunk
-  static constexpr int kSlots = 10, kPairs = kSlots / 2;
+  static constexpr int kSlots = 6, kPairs = kSlots / 2;
   static constexpr int kScales = 8;                         // chunks whose scales are kept (> kPairs)
-  static constexpr int kP = kDec8Keys * 128;                // weights of a chunk: hi | lo of 64 rows
+  static constexpr int kP = kDec8Keys * kRows * 2;          // fp16 weights of a chunk
+  static constexpr int kPanel = kDec8Keys * 128, kV = 2 * kPanel;  // 64 columns of V of a chunk in fp16; all
   static constexpr int kQ = kRows * D;                      // hi (and lo) of the query tile
-  static constexpr int kColS = 0, kColO = 128, kTmemCols = 256;  // S: 2 x 64 columns; O: hi and lo of 64
+  static constexpr int kColS = 0, kColO = 128, kColOld = 192, kTmemCols = 256;  // S: 2 x 64 columns; O: 64 each
+  static constexpr int kRun = 256;                               // chunks that the products add up
   static constexpr int kCols = kRows / kGroups;                  // query rows of a warpgroup, at most
-  static constexpr int kOffP = kSlots * kSlot, kOffQ = kOffP + 2 * kP, kOffMisc = kOffQ + 2 * kQ;
+  static constexpr int kOffP = kSlots * kSlot, kOffV = kOffP + 2 * kP, kOffQ = kOffV + 2 * kV;
+  static constexpr int kOffMisc = kOffQ + 2 * kQ;
   static constexpr int kSmem = 1024 + kOffMisc + kScales * 64 + kRows * 8 + kRows * 4 + kRows * 16 + 4 * kRows * 4 +
                                64 * 8;
 };
 
-constexpr float kTcTop = 8.5f, kTcStart = 2.f;  // largest exponent of a weight; the one at a new reference
+// Largest exponent of p sv; the one at a new reference; the weights are p sv 2^6.
+constexpr float kTcTop = 8.5f, kTcStart = 2.f, kTcLift = 64.f;
 
-// Instruction descriptor with both operands MN-major.
-constexpr uint32_t kMnMajorBoth = (1u << 15) | (1u << 16);
+// Instruction descriptor for kind::f16 with fp16 A and B (format code 0), both MN-major, fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16_f32_mn(int M, int N) {
+  return (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
 
 // True for every thread of the warpgroup if it is for one (named barrier `id`, 128 threads).
 __device__ __forceinline__ bool group_any(int id, bool x) {
@@ -87,6 +90,42 @@ __device__ __forceinline__ int ordered(float x) {
 }
 __device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
 
+// V codes of a chunk (128-byte rows from `slot`) that some query of the unit does not see: rows past the
+// end may hold anything and become zeros; a NaN code would reach every query, so it goes to the queries
+// that see its row by hand (sm_nan) and becomes a zero.  Two rows a thread, whole warps.
+__device__ __forceinline__ void dec8_tc_clean_v(uint8_t* slot, int first, int j0, int len, int rows, const int* sm_limit,
+                                             uint32_t* sm_nan) {
+  constexpr int D = Dec8TcCfg::D;
+#pragma unroll 1
+  for (int row = first; row < kDec8Keys; row += 64) {
+    uint8_t* const v = slot + row * D;
+    const bool past = j0 + row >= len;
+    uint32_t nan = 0;
+#pragma unroll 1
+    for (int u = 0; u < D / 16; ++u) {
+      uint4* const at = reinterpret_cast<uint4*>(v + u * 16);
+      const uint4 y = *at;
+      if (past)
+        *at = make_uint4(0u, 0u, 0u, 0u);
+      else
+        nan |= ((y.x & 0x7F7F7F7Fu) + 0x01010101u) | ((y.y & 0x7F7F7F7Fu) + 0x01010101u) |
+               ((y.z & 0x7F7F7F7Fu) + 0x01010101u) | ((y.w & 0x7F7F7F7Fu) + 0x01010101u);
+    }
+    if (!__any_sync(0xffffffffu, (nan & 0x80808080u) != 0u)) continue;
+#pragma unroll 1
+    for (int d = 0; d < D; ++d) {
+      uint8_t* const at = v + (((d >> 4) ^ (row & 7)) << 4) + (d & 15);
+      const bool bad = !past && (*at & 0x7Fu) == 0x7Fu;
+      if (bad) *at = 0;
+      if (__any_sync(0xffffffffu, bad))
+#pragma unroll 1
+        for (int r = 0; r < rows; ++r)
+          if (bad && j0 + row < sm_limit[r]) atomicOr(sm_nan + r * 4 + (d >> 5), 1u << (d & 31));
+      __syncwarp();
+    }
+  }
+}
+
 __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
     fa_decode_fp8_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const Dec8Params p) {
@@ -97,6 +136,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const sm_p = ring + C::kOffP;
+  uint8_t* const sm_v = ring + C::kOffV;  // [2 chunks][2][128 rows][64 columns] fp16
   uint8_t* const sm_q = ring + C::kOffQ;
   float* const sm_scale = reinterpret_cast<float*>(ring + C::kOffMisc);        // [kScales][2][8]
   float* const sm_f = sm_scale + C::kScales * 16;             // [R]: factor of a row's scores
@@ -111,14 +151,15 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
   uint64_t* const s_empty = s_full + 2;   // [2]
   uint64_t* const p_full = s_empty + 2;   // [2]
   uint64_t* const p_done = p_full + 2;    // [2]
-  uint64_t* const all_done = p_done + 2;
+  uint64_t* const v_full = p_done + 2;    // [2]
+  uint64_t* const all_done = v_full + 2;
   __shared__ uint32_t tmem_slot;
   __shared__ Dec8Share share;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(full + s, s & 1 ? 1 + 16 : 1);  // the producer's expect_tx; with V, sixteen lanes' scales
-      mbar_init(empty + s, 1);
+      mbar_init(empty + s, s & 1 ? 2 + C::kWork / 32 : 1);  // V: the warps that widen it, those that take its scales
     }
     mbar_init(q_full, C::kWork / 32);
     for (int w = 0; w < 2; ++w) {
@@ -126,6 +167,7 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
       mbar_init(s_empty + w, C::kWork / 32);
       mbar_init(p_full + w, C::kWork / 32);
       mbar_init(p_done + w, 1);
+      mbar_init(v_full + w, 2);
     }
     mbar_init(all_done, 1);
     fence_barrier_init();
@@ -144,7 +186,6 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
   Dec8Seg seg;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kControlRegs));
     if (warp == 0) {
       // ------------------------------------------------------------ producer
       // Lanes 0..15: (K or V, 16-row tile of the chunk), as in fa_decode_fp8_kernel.
@@ -202,12 +243,13 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ MMA issuer
-      constexpr uint32_t idS = idesc_e4m3_f32(128, R), idO = idesc_e4m3_f32(128, 128) | kMnMajorBoth;
+      constexpr uint32_t idS = idesc_e4m3_f32(128, R), idO = idesc_f16_f32_mn(D, R);
       const uint64_t dRing = smem_desc_sw128(smem_u32(ring), 16, 1024);
       const uint64_t dP = smem_desc_sw128(smem_u32(sm_p), 16, 1024);
+      const uint64_t dV = smem_desc_sw128(smem_u32(sm_v), C::kPanel, 1024);
       const uint64_t dQ = smem_desc_sw128(smem_u32(sm_q), 16, 1024);
-      int pair = 0, vpair = 0;
-      uint32_t kphase = 0, vphase = 0, qphase = 0;
+      int pair = 0;
+      uint32_t kphase = 0, qphase = 0;
       uint32_t n_s = 0, n_p = 0;  // products issued; buffer = the last bit, use of it = the rest
       bool ok = true;
       auto product_s = [&] {
@@ -232,22 +274,19 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
       };
       auto product_o = [&](bool first) {
         const uint32_t w = n_p & 1u;
-        ok = ok && warp_wait(full + 2 * vpair + 1, vphase) && warp_wait(p_full + w, (n_p >> 1) & 1u);
+        ok = ok && warp_wait(v_full + w, (n_p >> 1) & 1u) && warp_wait(p_full + w, (n_p >> 1) & 1u);
         if (!ok) return;
         tc_fence_after();
         if (elect_one_lane()) {
-          const uint64_t a = dRing + (uint64_t)(((2 * vpair + 1) * C::kSlot) >> 4);
-          const uint64_t b = dP + (uint64_t)((w * C::kP) >> 4);
+          const uint64_t a = dV + (uint64_t)((w * C::kV) >> 4), b = dP + (uint64_t)((w * C::kP) >> 4);
 #pragma unroll
-          for (int k = 0; k < kDec8Keys / 32; ++k)  // 32 cache rows = 4 KB of either operand
-            mma_ss<1>(tmem + C::kColO, a + (uint64_t)(k * 256), b + (uint64_t)(k * 256), idO,
+          for (int k = 0; k < kDec8Keys / 16; ++k)  // 16 cache rows = 2 KB of either operand
+            mma_ss<0>(tmem + C::kColO, a + (uint64_t)(k * 128), b + (uint64_t)(k * 128), idO,
                       first && k == 0 ? 0u : 1u);
           umma_commit(p_done + w);
-          umma_commit(empty + 2 * vpair + 1);
         }
         __syncwarp();
         ++n_p;
-        if (++vpair == C::kPairs) vpair = 0, vphase ^= 1u;
       };
       while (ok && walk.next(p, seg)) {
         const int n = seg.c1 - seg.c0;
@@ -257,14 +296,61 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         if (ok && n > 1) product_s();
         for (int k = 0; k < n && ok; ++k) {
           if (k + 2 < n) product_s();
-          product_o(k == 0);
+          product_o(k % C::kRun == 0);
         }
       }
       umma_commit_elect(all_done);  // nothing is in flight when the columns are given back
       (void)warp_wait(all_done, 0);
+    } else {
+      // ------------------------------------------------------------ V to fp16: two rows a thread
+      const int first = threadIdx.x - 64;
+      int pair = 0;
+      uint32_t phase = 0, qphase = 0, n = 0;
+      bool ok = true;
+      while (ok && walk.next(p, seg)) {
+        ok = warp_wait(q_full, qphase);  // the tables of the unit's query rows
+        qphase ^= 1u;
+        const int tile = seg.unit % p.tiles, rows = min(R, p.rows - tile * R);
+        const int first_limit = seg.len - p.Nq + 1 + (tile * R) / p.G;
+        for (int c = seg.c0; c < seg.c1 && ok; ++c, ++n) {
+          ok = warp_wait(full + 2 * pair + 1, phase);
+          if (!ok) break;
+          uint8_t* const slot = ring + (2 * pair + 1) * C::kSlot;
+          const bool partly = (c + 1) * kDec8Keys > first_limit;
+          if (partly) dec8_tc_clean_v(slot, first, c * kDec8Keys, seg.len, rows, sm_limit, sm_nan);
+          const int sw = first & 7;  // of both rows
+          // the product that reads the chunk before the last has ended
+          ok = n < 2 || warp_wait(p_done + (n & 1u), ((n >> 1) - 1) & 1u);
+          if (!ok) break;
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            const int row = first + 64 * t;
+            uint4 y[D / 16];  // (all of a row before the first store, which might be to where the next load is from)
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) y[u] = *reinterpret_cast<const uint4*>(slot + row * D + ((u ^ sw) << 4));
+#pragma unroll
+            for (int u = 0; u < D / 16; ++u) {  // 16 columns: two units of 8 of panel u / 4
+              uint4 h0, h1;
+              e4m3x4_to_f16(y[u].x, h0.x, h0.y);
+              e4m3x4_to_f16(y[u].y, h0.z, h0.w);
+              e4m3x4_to_f16(y[u].z, h1.x, h1.y);
+              e4m3x4_to_f16(y[u].w, h1.z, h1.w);
+              uint8_t* const to = sm_v + (n & 1u) * C::kV + (u >> 2) * C::kPanel + row * 128;
+              *reinterpret_cast<uint4*>(to + (((u & 3) * 2 ^ sw) << 4)) = h0;
+              *reinterpret_cast<uint4*>(to + ((((u & 3) * 2 + 1) ^ sw) << 4)) = h1;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(v_full + (n & 1u));
+            mbar_arrive(empty + 2 * pair + 1);
+          }
+          if (++pair == C::kPairs) pair = 0, phase ^= 1u;
+        }
+      }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kWorkRegs));
     // -------------------------------------------------------------- weights
     const int w = (warp >> 2) - 1, tid = threadIdx.x - 128;  // group; thread among the groups'
     const int row = tid & 127, quarter = row >> 5;           // cache row of a chunk = TMEM lane
@@ -385,6 +471,29 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
         tmem_wait_ld();
         tc_fence_before();
         arrive(s_empty + buf);
+        if (lane == 0) mbar_arrive(empty + 2 * pair + 1);  // (the scales have been read)
+        // The products' additions drop bits under the last of the sum so far, all downwards: a run of chunks
+        // is added to the runs before it, rounded to nearest, and the next one starts at 0.  (One sum over
+        // 512K keys was 0.5 % low, over 2M 1.4 %.)
+        const int run = c - seg.c0;
+        if (run > 0 && run % C::kRun == 0) {
+          if (ok) ok = mbar_wait(p_done + (buf ^ 1u), ((n - 1) >> 1) & 1u);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll
+          for (int b = 0; b < N / 8; ++b)
+            if (b < blocks) {
+              float o[8], old[8];
+              const uint32_t at = tmem + col0 + b * 8 + lanes;
+              tmem_ld8(at + C::kColO, reinterpret_cast<uint32_t(&)[8]>(o));
+              tmem_ld8(at + C::kColOld, reinterpret_cast<uint32_t(&)[8]>(old));
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 8; ++x) o[x] = run > C::kRun ? o[x] + old[x] : o[x];
+              tmem_st8(at + C::kColOld, reinterpret_cast<uint32_t(&)[8]>(o));
+            }
+          tmem_wait_st();
+        }
         // exponents t - reference, and whether one is past the top
         float most[N / 8];
         bool past_top = false;
@@ -476,10 +585,9 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
                 }
 #pragma unroll
                 for (int x = 0; x < 8; ++x) up[x] = ex2_approx(-up[x]);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int old = 0; old <= (run >= C::kRun); ++old) {
                   float o[8];
-                  const uint32_t at = tmem + C::kColO + t * R + col0 + b * 8 + lanes;
+                  const uint32_t at = tmem + (old ? C::kColOld : C::kColO) + col0 + b * 8 + lanes;
                   tmem_ld8(at, reinterpret_cast<uint32_t(&)[8]>(o));
                   tmem_wait_ld();
 #pragma unroll
@@ -496,73 +604,24 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
           __syncwarp();
           asm volatile("bar.sync %0, 128;" ::"r"(2 + w) : "memory");
         }
-        // V rows that some query does not see (this group's part of the columns): past the end they
-        // may hold anything, and a NaN code would reach every query; it goes to the queries that see
-        // it by hand
-        if (partly) {
-          uint8_t* const v = ring + (2 * pair + 1) * C::kSlot + row * D;
-          uint32_t nan = 0;
-          const bool past = j >= seg.len;
-#pragma unroll
-          for (int u = 0; u < 8 / C::kGroups; ++u) {
-            uint4* const at = reinterpret_cast<uint4*>(v) + ((8 / C::kGroups * w + u) ^ (row & 7));
-            uint4 y = *at;
-            if (past) y = make_uint4(0u, 0u, 0u, 0u);
-            *at = y;
-            nan |= ((y.x & 0x7F7F7F7Fu) + 0x01010101u) | ((y.y & 0x7F7F7F7Fu) + 0x01010101u) |
-                   ((y.z & 0x7F7F7F7Fu) + 0x01010101u) | ((y.w & 0x7F7F7F7Fu) + 0x01010101u);
-          }
-          // (rare, and taken by whole warps)
-          if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0u)) {
-#pragma unroll 1
-            for (int d = D / C::kGroups * w; d < D / C::kGroups * (w + 1); ++d) {
-              uint8_t* const at = v + (((d >> 4) ^ (row & 7)) << 4) + (d & 15);
-              const bool bad = (*at & 0x7Fu) == 0x7Fu;
-              if (bad) *at = 0;
-              if (__any_sync(0xffffffffu, bad)) {
-#pragma unroll 1
-                for (int r = 0; r < rows; ++r)
-                  if (bad && j < sm_limit[r]) atomicOr(sm_nan + r * 4 + (d >> 5), 1u << (d & 31));
-              }
-              __syncwarp();
-            }
-          }
-        }
         // the weights replace those of the chunk before the last once their product is done
         if (n >= 2 && ok) ok = mbar_wait(p_done + buf, (use - 1) & 1u);
         uint8_t* const prow = sm_p + buf * C::kP + row * 128;
-        const uint64_t sv2 = f2(sv, sv), sv16 = f2(sv * 16.f, sv * 16.f), m16 = f2(-16.f, -16.f);
-        // up to half a step of the second term for small weights, 2^-10, either way, evenly over the rows
-        const float nudge = (float)(int)((uint32_t)j * 0x9E3779B9u) * 4.547473508864641e-13f;
-        const uint64_t nudge2 = f2(nudge, nudge);
+        const uint64_t sv2 = f2(sv * kTcLift, sv * kTcLift);
 #pragma unroll
         for (int b = 0; b < N / 8; ++b)
           if (b < blocks) {
-            uint32_t hi[2], lo[2];
+            uint4 h;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int r = b * 8 + 4 * x;
+            for (int x = 0; x < 4; ++x) {
+              const int r = b * 8 + 2 * x;
               const uint64_t p0 = f2(ex2_approx(s[r]), ex2_approx(s[r + 1]));
-              const uint64_t p1 = f2(ex2_approx(s[r + 2]), ex2_approx(s[r + 3]));
               l2[r / 2] = f2_add(l2[r / 2], p0);
-              l2[r / 2 + 1] = f2_add(l2[r / 2 + 1], p1);
-              float w0, w1, w2, w3;
+              float w0, w1;
               f2_split(f2_mul(p0, sv2), w0, w1);
-              f2_split(f2_mul(p1, sv2), w2, w3);
-              hi[x] = e4m3x4(w0, w1, w2, w3);
-              uint32_t b0, b1;
-              e4m3x4_to_f16(hi[x], b0, b1);
-              const float2 f0 = __half22float2(*reinterpret_cast<__half2*>(&b0));
-              const float2 f1 = __half22float2(*reinterpret_cast<__half2*>(&b1));
-              // 16 (w - hi), with 16 w = p (16 sv) the same value
-              f2_split(f2_fma(f2(f0.x, f0.y), m16, f2_fma(p0, sv16, nudge2)), w0, w1);
-              f2_split(f2_fma(f2(f1.x, f1.y), m16, f2_fma(p1, sv16, nudge2)), w2, w3);
-              lo[x] = e4m3x4(w0, w1, w2, w3);
+              (&h.x)[x] = pack_f16x2(w0, w1);
             }
-            const int at = col0 + b * 8;  // byte of the row; its 16-byte unit is swizzled
-            *reinterpret_cast<uint2*>(prow + (((at >> 4) ^ (row & 7)) << 4) + (at & 8)) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(prow + (((4 + (at >> 4)) ^ (row & 7)) << 4) + (at & 8)) =
-                make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint4*>(prow + ((((col0 >> 3) + b) ^ (row & 7)) << 4)) = h;
           }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -602,17 +661,21 @@ __global__ void __launch_bounds__(Dec8TcCfg::kThreads, 1)
 #pragma unroll
       for (int b = 0; b < N / 8; ++b)
         if (b < blocks) {
-          float hi[8], lo[8];
-          tmem_ld8(tmem + C::kColO + col0 + b * 8 + lanes, reinterpret_cast<uint32_t(&)[8]>(hi));
-          tmem_ld8(tmem + C::kColO + R + col0 + b * 8 + lanes, reinterpret_cast<uint32_t(&)[8]>(lo));
+          float sum[8], old[8];
+          const uint32_t from = tmem + col0 + b * 8 + lanes;
+          tmem_ld8(from + C::kColO, reinterpret_cast<uint32_t(&)[8]>(sum));
+          tmem_ld8(from + C::kColOld, reinterpret_cast<uint32_t(&)[8]>(old));
           tmem_wait_ld();
+          if (seg.c1 - seg.c0 > C::kRun)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) sum[x] += old[x];
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             const int r = b * 8 + x, tr = col0 + r, qr = tile * R + tr;
             if (tr >= rows) continue;
             const float L = red[r] + red[N + r] + red[2 * N + r] + red[3 * N + r];
             const float M = L == 0.f ? kDec8Low : -ref[r];  // nothing seen: no reference
-            float A = fmaf(lo[x], 0.0625f, hi[x]);
+            float A = sum[x] * (1.f / kTcLift);
             if ((sm_nan[tr * 4 + (row >> 5)] >> (row & 31)) & 1u) A = __uint_as_float(0x7FC00000u);
             if (whole) {
               const int i = qr / p.G, h = kvh * p.G + qr - i * p.G;

@@ -323,12 +323,11 @@ FA_EXPORT fa_status fa_cache_append_fp8(const void* k, const void* v, const int3
  * count as 0, larger ones than max_pages_per_seq * page_size as that.  Rows past a sequence's end may hold anything; a NaN code or scale makes NaN of what
  * attends to it, and of nothing else.  An entry of the table outside [0, num_pages) is
  * read as page 0 and recorded (FA_ERR_INVALID_ARG from fa_last_device_error).
- * The stored values are exact in the products and all sums are fp32.  P times the V scale is
- * rounded to fp16 relative to a value within 2^6 of its largest; for more than 16 query rows of a K/V head
- * (Nq * Hq / Hkv) and d = 128 it is the sum of two e4m3 terms instead (8 bits, like bf16, in steps of
- * 2^-15 of the largest value at the least; values between two such steps go up or down in proportion, so
- * that the sum of many is kept), and so is q (2^-17 of a row's largest element at the least);
- * V scales outside 2^-100 .. 2^100 lose accuracy there.  o is rounded to bf16.
+ * The stored values are exact in the products and all sums are fp32.  P times the V scale is rounded
+ * to fp16 relative to a value within 2^6 of its largest.  For more than 16 query rows of a K/V head
+ * (Nq * Hq / Hkv) and d = 128, q is the sum of two e4m3 terms (8 bits, like bf16; 2^-17 of a row's
+ * largest element at the least), and V scales outside 2^-100 .. 2^100 lose accuracy.  o is rounded to
+ * bf16.
  * Hq a multiple of Hkv; d 64 or 128; sizes as in fa_cache_append_fp8, and B * Hkv *
  * max_pages_per_seq * page_size * (Nq * (Hq / Hkv) / 64, rounded up) < 2^37 (FA_ERR_UNSUPPORTED
  * beyond).  workspace: at least fa_decode_paged_fp8_workspace_size(...) bytes (with the call's

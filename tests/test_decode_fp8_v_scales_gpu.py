@@ -1,9 +1,9 @@
 """Decode over the e4m3 cache where the V scales of one sequence lie far apart: every key keeps its
 share of the softmax's sum, whatever its scale.
 
-lse: 2^-17 (1 + t), as in test_cache_fp8_gpu.py.  o: half a bf16 step; the weights' relative rounding
-and the scores' 2^-17 (1 + t); and what a small weight may be off by against the largest one (2^-25 in
-fp16, a step of 2^-15 as two e4m3 terms) for a code of at most 448."""
+lse: 2^-17 (1 + t), as in test_cache_fp8_gpu.py.  o: half a bf16 step; the fp16 weights' 2^-11 and the
+scores' 2^-17 (1 + t), relative; and 2^-25 of the largest weight, which is at least 1, for a code of at
+most 448."""
 import numpy as np
 import pytest
 import torch
@@ -28,13 +28,11 @@ def _far_scales(lens, Hq, d, place, ps=32, sb=16):
     q64 = q.double().cpu().numpy()
     r_o, r_lse, o_abs, _, t_abs = cache8.attend(q64, kc, ks, vc, vs, table, lens, sb, 1.0)
     o, lse = fa.decode_paged_fp8(q, dev[0], dev[2], dev[1], dev[3], dev[4], dev[5], scale=1.0)
-    two = Hq > 16 and d == 128
-    u = _score_bound(q64, (kc, ks, vc, vs, table, lens, sb, 1.0)) if two else 0.0
+    u = _score_bound(q64, (kc, ks, vc, vs, table, lens, sb, 1.0)) if Hq > 16 and d == 128 else 0.0
     assert np.all(np.abs(lse.double().cpu().numpy() - r_lse) <= 2.0 ** -17 * (1 + t_abs + u))
-    weight, small = (2.0 ** -8, 2.0 ** -15) if two else (2.0 ** -11, 2.0 ** -25)
     top = _weight_max(q64, kc, ks, vs, table, lens, sb)
     tt = (t_abs + u).transpose(0, 2, 1)[..., None]
-    tol = 2.0 ** -8 * np.abs(r_o) + (weight + 2.0 ** -17 * (1 + tt)) * o_abs + max(lens) * small * 448 * top
+    tol = 2.0 ** -8 * np.abs(r_o) + (2.0 ** -11 + 2.0 ** -17 * (1 + tt)) * o_abs + max(lens) * 2.0 ** -25 * 448 * top
     assert np.all(np.abs(o.double().cpu().numpy() - r_o) <= tol)
 
 
