@@ -289,10 +289,10 @@ __device__ __noinline__ bool dec8_clean_v(uint8_t* vs, int j0, int len) {
 }
 
 // A NaN code may be for some queries only, but 0 * NaN would reach the others: it goes straight
-// into the sums of those that see its row, and becomes a zero code: in the tile itself (ZERO), or, where
-// warps of other query rows read the same tile, in each warp's registers (dec8_zero_nan).  Rare, so a call.
-template <int D, int MT, bool ZERO>
-__device__ __noinline__ void dec8_nan_v(uint8_t* vs, int j0, int len, const int (&limit)[MT][2],
+// into the sums of those that see its row (dec8_nan_v), and becomes a zero code (dec8_zero_v).  Rare, so
+// calls.
+template <int D, int MT>
+__device__ __noinline__ void dec8_nan_v(const uint8_t* vs, int j0, int len, const int (&limit)[MT][2],
                                         float (&acc)[MT][D / 8][4]) {
   constexpr int n = 16;
   const int lane = threadIdx.x & 31, tig = lane & 3;
@@ -310,16 +310,13 @@ __device__ __noinline__ void dec8_nan_v(uint8_t* vs, int j0, int len, const int 
               if (j0 + r < limit[mt][hr]) acc[mt][2 * k + (x & 1)][2 * hr + (x >> 1)] = __uint_as_float(0x7FC00000u);
     }
   __syncwarp();
-  if (!ZERO) return;
-  for (int u = lane; u < n * D; u += 32)
-    if ((vs[u] & 0x7Fu) == 0x7Fu) vs[u] = 0;
-  __syncwarp();
 }
 
-// Four codes with zeros for the NaN ones.
-__device__ __forceinline__ uint32_t dec8_zero_nan(uint32_t w) {
-  const uint32_t nan = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // the top bit of each such byte
-  return w & ~((nan >> 7) * 0xFFu);
+template <int D>
+__device__ __noinline__ void dec8_zero_v(uint8_t* vs) {
+  for (int u = threadIdx.x & 31; u < 16 * D; u += 32)
+    if ((vs[u] & 0x7Fu) == 0x7Fu) vs[u] = 0;
+  __syncwarp();
 }
 
 // The producer warp's part.  Lanes 0..15: (K or V, K/V head, 16-row tile of the chunk), in the order of
@@ -512,8 +509,11 @@ __global__ void __launch_bounds__(Dec8WideCfg<D, MT, RG>::kThreads, Dec8WideCfg<
         }
       }
     if constexpr (MT > 1) asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
-    const int first_limit = seg.len - p.Nq + 1 + min(row0, p.rows - 1) / p.G;
+    // of the whole tile, so that its row groups agree on the cache tiles that they look through
+    const int first_limit = seg.len - p.Nq + 1 + tile * R / p.G;
     const bool idle = row0 >= p.rows;  // a row group without rows
+    const bool both = RG > 1 && tile * R + 16 * MT < p.rows;  // no row group is
+    static_assert(RG <= 2, "two row groups at most");
 
     float acc[MT][D / 8][4];
     float m_r[MT][2], l_r[MT][2], w_r[MT][2];  // references of t and of t + log2(sv); sum of p
@@ -540,12 +540,16 @@ __global__ void __launch_bounds__(Dec8WideCfg<D, MT, RG>::kThreads, Dec8WideCfg<
           const int j0 = jw + 16 * t0;
           if (KT == 1 && j0 >= seg.len) break;
           const bool partly = j0 + 16 * KT > first_limit;  // rows past the end, or that some query does not see
-          bool nan_codes = false;                          // in a tile that other row groups read too
           if (partly) {
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) {
               uint8_t* const vs = st + C::kHalf + toff[t0 + kt];
-              if (!dec8_clean_v<D>(vs, j0 + 16 * kt, seg.len)) continue;
+              const bool nan = dec8_clean_v<D>(vs, j0 + 16 * kt, seg.len);
+              // the other row group's warp looks at the same tile: neither zeroes a code before both have
+              if (!nan) {
+                if (RG > 1 && both) asm volatile("bar.sync %0, 64;" ::"r"(2 + w4) : "memory");
+                continue;
+              }
               // copies, so that the sums themselves stay in registers
               int lim[MT][2];
               float sums[MT][D / 8][4];
@@ -557,8 +561,9 @@ __global__ void __launch_bounds__(Dec8WideCfg<D, MT, RG>::kThreads, Dec8WideCfg<
 #pragma unroll
                   for (int e = 0; e < 4; ++e) sums[mt][n][e] = acc[mt][n][e];
               }
-              dec8_nan_v<D, MT, RG == 1>(vs, j0 + 16 * kt, seg.len, lim, sums);
-              nan_codes = RG > 1;
+              dec8_nan_v<D, MT>(vs, j0 + 16 * kt, seg.len, lim, sums);
+              if (RG > 1 && both) asm volatile("bar.sync %0, 64;" ::"r"(2 + w4) : "memory");
+              dec8_zero_v<D>(vs);
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -691,9 +696,6 @@ __global__ void __launch_bounds__(Dec8WideCfg<D, MT, RG>::kThreads, Dec8WideCfg<
               // transposed: a register holds bytes (2 g, 2 g + 1) of the unit for rows 2 tig and 2 tig + 1
               uint32_t w[4], e0, o0, e1, o1;
               ldsm_x4_t((base + C::kHalf + toff[t0 + kt]) ^ (k << 4), w[0], w[1], w[2], w[3]);
-              if (RG > 1 && nan_codes)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) w[x] = dec8_zero_nan(w[x]);
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
                 e4m3x4_to_f16(__byte_perm(w[2 * x], 0u, 0x3120), e0, o0);
