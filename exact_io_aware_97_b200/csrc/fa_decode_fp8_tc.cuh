@@ -101,15 +101,17 @@ __device__ __forceinline__ void dec8_tc_clean_v(uint8_t* slot, int first, int j0
     uint8_t* const v = slot + row * D;
     const bool past = j0 + row >= len;
     uint32_t nan = 0;
-#pragma unroll 1
-    for (int u = 0; u < D / 16; ++u) {
-      uint4* const at = reinterpret_cast<uint4*>(v + u * 16);
-      const uint4 y = *at;
-      if (past)
-        *at = make_uint4(0u, 0u, 0u, 0u);
-      else
+    uint4* const at16 = reinterpret_cast<uint4*>(v);
+    if (past) {
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u) at16[u ^ (row & 7)] = make_uint4(0u, 0u, 0u, 0u);
+    } else {
+#pragma unroll
+      for (int u = 0; u < D / 16; ++u) {
+        const uint4 y = at16[u ^ (row & 7)];
         nan |= ((y.x & 0x7F7F7F7Fu) + 0x01010101u) | ((y.y & 0x7F7F7F7Fu) + 0x01010101u) |
                ((y.z & 0x7F7F7F7Fu) + 0x01010101u) | ((y.w & 0x7F7F7F7Fu) + 0x01010101u);
+      }
     }
     if (!__any_sync(0xffffffffu, (nan & 0x80808080u) != 0u)) continue;
 #pragma unroll 1
