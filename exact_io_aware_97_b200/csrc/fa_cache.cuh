@@ -12,7 +12,8 @@
 // Bound by HBM for prompts (2 bytes read and 1 written per element; 67.6K rows of 8 heads, d = 128: 78
 // us, 5.7 TB/s of the copy's 6.55) and by the chain of dependent loads (lengths, block table, scale,
 // rows) for single tokens.  A unit is one (block, head): its warps hold the rows of K and V in
-// registers, so a row is read once for the maximum and the rounding alike.
+// registers (64 a thread, and 72 bytes of other values spilled), so a row is read once for the maximum
+// and the rounding alike.
 #pragma once
 
 #include <cuda_fp16.h>

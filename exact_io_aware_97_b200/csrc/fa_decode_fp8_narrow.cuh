@@ -9,7 +9,7 @@
 // 16-row operand, 303 instructions of a warp for 16 cache rows and two CTAs per SM, 8 sequences of
 // 32K rows took 100 us and, once the power limit has the clock at 1780 MHz, 110 (latencies, not
 // HBM, were the bound); so, with 247 instructions and three CTAs per SM, 90, and 92 at 1640 MHz.
-// (16 rows this way, as two 8-column operands, spill: 69 to 118 us for the 59 of the other kernel.)
+// (16 rows this way, as two 8-column operands, spill and are slower than as one 16-row operand.)
 #pragma once
 
 #include "fa_decode_fp8.cuh"

@@ -10,8 +10,8 @@
 // integer), so a position of millions loses nothing; sine and cosine of the reduced angle, and
 // the products, are fp32, rounded once on output.
 //
-// Bound by HBM: every element is read and written once (8192 rows of 72 heads, d = 128, bf16: 52 us, 5.8
-// TB/s of the 6.55 that a copy reaches; 32749 rows of 40 heads: 107 us, 6.2 TB/s).  One warp owns one (token, run of
+// Bound by HBM: every element is read and written once (8192 rows of 72 heads, d = 128, bf16: 50.5 us, 6.0
+// TB/s of the 6.55 that a copy reaches; 32749 rows of 40 heads: 106 us, 6.3 TB/s).  One warp owns one (token, run of
 // heads): its lanes hold the sines and cosines of their own columns in registers for all heads
 // of the run, so no shared memory, barrier or table in device memory is involved.
 #pragma once
@@ -52,7 +52,7 @@ __device__ __forceinline__ void rope_store(float* y, float v) { *y = v; }
 __device__ __forceinline__ void rope_store(__nv_bfloat16* y, float v) { *y = __float2bfloat16_rn(v); }
 
 // Any even rot in the half layout: one lane per pair of columns (or per copied column); what the
-// vectors below cannot take (8192 rows as above in this way: 184 us).
+// vectors below cannot take (8192 rows as above: 184 us for rot = 128 in this way, 315 for 120, 92 or 74).
 template <typename T, int D>
 __global__ void __launch_bounds__(256) fa_rope_kernel(const RopeParams p) {
   grid_wait();

@@ -252,8 +252,8 @@ FA_EXPORT size_t fa_decode_paged_workspace_size(int B, int Hq, int Hkv, int max_
  *   y_a = amplitude (x_a cos - x_b sin),  y_b = amplitude (x_b cos + x_a sin),
  * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) if `interleaved`; the other columns are
  * copied.  backward != 0 gives the gradient: x is the gradient of y, y that of x (the same
- * formula with -sin).  Angles are reduced in fp64, so far positions lose nothing; the products
- * are fp32 and rounded once to the element type.
+ * formula with -sin).  Angles are reduced to less than a turn in fp64, so far positions lose nothing;
+ * what remains of them, sines, cosines and products are fp32, rounded once to the element type.
  *
  * q [rows, Hq, d], k [rows, Hk, d] (Hk may be 0: q alone), each row's heads dense and rows
  * q_stride / k_stride elements apart (Hq * d when dense; 3 H d for q and k inside a packed
@@ -329,8 +329,8 @@ FA_EXPORT fa_status fa_cache_append_fp8(const void* k, const void* v, const int3
  * largest element at the least), and V scales outside 2^-100 .. 2^100 lose accuracy.  o is rounded to
  * bf16.
  * Hq a multiple of Hkv; d 64 or 128; sizes as in fa_cache_append_fp8, and B * Hkv *
- * max_pages_per_seq * page_size * (Nq * (Hq / Hkv) / 64, rounded up) < 2^37 (FA_ERR_UNSUPPORTED
- * beyond).  workspace: at least fa_decode_paged_fp8_workspace_size(...) bytes (with the call's
+ * (max_pages_per_seq * page_size + 1408) * (Nq * (Hq / Hkv) / 64, rounded up) < 2^38 suffices for what
+ * is counted in 32 bits (FA_ERR_UNSUPPORTED beyond).  workspace: at least fa_decode_paged_fp8_workspace_size(...) bytes (with the call's
  * device current), 16-byte aligned, not initialised; calls that share one must not overlap on the
  * GPU.  o and lse must not overlap the inputs. */
 FA_EXPORT fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
@@ -365,7 +365,8 @@ typedef struct {
  * page_size is a power of two.
  * Recorded for fa_last_device_error (FA_ERR_INVALID_ARG): a parent outside [-1, B) (taken as
  * -1), a length that is negative or past the table (taken as 0), an entry outside [0, num_pages)
- * (passed on, never copied), and too few free pages (those new sequences become empty).
+ * (passed on, never copied), and too few free pages (those new sequences become empty; pages that only
+ * they name are in no list then, and come back with the next fork or compaction).
  * workspace: at least fa_pages_workspace_size(num_pages, B_out) bytes, 16-byte aligned, not
  * initialised; calls that share one must not overlap on the GPU. */
 FA_EXPORT fa_status fa_pages_fork(const fa_pool* pools, int n_pools, const int32_t* block_table,
