@@ -252,8 +252,9 @@ FA_EXPORT size_t fa_decode_paged_workspace_size(int B, int Hq, int Hkv, int max_
  *   y_a = amplitude (x_a cos - x_b sin),  y_b = amplitude (x_b cos + x_a sin),
  * with (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) if `interleaved`; the other columns are
  * copied.  backward != 0 gives the gradient: x is the gradient of y, y that of x (the same
- * formula with -sin).  Angles are reduced to less than a turn in fp64, so far positions lose nothing;
- * what remains of them, sines, cosines and products are fp32, rounded once to the element type.
+ * formula with -sin).  Angles are reduced in fp64, so far positions lose nothing; their sines and
+ * cosines (within 1.5 * 2^-24, and 2^-51 of the angle) and the products are fp32, rounded once to the
+ * element type.
  *
  * q [rows, Hq, d], k [rows, Hk, d] (Hk may be 0: q alone), each row's heads dense and rows
  * q_stride / k_stride elements apart (Hq * d when dense; 3 H d for q and k inside a packed
