@@ -1094,7 +1094,7 @@ fa_status launch_append(const AppendParams& prm, cudaStream_t st) {
 constexpr int kDec8Lead = 4, kDec8TcLead = 10;
 // Query rows of a unit: the 8 columns of a tensor-core product, or its 16 rows, where that holds them
 // (8 rows over 8 sequences of 32K: 90 us instead of 100 as 16); else the kernel on tcgen05 products with 64
-// (d = 128: 40 rows, 8 sequences of up to 32K, in 99 us instead of 211 with 64 rows in registers), or
+// (d = 128: 40 rows, 8 sequences of up to 32K, in 104 us instead of 211 with 64 rows in registers), or
 // registers for 32 or 64 (d = 64, where a cache row is too short for those products' 128 rows).
 int dec8_tile(int64_t rows, int d) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 && d == 64 ? 32 : 64; }
 // K/V heads of a unit, as a shift: one where the query rows fill more than a tile (the products,

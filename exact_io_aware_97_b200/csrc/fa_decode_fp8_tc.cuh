@@ -35,9 +35,11 @@
 // warpgroups: 106 to 136, with spills.)
 //
 // Bound by the weights: per chunk each warp spends about 170 instructions that do not depend on its
-// rows (waits, scales, a vote, loads) and 11 a row.  8 sequences of up to 32K rows, 5 new tokens, 64 query and
-// 8 K/V heads (40 rows): 99 to 103 us for 311 MB, 3.1 TB/s, where the kernel of products in registers took 211
-// us.  For 40 rows the four warpgroups have 8, 8, 8 and 16 rows (TMEM is read in blocks of eight), and the
+// rows (waits, scales, a vote, loads) and 11 a row, at 51 % of the issue slots; the threads' own accesses take
+// 45 % of shared memory's cycles, the products 19 % of the tensor pipe's.  8 sequences of up to 32K rows, 5 new tokens, 64 query and
+// 8 K/V heads (40 rows): 102 to 104 us for 311 MB, 3.0 TB/s, where the kernel of products in registers took 211
+// us; 8 of 32K: 136 us for 24 rows, 151 for 40, 168 for 64 (a floor of 82; for few rows the two warps that
+// widen V are the bound, 2400 cycles a chunk).  For 40 rows the four warpgroups have 8, 8, 8 and 16 rows (TMEM is read in blocks of eight), and the
 // chunk waits for the last: an even split would save it a quarter of its rows' instructions.
 #pragma once
 
