@@ -106,7 +106,9 @@ struct Dec8Seg {
   int c0, c1;          // chunks [c0, c1)
 };
 
-__device__ __forceinline__ int dec8_len(const Dec8Params& p, int b) { return min(max(load_in(p.seqlens + b), 0), p.cap); }
+__device__ __forceinline__ int dec8_len(const Dec8Params& p, int b) {
+  return min(max(load_in(p.seqlens + b), 0), p.cap);
+}
 
 // Positions count chunks and, before each unit's first, p.lead more that stand for what a unit costs
 // on its own (its queries, the start and the end of its pipeline), so that shares of many short units

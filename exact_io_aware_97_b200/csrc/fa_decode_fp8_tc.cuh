@@ -36,11 +36,12 @@
 //
 // Bound by the weights: per chunk each warp spends about 170 instructions that do not depend on its
 // rows (waits, scales, a vote, loads) and 11 a row, at 51 % of the issue slots; the threads' own accesses take
-// 45 % of shared memory's cycles, the products 19 % of the tensor pipe's.  8 sequences of up to 32K rows, 5 new tokens, 64 query and
-// 8 K/V heads (40 rows): 102 to 104 us for 311 MB, 3.0 TB/s, where the kernel of products in registers took 211
-// us; 8 of 32K: 136 us for 24 rows, 151 for 40, 168 for 64 (a floor of 82; for few rows the two warps that
-// widen V are the bound, 2400 cycles a chunk).  For 40 rows the four warpgroups have 8, 8, 8 and 16 rows (TMEM is read in blocks of eight), and the
-// chunk waits for the last: an even split would save it a quarter of its rows' instructions.
+// 45 % of shared memory's cycles, the products 19 % of the tensor pipe's.  8 sequences of up to 32K rows, 5
+// new tokens, 64 query and 8 K/V heads (40 rows): 102 to 104 us for 311 MB, 3.0 TB/s, where the kernel of
+// products in registers took 211 us; 8 of 32K: 136 us for 24 rows, 151 for 40, 168 for 64 (a floor of 82; for
+// few rows the two warps that widen V are the bound, 2400 cycles a chunk).  For 40 rows the four warpgroups
+// have 8, 8, 8 and 16 rows (TMEM is read in blocks of eight), and the chunk waits for the last: an even split
+// would save it a quarter of its rows' instructions.
 #pragma once
 
 #include "fa_decode_fp8.cuh"
@@ -95,8 +96,8 @@ __device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0
 // V codes of a chunk (128-byte rows from `slot`) that some query of the unit does not see: rows past the
 // end may hold anything and become zeros; a NaN code would reach every query, so it goes to the queries
 // that see its row by hand (sm_nan) and becomes a zero.  Two rows a thread, whole warps.
-__device__ __forceinline__ void dec8_tc_clean_v(uint8_t* slot, int first, int j0, int len, int rows, const int* sm_limit,
-                                             uint32_t* sm_nan) {
+__device__ __forceinline__ void dec8_tc_clean_v(uint8_t* slot, int first, int j0, int len, int rows,
+                                                const int* sm_limit, uint32_t* sm_nan) {
   constexpr int D = Dec8TcCfg::D;
 #pragma unroll 1
   for (int row = first; row < kDec8Keys; row += 64) {

@@ -414,7 +414,8 @@ __global__ void __launch_bounds__(kCopyThreads + 32, 2)
     bytes[slot] = (unsigned)min(page - piece * kBulkBytes, (unsigned long long)kBulkBytes);
     to[slot] = base + (unsigned long long)load_in(dst + k) * page;
     mbar_arrive_expect_tx(full + slot, bytes[slot]);
-    bulk_load(smem_raw + slot * kBulkBytes, base + (unsigned long long)load_in(src + k) * page, bytes[slot], full + slot);
+    bulk_load(smem_raw + slot * kBulkBytes, base + (unsigned long long)load_in(src + k) * page, bytes[slot],
+              full + slot);
   };
   // the store of a piece follows its load; the load of the piece five further on follows the store
   // of the one before, once that has read its slot

@@ -321,9 +321,10 @@ FA_EXPORT fa_status fa_cache_append_fp8(const void* k, const void* v, const int3
  * cache rows j <= seqlens[b] - Nq + i (every row for Nq = 1); a query that sees no row gets o = 0
  * and lse = -inf.  Cache, scales, block_table and seqlens as in fa_cache_append_fp8
  * (scales 0 .. 2^120 or NaN; the append writes no larger ones for finite rows); lengths below 0
- * count as 0, larger ones than max_pages_per_seq * page_size as that.  Rows past a sequence's end may hold anything; a NaN code or scale makes NaN of what
- * attends to it, and of nothing else.  An entry of the table outside [0, num_pages) is
- * read as page 0 and recorded (FA_ERR_INVALID_ARG from fa_last_device_error).
+ * count as 0, larger ones than max_pages_per_seq * page_size as that.  Rows past a sequence's end may
+ * hold anything; a NaN code or scale makes NaN of what attends to it, and of nothing else.  An entry of
+ * the table outside [0, num_pages) is read as page 0 and recorded (FA_ERR_INVALID_ARG from
+ * fa_last_device_error).
  * The stored values are exact in the products and all sums are fp32.  P times the V scale is rounded
  * to fp16 relative to a value within 2^6 of its largest.  For more than 16 query rows of a K/V head
  * (Nq * Hq / Hkv) and d = 128, q is the sum of two e4m3 terms (8 bits, like bf16; 2^-17 of a row's
@@ -331,9 +332,10 @@ FA_EXPORT fa_status fa_cache_append_fp8(const void* k, const void* v, const int3
  * bf16.
  * Hq a multiple of Hkv; d 64 or 128; sizes as in fa_cache_append_fp8, and B * Hkv *
  * (max_pages_per_seq * page_size + 1408) * (Nq * (Hq / Hkv) / 64, rounded up) < 2^38 suffices for what
- * is counted in 32 bits (FA_ERR_UNSUPPORTED beyond).  workspace: at least fa_decode_paged_fp8_workspace_size(...) bytes (with the call's
- * device current), 16-byte aligned, not initialised; calls that share one must not overlap on the
- * GPU.  o and lse must not overlap the inputs. */
+ * is counted in 32 bits (FA_ERR_UNSUPPORTED beyond).  workspace: at least
+ * fa_decode_paged_fp8_workspace_size(...) bytes (with the call's device current), 16-byte aligned, not
+ * initialised; calls that share one must not overlap on the GPU.  o and lse must not overlap the
+ * inputs. */
 FA_EXPORT fa_status fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
                                         const float* k_scale, const float* v_scale, const int32_t* block_table,
                                         const int32_t* seqlens, void* o, float* lse, int B, int Nq, int Hq, int Hkv,
@@ -393,7 +395,8 @@ FA_EXPORT size_t fa_pages_workspace_size(int num_pages, int B_out);
  * device-side timeout since the previous call, else FA_ERR_CUDA if a kernel found its shared
  * memory carve-out too small, else FA_ERR_INVALID_ARG if a kernel recorded an invalid
  * device-side input (a block-table entry out of range, a cu_seqlens that fa_fwd or
- * fa_bwd_varlen cannot use, what fa_cache_append_fp8 and the fa_pages calls name); FA_ERR_CUDA if the stream reports an error; else FA_OK.
+ * fa_bwd_varlen cannot use, what fa_cache_append_fp8 and the fa_pages calls name); FA_ERR_CUDA if the
+ * stream reports an error; else FA_OK.
  * The record is shared by all kernels of the library on the device (all streams); a timeout
  * stops only the kernel whose wait ran out, and later launches run normally whether or not
  * the record has been taken. */
